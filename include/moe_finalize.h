@@ -20,6 +20,15 @@
  *     name: the Beam finalize, then a residual add and the next RMSNorm, in one
  *     kernel (the residual step is a reading of the pages; see its comment).
  *
+ * and the operations that make what they read, and train it:
+ *
+ *   moe_expert_permutation -- the index map from routed expert ids, and
+ *     moe_permuted_row_sum, the gradient of the gather that it defines.
+ *   moe_grouped_gemm, moe_grouped_gemm_dgrad, moe_grouped_gemm_wgrad -- matrix
+ *     products over each expert's rows: forward and both gradients.
+ *   moe_grouped_gemv_int4 -- the product with 4-bit weights, for few rows per
+ *     expert.
+ *
  * Conventions for every entry point:
  *   - Pointers marked "device" are CUDA device (or managed) memory of the
  *     current device; the caller owns all of them.  The library allocates no
@@ -240,6 +249,175 @@ mf_status beam_moe_finalize_norm_residual_norm(
     const void *post_weight, float post_eps, int has_post_norm, const void *next_weight,
     float next_eps, int has_next_norm, float scale_x, float scale_residual, void *hidden_out,
     void *normalized_out, mf_stream_t stream);
+
+/*
+ * moe_expert_permutation -- sorts the routed slots by expert (stable: slots of
+ * one expert keep their order), which gives the index map that
+ * moe_finalize_rmsnorm reads and the row order of the grouped products.
+ *
+ *   expert_ids       device, int32 [num_tokens, top_k] contiguous, 16-byte
+ *                    aligned: expert ids, or with nonzero `packed` routing words
+ *                    (expert_id << 16) | weight bits (MF_DTYPE_PACKED_TOPK; the
+ *                    id is the high half, unsigned).  A slot whose id is outside
+ *                    [0, num_experts) has no expert: it gets no row.
+ *   expert_offsets   device, int32 [num_experts + 1], 4-byte aligned, written:
+ *                    the rows of expert e are expert_offsets[e] up to
+ *                    expert_offsets[e + 1].
+ *   expanded_idx_to_permuted_idx
+ *                    device, int32 [num_tokens, top_k], 16-byte aligned,
+ *                    written: the row of each slot, -1 for a slot without one.
+ *   permuted_row_to_token
+ *                    device, int32 [num_tokens * top_k], 16-byte aligned,
+ *                    written: the token of each row, -1 behind the last row.
+ *   num_experts, top_k   1 .. 1024 and 1 .. 32.
+ *
+ * Zero tokens: expert_offsets is written (zeros), the other pointers are not
+ * used.  Errors: MF_ERR_UNSUPPORTED, MF_ERR_SHAPE (num_tokens < 0 or
+ * num_tokens * top_k above 2^31 - 1025), MF_ERR_NULL, MF_ERR_ALIGN, MF_ERR_CUDA.
+ */
+mf_status moe_expert_permutation(const int32_t *expert_ids, int packed, int64_t num_tokens,
+                                 int32_t top_k, int32_t num_experts, int32_t *expert_offsets,
+                                 int32_t *expanded_idx_to_permuted_idx,
+                                 int32_t *permuted_row_to_token, mf_stream_t stream);
+
+/*
+ * moe_permuted_row_sum -- output[t, :] = sum over j of permuted[idx[t, j], :],
+ * FP32 in ascending j, rounded once: the gradient with respect to the tokens
+ * when the rows of a grouped product were gathered from them (the gradient of
+ * a row that went to several slots is the sum of theirs).
+ *
+ *   permuted         device, BF16 or FP32 [rows, row_stride], columns
+ *                    [0, hidden) used; row_stride >= hidden, a multiple of 8;
+ *                    16-byte aligned.  May be NULL only when rows == 0.
+ *   expanded_idx_to_permuted_idx
+ *                    device, int32 [num_tokens, top_k] contiguous, 4-byte
+ *                    aligned; a negative or out-of-range entry contributes zero
+ *                    and its row is not read.
+ *   output           device, BF16 or FP32 [num_tokens, hidden] contiguous,
+ *                    16-byte aligned.
+ *   hidden           a multiple of 8, 8 .. 2^20.   top_k  1 .. 32.
+ *
+ * Errors: MF_ERR_UNSUPPORTED, MF_ERR_SHAPE, MF_ERR_DTYPE, MF_ERR_NULL,
+ * MF_ERR_ALIGN, MF_ERR_CUDA.
+ */
+mf_status moe_permuted_row_sum(const void *permuted, mf_dtype permuted_dtype, int64_t rows,
+                               int64_t row_stride, const int32_t *expanded_idx_to_permuted_idx,
+                               void *output, mf_dtype output_dtype, int64_t num_tokens,
+                               int32_t hidden, int32_t top_k, mf_stream_t stream);
+
+/*
+ * moe_grouped_gemm -- for each expert e and each of its rows r
+ * (expert_offsets[e] <= r < expert_offsets[e + 1]):
+ *
+ *   output[r, :] = weight[e] . x[i(r), :]     i(r) = row_index[r], or r
+ *
+ * with FP32 accumulation, rounded once.  Rows outside every expert are left as
+ * they were.
+ *
+ *   x                device, BF16 [x_rows, x_stride], columns [0, k) used.
+ *   row_index        device, int32 [rows], or NULL (row r reads row r of x and
+ *                    x_rows >= rows).  An entry outside [0, x_rows) selects a
+ *                    row of zeros.  moe_expert_permutation's
+ *                    permuted_row_to_token gathers the tokens' rows this way,
+ *                    with no permuted copy of them.
+ *   weight           device, BF16 [num_experts, n, k], unit stride along k;
+ *                    weight_row_stride and weight_expert_stride in elements, an
+ *                    expert's matrix not overlapping the next.
+ *   expert_offsets   device, int32 [num_experts + 1], ascending, 4-byte aligned.
+ *                    They are read on the device and brought into [0, rows]:
+ *                    values that do not ascend give unspecified rows, and no
+ *                    access outside the buffers.
+ *   output           device, BF16 or FP32 [rows, output_stride].
+ *   n, k             multiples of 8, 8 .. 2^20.   num_experts  1 .. 1024.
+ *   All strides are multiples of 8 elements, at least the row's width; x,
+ *   weight and output 16-byte aligned.
+ *
+ * Errors: MF_ERR_UNSUPPORTED (n, k, num_experts), MF_ERR_SHAPE (negative sizes,
+ * strides, fewer x rows than rows without row_index, no x row at all, rows
+ * above 2^31 - 1025), MF_ERR_DTYPE, MF_ERR_NULL, MF_ERR_ALIGN, MF_ERR_CUDA.
+ * Zero rows: MF_OK, nothing launched.
+ */
+mf_status moe_grouped_gemm(const void *x, int64_t x_rows, int64_t x_stride,
+                           const int32_t *row_index, const void *weight, int64_t weight_row_stride,
+                           int64_t weight_expert_stride, const int32_t *expert_offsets,
+                           void *output, mf_dtype output_dtype, int64_t output_stride, int64_t rows,
+                           int32_t num_experts, int32_t n, int32_t k, mf_stream_t stream);
+
+/*
+ * moe_grouped_gemm_dgrad -- the gradient of moe_grouped_gemm with respect to
+ * its rows: grad_input[r, :] = transpose(weight[e]) . grad_output[r, :] for the
+ * rows of each expert; other rows are left as they were.  Where the forward
+ * pass gathered its rows, moe_permuted_row_sum adds them up per token.
+ *
+ *   grad_output      device, BF16 [rows, grad_output_stride], n columns used.
+ *   grad_input       device, BF16 or FP32 [rows, grad_input_stride], k columns
+ *                    written.
+ *   The rest, and the errors, as for moe_grouped_gemm.
+ */
+mf_status moe_grouped_gemm_dgrad(const void *grad_output, int64_t grad_output_stride,
+                                 const void *weight, int64_t weight_row_stride,
+                                 int64_t weight_expert_stride, const int32_t *expert_offsets,
+                                 void *grad_input, mf_dtype grad_input_dtype,
+                                 int64_t grad_input_stride, int64_t rows, int32_t num_experts,
+                                 int32_t n, int32_t k, mf_stream_t stream);
+
+/*
+ * moe_grouped_gemm_wgrad -- the gradient of moe_grouped_gemm with respect to
+ * its weights: for each expert
+ *
+ *   grad_weight[e] (+)= sum over its rows r of grad_output[r, :] x[i(r), :]^T
+ *
+ * added to what grad_weight holds when `accumulate` is nonzero, else written
+ * (zeros for an expert without rows).  Rows outside every expert enter nothing,
+ * whatever they hold.
+ *
+ *   grad_weight      device, BF16 or FP32 [num_experts, n, k] contiguous,
+ *                    16-byte aligned.
+ *   The rest, and the errors, as for moe_grouped_gemm.  Zero rows: the zeros
+ *   are written (nothing with `accumulate`).
+ */
+mf_status moe_grouped_gemm_wgrad(const void *grad_output, int64_t grad_output_stride, const void *x,
+                                 int64_t x_rows, int64_t x_stride, const int32_t *row_index,
+                                 const int32_t *expert_offsets, void *grad_weight,
+                                 mf_dtype grad_weight_dtype, int accumulate, int64_t rows,
+                                 int32_t num_experts, int32_t n, int32_t k, mf_stream_t stream);
+
+/*
+ * moe_grouped_gemv_int4 -- moe_grouped_gemm with 4-bit weights, for decode (few
+ * rows per expert; any number is allowed, and the weights are read again for
+ * every 32 of an expert's rows):
+ *
+ *   w[e, n, c]   = (q[e, n, c] - zero[e, n, c / group_size]) * scale[e, n, c / group_size]
+ *   output[r, n] = sum over c of w[e, n, c] * x[i(r), c]
+ *
+ * q - zero is exact, the products with x of a group are summed in FP32, times
+ * the scale in FP32; the result is rounded once.
+ *
+ *   weight           device, uint8 [num_experts, n, k / 2] contiguous, 16-byte
+ *                    aligned: column c is the low half of byte c / 2 for even c,
+ *                    the high half for odd c.
+ *   scales           device, BF16 or FP32 [num_experts, n, k / group_size]
+ *                    contiguous, 4-byte aligned.
+ *   zeros            device, uint8 [num_experts, n, k / group_size] contiguous,
+ *                    values 0 .. 15 (the low four bits are read), or NULL: 8
+ *                    everywhere.
+ *   group_size       32, 64 or 128; k is a multiple of it, at most 2^20.
+ *   n                1 .. 2^20.
+ *   expert_offsets   as for moe_grouped_gemm, or NULL when num_experts is 1:
+ *                    every row belongs to the one matrix.
+ *   output           device, BF16 or FP32 [rows, output_stride], output_stride
+ *                    >= n, 4-byte aligned.
+ *   x, row_index, rows as for moe_grouped_gemm.
+ *
+ * Errors: those of moe_grouped_gemm, and MF_ERR_INVALID (no expert_offsets
+ * with more than one expert).  Zero rows: MF_OK, nothing launched.
+ */
+mf_status moe_grouped_gemv_int4(const void *x, int64_t x_rows, int64_t x_stride,
+                                const int32_t *row_index, const uint8_t *weight,
+                                const void *scales, mf_dtype scales_dtype, const uint8_t *zeros,
+                                int32_t group_size, const int32_t *expert_offsets, void *output,
+                                mf_dtype output_dtype, int64_t output_stride, int64_t rows,
+                                int32_t num_experts, int32_t n, int32_t k, mf_stream_t stream);
 
 /* The kernel AUTO would run for moe_finalize_rmsnorm with these sizes on the
  * calling thread's current device (MF_VARIANT_AUTO if none would run: no

@@ -12,6 +12,9 @@ streams.  There is no CPU fallback: without the built library the calls raise.
   beam_moe_finalize.
 * ``beam_moe_finalize_norm_residual_norm`` follows the same page's function of
   that name on one GPU (its residual step is a reading; see the C header).
+* ``moe_expert_permutation``, ``moe_permuted_row_sum``, ``moe_grouped_gemm`` with
+  its gradients and ``moe_grouped_gemv_int4`` (``experts.py``) are the steps of an
+  expert layer before the finalize.
 """
 from __future__ import annotations
 
@@ -20,10 +23,15 @@ import torch
 
 from ._abi import (MF_DTYPE_BF16, MF_DTYPE_FP32, MF_DTYPE_PACKED_TOPK, VARIANT_NAMES, VARIANTS, MoeFinalizeError,
                    check, lib)
+from ._binding import _on_device, _req, _stream_ptr
+from .experts import (moe_expert_permutation, moe_grouped_gemm, moe_grouped_gemm_dgrad,
+                      moe_grouped_gemm_wgrad, moe_grouped_gemv_int4, moe_permuted_row_sum)
 
 __all__ = [
     "moe_finalize_rmsnorm", "tp_moe_finalize_rmsnorm", "beam_moe_finalize",
-    "beam_moe_finalize_norm_residual_norm", "MoeFinalizeError",
+    "beam_moe_finalize_norm_residual_norm", "moe_expert_permutation", "moe_permuted_row_sum",
+    "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad",
+    "moe_grouped_gemv_int4", "MoeFinalizeError",
     "device_status", "selftest_wait_timeout", "select_finalize_variant", "select_beam_variant",
     "finalize_kernel_name", "beam_kernel_name", "finalize_data_movement",
     "version", "set_programmatic_launch", "programmatic_launch", "HIDDEN", "TOP_K",
@@ -36,24 +44,6 @@ TOP_K = 8
 _BF16 = torch.bfloat16
 _WEIGHT_DTYPES = {torch.bfloat16: MF_DTYPE_BF16, torch.float32: MF_DTYPE_FP32,
                   torch.int32: MF_DTYPE_PACKED_TOPK}
-
-
-def _stream_ptr(stream, device) -> int:
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return s.cuda_stream
-
-
-def _on_device(dev: torch.device, fn, *args) -> int:
-    """Call fn with dev as the current CUDA device (switching only if needed)."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return fn(*args)
-    with torch.cuda.device(dev):
-        return fn(*args)
-
-
-def _req(cond: bool, msg: str) -> None:
-    if not cond:
-        raise ValueError(msg)
 
 
 def _variant(name: str) -> int:

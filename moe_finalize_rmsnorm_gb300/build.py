@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libmoe_finalize.so")
 
-SOURCES = ["api.cu", "tp_finalize.cu", "beam_finalize.cu"]
+SOURCES = ["api.cu", "experts_api.cu", "tp_finalize.cu", "beam_finalize.cu", "permute.cu",
+           "grouped_gemm.cu", "grouped_gemv.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
               "--expt-relaxed-constexpr", f"-I{INCLUDE}"]

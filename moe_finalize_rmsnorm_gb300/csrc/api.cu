@@ -7,6 +7,8 @@
 
 #include "moe_finalize.h"
 #include "common.cuh"
+#include "device_info.h"
+#include "experts.h"
 #include "kernels.h"
 
 namespace {
@@ -15,51 +17,16 @@ namespace {
 // bounded wait gives up.  One per device (module globals are per context).
 __device__ unsigned int g_status_word;
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s bound on every device wait
 constexpr int kMaxDevices = 64;
 
-struct DeviceInfo {
-    bool ready = false;
-    int num_sms = 0;
-    int smem_optin = 0;
-    int smem_per_sm = 0;
-    int bulk_per_sm = 0;       // resident CTAs per SM of the staged hidden-4096 kernel
-    int token_cta_per_sm = 0;  // and of the register kernel
-    unsigned *status = nullptr;  // device address of g_status_word
-};
+using mf::aligned;
+using mf::device_info;
+using mf::DeviceInfo;
+using mf::kWaitLimitNs;
 
 std::mutex g_mutex;
 DeviceInfo g_devices[kMaxDevices];
 std::atomic<int> g_programmatic{1};  // programmatic dependent launch, on by default
-
-// Per-device set-up on first use: SM count, opt-in shared memory, the status
-// word's device address and the kernels' attributes.
-mf_status device_info(const DeviceInfo **out) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MF_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(g_mutex);
-    DeviceInfo &d = g_devices[dev];
-    if (!d.ready) {
-        if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&d.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) !=
-                cudaSuccess ||
-            cudaDeviceGetAttribute(&d.smem_per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor,
-                                   dev) != cudaSuccess ||
-            cudaGetSymbolAddress(reinterpret_cast<void **>(&d.status), g_status_word) !=
-                cudaSuccess ||
-            mf::prepare_tp_kernels(d.smem_optin, d.smem_per_sm) != cudaSuccess ||
-            mf::prepare_beam_kernels(d.smem_per_sm) != cudaSuccess ||
-            mf::tp_blocks_per_sm(&d.bulk_per_sm, &d.token_cta_per_sm) != cudaSuccess) {
-            (void)cudaGetLastError();
-            return MF_ERR_CUDA;
-        }
-        d.ready = true;
-    }
-    *out = &d;
-    return MF_OK;
-}
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Finalize + RMSNorm, by token count (measured on GB300):
 //   <= kClusterMaxTokens  cluster kernel: a token's gather spread over 8 SMs
@@ -98,6 +65,40 @@ mf_variant pick_beam(int64_t live) { return live <= 0 ? MF_VARIANT_AUTO : MF_VAR
 mf_status from_launch(cudaError_t e) { return e == cudaSuccess ? MF_OK : MF_ERR_CUDA; }
 
 }  // namespace
+
+namespace mf {
+
+// Per-device set-up on first use: SM count, opt-in shared memory, the status
+// word's device address and the kernels' attributes.
+mf_status device_info(const DeviceInfo **out) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MF_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    DeviceInfo &d = g_devices[dev];
+    if (!d.ready) {
+        if (cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&d.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) !=
+                cudaSuccess ||
+            cudaDeviceGetAttribute(&d.smem_per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor,
+                                   dev) != cudaSuccess ||
+            cudaGetSymbolAddress(reinterpret_cast<void **>(&d.status), g_status_word) !=
+                cudaSuccess ||
+            mf::prepare_tp_kernels(d.smem_optin, d.smem_per_sm) != cudaSuccess ||
+            mf::prepare_beam_kernels(d.smem_per_sm) != cudaSuccess ||
+            mf::prepare_expert_kernels() != cudaSuccess ||
+            mf::tp_blocks_per_sm(&d.bulk_per_sm, &d.token_cta_per_sm) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return MF_ERR_CUDA;
+        }
+        d.ready = true;
+    }
+    *out = &d;
+    return MF_OK;
+}
+
+bool programmatic_launch() { return g_programmatic.load() != 0; }
+
+}  // namespace mf
 
 extern "C" {
 
