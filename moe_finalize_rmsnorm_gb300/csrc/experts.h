@@ -59,6 +59,7 @@ struct GroupedArgs {
     int64_t out_ld;          // forward, dgrad
     int accumulate;          // wgrad: add to what out holds
     int num_sms;
+    int num_pairs;           // pairs of SMs that run at once
     unsigned *status;
     uint64_t timeout_ns;
     bool programmatic;
@@ -86,8 +87,9 @@ struct GemvArgs {
     bool programmatic;
 };
 
-// Per-device one-time set-up (kernel attributes).
-cudaError_t prepare_expert_kernels();
+// Per-device one-time set-up (kernel attributes); `pairs`: clusters of two CTAs
+// of the grouped product that the device runs at once.
+cudaError_t prepare_expert_kernels(int *pairs);
 
 cudaError_t launch_expert_permutation(const PermuteArgs &a, cudaStream_t s);
 cudaError_t launch_permuted_row_sum(const RowSumArgs &a, cudaStream_t s);

@@ -8,8 +8,12 @@
 
 namespace mf {
 cudaError_t prepare_permute_kernels();
+cudaError_t prepare_grouped_gemm(int *pairs);
 
-cudaError_t prepare_expert_kernels() { return prepare_permute_kernels(); }
+cudaError_t prepare_expert_kernels(int *pairs) {
+    const cudaError_t e = prepare_permute_kernels();
+    return e == cudaSuccess ? prepare_grouped_gemm(pairs) : e;
+}
 }  // namespace mf
 
 namespace {
@@ -49,6 +53,7 @@ mf_status fill(mf::GroupedArgs &a) {
     mf_status st = mf::device_info(&d);
     if (st != MF_OK) return st;
     a.num_sms = d->num_sms;
+    a.num_pairs = d->num_pairs;
     a.status = d->status;
     a.timeout_ns = mf::kWaitLimitNs;
     a.programmatic = mf::programmatic_launch();
@@ -151,7 +156,7 @@ mf_status moe_grouped_gemm(const void *x, int64_t x_rows, int64_t x_stride,
     a.row_index = row_index;
     a.w = weight;
     a.w_ld = weight_row_stride;
-    a.w_expert = weight_expert_stride;
+    a.w_expert = num_experts > 1 ? weight_expert_stride : weight_row_stride;  // not used by one
     a.offsets = expert_offsets;
     a.rows = rows;
     a.num_experts = num_experts;
@@ -189,7 +194,7 @@ mf_status moe_grouped_gemm_dgrad(const void *grad_output, int64_t grad_output_st
     a.dy_ld = grad_output_stride;
     a.w = weight;
     a.w_ld = weight_row_stride;
-    a.w_expert = weight_expert_stride;
+    a.w_expert = num_experts > 1 ? weight_expert_stride : weight_row_stride;  // not used by one
     a.offsets = expert_offsets;
     a.rows = rows;
     a.num_experts = num_experts;

@@ -1,106 +1,538 @@
 // Matrix products grouped by expert: forward, and the gradients of the rows
-// and of the weights.
+// and of the weights, on the tensor cores.
+//
+// Every product is computed transposed: a tile's M is the output's columns and
+// its N the output's rows,
+//
+//   forward  D[n, r] = sum_k W[e][n, k] x[i(r), k]
+//   dgrad    D[k, r] = sum_n W[e][n, k] dy[r, n]
+//   wgrad    D[k, n] = sum_r x[i(r), k] dy[r, n]
+//
+// so the ragged dimension of the first two, an expert's rows, is the one whose
+// tile may be any multiple of 16 up to 256: an expert of 40 rows costs 48, not
+// 128 or 256.  An expert's rows are split evenly over its tiles.  In wgrad the
+// ragged dimension is the summed one; the step that holds an expert's last rows
+// reads them by number, and the rows behind them as zeros, so that a row of
+// another expert (or one that was never written) enters nothing.
+//
+// One persistent CTA (or pair of CTAs: one tile of 256 columns over two SMs,
+// each holding half of either operand) per SM walks the tiles: a warp that
+// issues the copies (TMA, 128-byte swizzle, 64 summed values a step), a warp
+// that issues the products into one of two accumulators in TMEM, four warps that
+// move the other accumulator out.
+#include <cuda.h>
+
 #include "experts.cuh"
 #include "experts.h"
 
 namespace mf {
 namespace {
 
-constexpr int kTile = 64, kStep = 16;
+constexpr int kThreads = 256;
+constexpr int kRowsMax = 256;               // N of a tile
+constexpr int kStep = 64;                   // summed values per stage: 128 bytes of BF16
+constexpr int kABytes = 128 * kStep * 2;    // A of one CTA and stage
+constexpr int kEpilogueBytes = 4 * 32 * 128;  // one 32 x 32 FP32 block per warp
+constexpr int kTmemColumns = 512;           // two accumulators of 256
 
-// One 64 x 64 tile of an expert's product per CTA, FP32 multiply-adds, 4 x 4
-// results per thread.  Result (i, j) = sum_c A(i, c) B(j, c):
-//   forward  i = row r, j = n, c = k:  A = x,    B = W[e]
-//   dgrad    i = row r, j = k, c = n:  A = dy,   B = W[e] transposed
-//   wgrad    i = n,     j = k, c = r:  A = dy^T, B = x^T
-template <int KIND>
-__global__ void __launch_bounds__(256) grouped_gemm_simple_kernel(GroupedArgs a) {
-    __shared__ float as[kStep][kTile + 1], bs[kStep][kTile + 1];
-    pdl_wait();
-    const int e = blockIdx.z;
-    int lo, hi;
-    expert_rows(a.offsets, e, static_cast<int>(a.rows), lo, hi);
-    const int m = hi - lo;
-    const int I = KIND == kWgrad ? a.n : m;
-    const int J = KIND == kForward ? a.n : a.k;
-    const int C = KIND == kForward ? a.k : KIND == kDgrad ? a.n : m;
-    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x);
-    const __nv_bfloat16 *dy = static_cast<const __nv_bfloat16 *>(a.dy);
-    const __nv_bfloat16 *w =
-        KIND == kWgrad ? nullptr : static_cast<const __nv_bfloat16 *>(a.w) + e * a.w_expert;
-    auto x_at = [&](int r, int c) -> float {
-        const int64_t row = a.row_index ? a.row_index[lo + r] : lo + r;
-        if (row < 0 || row >= a.x_rows) return 0.f;
-        return __bfloat162float(x[row * a.x_ld + c]);
-    };
-    auto dy_at = [&](int r, int c) { return __bfloat162float(dy[(lo + r) * a.dy_ld + c]); };
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const int j0 = blockIdx.x * kTile;
-    for (int i0 = blockIdx.y * kTile; i0 < I; i0 += gridDim.y * kTile) {
-        float acc[4][4] = {};
-        for (int c0 = 0; c0 < C; c0 += kStep) {
-            for (int t = threadIdx.x; t < kTile * kStep; t += 256) {
-                const int c = KIND == kWgrad ? t / kTile : t % kStep;
-                const int i = KIND == kWgrad ? t % kTile : t / kStep;
-                const bool in_c = c0 + c < C;
-                float v = 0.f, u = 0.f;
-                if (in_c && i0 + i < I)
-                    v = KIND == kForward ? x_at(i0 + i, c0 + c)
-                        : KIND == kDgrad ? dy_at(i0 + i, c0 + c)
-                                         : dy_at(c0 + c, i0 + i);
-                if (in_c && j0 + i < J)
-                    u = KIND == kForward ? __bfloat162float(w[(j0 + i) * a.w_ld + c0 + c])
-                        : KIND == kDgrad ? __bfloat162float(w[(c0 + c) * a.w_ld + j0 + i])
-                                         : x_at(c0 + c, j0 + i);
-                as[c][i] = v;
-                bs[c][i] = u;
-            }
-            __syncthreads();
-            for (int c = 0; c < kStep; ++c)
-                for (int p = 0; p < 4; ++p)
-                    for (int q = 0; q < 4; ++q)
-                        acc[p][q] = fmaf(as[c][ty + 16 * p], bs[c][tx + 16 * q], acc[p][q]);
-            __syncthreads();
+template <int CTAS>
+struct Shape {
+    static constexpr int kBBytes = kRowsMax / CTAS * kStep * 2;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = CTAS == 2 ? 6 : 4;  // 192 KB either way
+    static constexpr int kM = 128 * CTAS;
+};
+
+// Shared memory behind the stages and the epilogue's blocks.
+struct Control {
+    uint64_t full[6], empty[6], acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int scan[8];
+    int tiles[kMaxExperts + 1];  // row tiles of the experts before this one
+    int lo[kMaxExperts];
+    int rows[kMaxExperts];
+};
+
+constexpr int kSmemBytes = 1024 + 192 * 1024 + kEpilogueBytes + sizeof(Control);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+
+struct Maps {
+    CUtensorMap a, b;    // whole blocks
+    CUtensorMap a4, b4;  // rows by number
+};
+
+struct Tile {
+    int expert;
+    int m0;       // first output column
+    int row0;     // first output row (forward, dgrad: of the buffer; wgrad: n)
+    int nrows;    // output rows
+    int n;        // nrows rounded up to what the instruction takes
+    int steps;    // of 64 summed values
+    int summed;   // summed values
+    int sum0;     // wgrad: first row of the expert
+};
+
+__device__ __forceinline__ int round_up(int v, int to) { return (v + to - 1) / to * to; }
+
+template <int KIND, int CTAS>
+__device__ __forceinline__ Tile tile_of(const GroupedArgs &a, const Control &c, int64_t t) {
+    constexpr int M = Shape<CTAS>::kM;
+    const int columns = KIND == kForward ? a.n : a.k;
+    const int mt = (columns + M - 1) / M;
+    Tile r;
+    if (KIND == kWgrad) {
+        const int nt = (a.n + kRowsMax - 1) / kRowsMax;
+        r.expert = static_cast<int>(t / (int64_t{mt} * nt));
+        const int local = static_cast<int>(t - r.expert * (int64_t{mt} * nt));
+        r.m0 = local % mt * M;
+        r.row0 = local / mt * kRowsMax;
+        r.nrows = min(kRowsMax, a.n - r.row0);
+        r.summed = c.rows[r.expert];
+        r.sum0 = c.lo[r.expert];
+    } else {
+        const int u = static_cast<int>(t / mt);
+        int e = 0;  // the last expert whose tiles start at or before u
+        for (int step = 512; step > 0; step /= 2)
+            if (e + step < a.num_experts && c.tiles[e + step] <= u) e += step;
+        r.expert = e;
+        const int rows = c.rows[e];
+        const int rt = c.tiles[e + 1] - c.tiles[e];
+        const int local = static_cast<int>(t - c.tiles[e] * int64_t{mt});
+        const int each = round_up((rows + rt - 1) / rt, 16);
+        const int first = min(local % rt * each, rows);
+        r.m0 = local / rt * M;
+        r.row0 = c.lo[e] + first;
+        r.nrows = min(each, rows - first);
+        r.summed = KIND == kForward ? a.k : a.n;
+        r.sum0 = 0;
+    }
+    r.n = round_up(r.nrows, 16 * CTAS);
+    r.steps = (r.summed + kStep - 1) / kStep;
+    return r;
+}
+
+template <int KIND, int CTAS, bool GATHER>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_gemm_kernel(const __grid_constant__ Maps maps, const GroupedArgs a) {
+    using S = Shape<CTAS>;
+    constexpr bool PAIR = CTAS == 2;
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    uint8_t *aligned_raw = raw + (base - smem_u32(raw));
+    uint8_t *blocks = aligned_raw + S::kStages * S::kStageBytes;
+    Control &c = *reinterpret_cast<Control *>(blocks + kEpilogueBytes);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const uint32_t full = smem_u32(c.full), empty = smem_u32(c.empty);
+    const uint32_t acc_full = smem_u32(c.acc_full), acc_empty = smem_u32(c.acc_empty);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
         }
-        for (int p = 0; p < 4; ++p)
-            for (int q = 0; q < 4; ++q) {
-                const int i = i0 + ty + 16 * p, j = j0 + tx + 16 * q;
-                if (i >= I || j >= J) continue;
-                const int64_t at = KIND == kWgrad
-                                       ? (int64_t{e} * a.n + i) * a.k + j
-                                       : (int64_t{lo} + i) * a.out_ld + j;
-                float v = acc[p][q];
-                if (a.out_fp32) {
-                    float *o = static_cast<float *>(a.out) + at;
-                    *o = KIND == kWgrad && a.accumulate ? *o + v : v;
-                } else {
-                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at;
-                    if (KIND == kWgrad && a.accumulate) v += __bfloat162float(*o);
-                    *o = __float2bfloat16_rn(v);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_empty + 8 * i, 4 * CTAS);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 2) tmem_alloc<CTAS>(smem_u32(&c.tmem), kTmemColumns);
+
+    // The experts' rows and their tiles' numbers (an exclusive scan, each thread
+    // a run of experts).
+    pdl_wait();
+    const int per = (a.num_experts + kThreads - 1) / kThreads;
+    const int first = threadIdx.x * per, last = min(first + per, a.num_experts);
+    int sum = 0;
+    for (int e = first; e < last; ++e) {
+        int lo, hi;
+        expert_rows(a.offsets, e, static_cast<int>(a.rows), lo, hi);
+        c.lo[e] = lo;
+        c.rows[e] = hi - lo;
+        c.tiles[e] = sum;
+        sum += (hi - lo + kRowsMax - 1) / kRowsMax;
+    }
+    int before = sum;
+    for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+    }
+    if (lane == 31) c.scan[warp] = before;
+    before -= sum;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += c.scan[w];
+        total += c.scan[w];
+    }
+    for (int e = first; e < last; ++e) c.tiles[e] += before;
+    if (threadIdx.x == 0) c.tiles[a.num_experts] = total;
+    tcgen05_fence_before();
+    __syncthreads();
+    if (PAIR) cluster_barrier();
+    tcgen05_fence_after();
+    const uint32_t tmem = c.tmem;
+
+    const int columns = KIND == kForward ? a.n : a.k;
+    const int64_t mt = (columns + S::kM - 1) / S::kM;
+    const int64_t tiles = KIND == kWgrad
+                              ? int64_t{a.num_experts} * mt * ((a.n + kRowsMax - 1) / kRowsMax)
+                              : mt * total;
+    const int64_t first_tile = blockIdx.x / CTAS, tile_step = gridDim.x / CTAS;
+
+    if (warp == 0) {
+        // Copies.  Every lane waits for the stage; lane 0 issues the block copies,
+        // all lanes the copies of rows by number (four rows each).
+        const uint32_t full_at = PAIR ? map_to_cta(full, 0) : full;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t t = first_tile; t < tiles && ok; t += tile_step) {
+            const Tile d = tile_of<KIND, CTAS>(a, c, t);
+            const int half = d.n / CTAS;               // B rows of this CTA
+            const int b0 = d.row0 + rank * half;
+            const int m0 = d.m0 + rank * 128;
+            // the row of x that row i reads; -1 (zeros) where there is none
+            const int row_end = KIND == kWgrad ? d.sum0 + d.summed : d.row0 + d.nrows;
+            auto x_row = [&](int i) {
+                if (i >= row_end) return -1;
+                if (!GATHER) return i;
+                const int v = __ldg(a.row_index + i);
+                return v >= 0 && v < a.x_rows ? v : -1;
+            };
+            auto x_rows4 = [&](int i) {
+                return make_int4(x_row(i), x_row(i + 1), x_row(i + 2), x_row(i + 3));
+            };
+            int4 idx[2 / CTAS];                        // forward: this lane's rows of x
+            if (KIND == kForward && GATHER)
+#pragma unroll
+                for (int g = 0; g < 2 / CTAS; ++g) idx[g] = x_rows4(b0 + 4 * lane + 128 * g);
+            const uint32_t b_bytes = KIND == kWgrad ? round_up(half, 64) * kStep * 2
+                                     : GATHER       ? half * kStep * 2
+                                                    : round_up(half, 32) * kStep * 2;
+            for (int s = 0; s < d.steps; ++s, ++it) {
+                const uint32_t stage = it % S::kStages, phase = it / S::kStages & 1;
+                // all lanes give up together: the warp meets again below
+                ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * stage, phase ^ 1, a.timeout_ns));
+                if (!ok) break;
+                const uint32_t bar = full_at + 8 * stage;
+                const uint32_t sa = base + stage * S::kStageBytes, sb = sa + kABytes;
+                const int c0 = s * kStep;
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * stage, CTAS * (kABytes + b_bytes));
+                    if (KIND == kForward) tma_3d<PAIR>(sa, &maps.a, c0, m0, d.expert, bar);
+                    if (KIND == kDgrad)
+                        for (int i = 0; i < 2; ++i)
+                            tma_3d<PAIR>(sa + i * 8192, &maps.a, m0 + 64 * i, c0, d.expert, bar);
+                    if (KIND != kWgrad && !GATHER)
+                        for (int i = 0; i < half; i += 32)
+                            tma_2d<PAIR>(sb + i * kStep * 2, &maps.b, c0, b0 + i, bar);
+                }
+                __syncwarp();
+                if (KIND == kForward && GATHER)
+#pragma unroll
+                    for (int g = 0; g < 2 / CTAS; ++g)
+                        if (4 * lane + 128 * g < half)
+                            tma_gather4<PAIR>(sb + lane * 512 + g * 16384, &maps.b4, c0, idx[g], bar);
+                if (KIND == kWgrad) {
+                    const bool whole = c0 + kStep <= d.summed;
+                    const int r = d.sum0 + c0;
+                    if (whole && lane == 0) {
+                        if (!GATHER)
+                            for (int i = 0; i < 2; ++i)
+                                tma_2d<PAIR>(sa + i * 8192, &maps.a, m0 + 64 * i, r, bar);
+                        for (int i = 0; i < half; i += 64)
+                            tma_2d<PAIR>(sb + i / 64 * 8192, &maps.b, b0 + i, r, bar);
+                    }
+                    __syncwarp();
+                    // lanes 0-15 and 16-31: the two halves of a 128-column operand
+                    const int q = lane % 16, h = lane / 16;
+                    if (GATHER || !whole)
+                        tma_gather4<PAIR>(sa + h * 8192 + q * 512, &maps.a4, m0 + 64 * h,
+                                          x_rows4(r + 4 * q), bar);
+                    if (!whole) {
+                        auto row = [&](int i) { return i < row_end ? i : -1; };
+                        const int i = r + 4 * q;
+                        const int4 rows = make_int4(row(i), row(i + 1), row(i + 2), row(i + 3));
+                        for (int at = 64 * h; at < half; at += 128)
+                            tma_gather4<PAIR>(sb + at / 64 * 8192 + q * 512, &maps.b4, b0 + at, rows,
+                                              bar);
+                    }
                 }
             }
+        }
+        // The products have read every stage (and in a pair, the other CTA's
+        // completions have arrived here) before this CTA may leave.
+        if (ok)
+            for (uint32_t i = 0; i < S::kStages && i < it; ++i) {
+                const uint32_t p = it - 1 - i;
+                ok = ok && mbar_wait(empty + 8 * (p % S::kStages), p / S::kStages & 1,
+                                     a.timeout_ns);
+            }
+        if (!ok) {
+            if (lane == 0) atomicOr(a.status, kStatusWaitTimeout);
+            if (rank == 0)  // the copies in flight, before the memory is given back
+                for (uint32_t i = 0; i < S::kStages && i < it; ++i) {
+                    const uint32_t p = it - 1 - i;
+                    (void)mbar_wait(full + 8 * (p % S::kStages), p / S::kStages & 1, a.timeout_ns);
+                }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // Products.
+        constexpr bool A_MN = KIND != kForward, B_MN = KIND == kWgrad;
+        uint32_t it = 0, acc = 0;
+        bool ok = true;
+        for (int64_t t = first_tile; t < tiles && ok; t += tile_step) {
+            const Tile d = tile_of<KIND, CTAS>(a, c, t);
+            if (d.steps == 0) continue;
+            ok = mbar_wait(acc_empty + 8 * (acc & 1), (acc >> 1 & 1) ^ 1, a.timeout_ns);
+            if (!ok) break;
+            tcgen05_fence_after();
+            const uint32_t idesc = instr_desc(S::kM, d.n, A_MN, B_MN);
+            const uint32_t dst = tmem + (acc & 1) * kRowsMax;
+            for (int s = 0; s < d.steps; ++s, ++it) {
+                const uint32_t stage = it % S::kStages;
+                ok = mbar_wait(full + 8 * stage, it / S::kStages & 1, a.timeout_ns);
+                if (!ok) break;
+                tcgen05_fence_after();
+                const uint32_t sa = base + stage * S::kStageBytes, sb = sa + kABytes;
+                const int parts = min(kStep, d.summed - s * kStep);
+                for (int p = 0; 16 * p < parts; ++p) {
+                    // 16 summed values: 32 bytes along a K-major row, 16 rows of an MN-major block
+                    const uint64_t da = A_MN ? smem_desc(sa + p * 2048, 8192, 1024)
+                                             : smem_desc(sa + p * 32, 16, 1024);
+                    const uint64_t db = B_MN ? smem_desc(sb + p * 2048, 8192, 1024)
+                                             : smem_desc(sb + p * 32, 16, 1024);
+                    mma_bf16<CTAS>(dst, da, db, idesc, s + p > 0);
+                }
+                mma_commit<CTAS>(empty + 8 * stage);
+            }
+            if (ok) mma_commit<CTAS>(acc_full + 8 * (acc & 1));
+            ++acc;
+        }
+        if (!ok) atomicOr(a.status, kStatusWaitTimeout);
+    } else if (warp >= 4) {
+        // Results: lane = output column, register = output row.  Each warp turns
+        // its 32 x 32 block in shared memory and stores 64 (BF16) or 128 bytes of
+        // every row.
+        const int w = warp - 4;
+        uint8_t *block = blocks + w * 32 * 128;
+        const uint32_t done_at = PAIR ? map_to_cta(acc_empty, 0) : acc_empty;
+        uint32_t acc = 0;
+        bool ok = true;
+        for (int64_t t = first_tile; t < tiles; t += tile_step) {
+            const Tile d = tile_of<KIND, CTAS>(a, c, t);
+            const bool empty_sum = d.steps == 0;
+            if (empty_sum && (a.accumulate || d.nrows == 0)) continue;
+            if (!empty_sum) {
+                ok = __all_sync(0xffffffffu, mbar_wait(acc_full + 8 * (acc & 1), acc >> 1 & 1,
+                                                       a.timeout_ns));
+                if (!ok) break;
+                tcgen05_fence_after();
+            }
+            const int col0 = d.m0 + rank * 128 + w * 32;
+            const int64_t ld = KIND == kWgrad ? a.k : a.out_ld;
+            const int64_t out0 =
+                (KIND == kWgrad ? int64_t{d.expert} * a.n + d.row0 : int64_t{d.row0}) * ld + col0;
+            for (int r0 = 0; r0 < d.nrows; r0 += 32) {
+                uint32_t v[32];
+                if (empty_sum) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0;
+                } else {
+                    tmem_ld32(tmem + (acc & 1) * kRowsMax + r0 + (static_cast<uint32_t>(w * 32) << 16),
+                              v);
+                }
+                if (a.out_fp32) {
+                    float *f = reinterpret_cast<float *>(block);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) f[j * 32 + lane] = __uint_as_float(v[j]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = i * 4 + lane / 8, col = lane % 8 * 4;
+                        if (r0 + r < d.nrows && col0 + col < columns) {
+                            float4 x = *reinterpret_cast<float4 *>(f + r * 32 + col);
+                            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) +
+                                                                   out0 + (r0 + r) * ld + col);
+                            if (KIND == kWgrad && a.accumulate) {
+                                const float4 y = *o;
+                                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                            }
+                            *o = x;
+                        }
+                    }
+                } else {
+                    __nv_bfloat16 *h = reinterpret_cast<__nv_bfloat16 *>(block);
+                    const bool add = KIND == kWgrad && a.accumulate;
+                    if (!add) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            h[j * 32 + lane] = __float2bfloat16_rn(__uint_as_float(v[j]));
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = i * 8 + lane / 4, col = lane % 4 * 8;
+                            if (r0 + r < d.nrows && col0 + col < columns)
+                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                           out0 + (r0 + r) * ld + col) =
+                                    *reinterpret_cast<uint4 *>(h + r * 32 + col);
+                        }
+                    } else {
+                        // the sum with what the output holds is rounded once
+                        float *f = reinterpret_cast<float *>(block);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j * 32 + lane] = __uint_as_float(v[j]);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = i * 8 + lane / 4, col = lane % 4 * 8;
+                            if (r0 + r < d.nrows && col0 + col < columns) {
+                                uint4 *o = reinterpret_cast<uint4 *>(
+                                    static_cast<__nv_bfloat16 *>(a.out) + out0 + (r0 + r) * ld + col);
+                                float y[8];
+                                unpack8(*o, y);
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) y[u] += f[r * 32 + col + u];
+                                *o = pack8_rn(y);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            if (!empty_sum) {
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(done_at + 8 * (acc & 1));
+                ++acc;
+            }
+        }
+        if (!ok && lane == 0) atomicOr(a.status, kStatusWaitTimeout);
     }
+    __syncwarp();
+    tcgen05_fence_before();
+    __syncthreads();
+    if (PAIR) cluster_barrier();
+    if (warp == 2) {
+        tcgen05_fence_after();
+        tmem_dealloc<CTAS>(tmem, kTmemColumns);
+    }
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn g_encode = nullptr;  // the driver's encoder, found once (prepare)
+
+// Tensor map of BF16 values: `dims` sizes fastest first, `strides` (elements) of
+// the slower ones, boxes of 64 values by `rows`.
+bool encode(CUtensorMap *m, const void *p, int rank, const cuuint64_t (&dims)[3],
+            const int64_t (&strides)[2], int rows) {
+    cuuint64_t bytes[2] = {static_cast<cuuint64_t>(strides[0]) * 2,
+                           static_cast<cuuint64_t>(strides[1]) * 2};
+    cuuint32_t box[3] = {kStep, static_cast<cuuint32_t>(rows), 1};
+    cuuint32_t ones[3] = {1, 1, 1};
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(p), dims, bytes,
+                    box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int KIND, int CTAS, bool GATHER>
+cudaError_t launch(const Maps &maps, const GroupedArgs &a, int64_t tiles, cudaStream_t s) {
+    const unsigned ctas =
+        static_cast<unsigned>(CTAS * min(tiles, int64_t{CTAS == 2 ? a.num_pairs : a.num_sms}));
+    return launch_ex(grouped_gemm_kernel<KIND, CTAS, GATHER>, dim3(ctas), dim3(kThreads),
+                     kSmemBytes, s, CTAS, a.programmatic, maps, a);
+}
+
+template <int CTAS>
+cudaError_t launch_ctas(const GroupedArgs &a, cudaStream_t s) {
+    using u64 = cuuint64_t;
+    Maps m = {};
+    const u64 n = a.n, k = a.k, E = a.num_experts, xr = a.x_rows, rows = a.rows;
+    bool ok = true;
+    if (a.kind != kWgrad)
+        ok = encode(&m.a, a.w, 3, {k, n, E}, {a.w_ld, a.w_expert}, a.kind == kForward ? 128 : 64);
+    if (a.kind == kForward) {
+        ok = ok && encode(&m.b, a.x, 2, {k, xr, 1}, {a.x_ld, 0}, 32);
+        ok = ok && encode(&m.b4, a.x, 2, {k, xr, 1}, {a.x_ld, 0}, 1);
+    } else if (a.kind == kDgrad) {
+        ok = ok && encode(&m.b, a.dy, 2, {n, rows, 1}, {a.dy_ld, 0}, 32);
+    } else {
+        ok = ok && encode(&m.a, a.x, 2, {k, xr, 1}, {a.x_ld, 0}, 64);
+        ok = ok && encode(&m.a4, a.x, 2, {k, xr, 1}, {a.x_ld, 0}, 1);
+        ok = ok && encode(&m.b, a.dy, 2, {n, rows, 1}, {a.dy_ld, 0}, 64);
+        ok = ok && encode(&m.b4, a.dy, 2, {n, rows, 1}, {a.dy_ld, 0}, 1);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    const int columns = a.kind == kForward ? a.n : a.k;
+    const int64_t mt = (columns + Shape<CTAS>::kM - 1) / Shape<CTAS>::kM;
+    // at most this many tiles: the experts' sizes are known on the device only
+    const int64_t tiles =
+        a.kind == kWgrad
+            ? mt * a.num_experts * ((a.n + kRowsMax - 1) / kRowsMax)
+            : mt * (a.rows / kRowsMax + min(int64_t{a.num_experts}, a.rows));
+    switch (a.kind) {
+        case kForward:
+            return a.row_index ? launch<kForward, CTAS, true>(m, a, tiles, s)
+                               : launch<kForward, CTAS, false>(m, a, tiles, s);
+        case kDgrad: return launch<kDgrad, CTAS, false>(m, a, tiles, s);
+        default:
+            return a.row_index ? launch<kWgrad, CTAS, true>(m, a, tiles, s)
+                               : launch<kWgrad, CTAS, false>(m, a, tiles, s);
+    }
+}
+
+template <int CTAS>
+cudaError_t prepare_ctas() {
+    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(grouped_gemm_kernel<kForward, CTAS, false>, attr, kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(grouped_gemm_kernel<kForward, CTAS, true>, attr, kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(grouped_gemm_kernel<kDgrad, CTAS, false>, attr, kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(grouped_gemm_kernel<kWgrad, CTAS, false>, attr, kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(grouped_gemm_kernel<kWgrad, CTAS, true>, attr, kSmemBytes);
+    return e;
 }
 
 }  // namespace
 
-cudaError_t launch_grouped_gemm(const GroupedArgs &a, cudaStream_t s) {
-    const int J = a.kind == kForward ? a.n : a.k;
-    const int64_t I = a.kind == kWgrad ? a.n : a.rows;
-    const dim3 grid((J + kTile - 1) / kTile,
-                    static_cast<unsigned>(min((I + kTile - 1) / kTile, int64_t{1024})),
-                    a.num_experts);
-    switch (a.kind) {
-        case kForward:
-            return launch_ex(grouped_gemm_simple_kernel<kForward>, grid, dim3(256), 0, s, 1,
-                             a.programmatic, a);
-        case kDgrad:
-            return launch_ex(grouped_gemm_simple_kernel<kDgrad>, grid, dim3(256), 0, s, 1,
-                             a.programmatic, a);
-        default:
-            return launch_ex(grouped_gemm_simple_kernel<kWgrad>, grid, dim3(256), 0, s, 1,
-                             a.programmatic, a);
+cudaError_t prepare_grouped_gemm(int *pairs) {
+    if (!g_encode) {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                         cudaEnableDefault, &found);
+        if (e != cudaSuccess) return e;
+        if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+        g_encode = reinterpret_cast<EncodeFn>(fn);
     }
+    cudaError_t e = prepare_ctas<1>();
+    if (e == cudaSuccess) e = prepare_ctas<2>();
+    if (e != cudaSuccess) return e;
+    // pairs of SMs that run at once: a persistent grid of more would leave some
+    // pairs' tiles for a second wave
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(pairs, grouped_gemm_kernel<kForward, 2, false>, &cfg);
+}
+
+cudaError_t launch_grouped_gemm(const GroupedArgs &a, cudaStream_t s) {
+    return (a.kind == kForward ? a.n : a.k) <= 128 ? launch_ctas<1>(a, s) : launch_ctas<2>(a, s);
 }
 
 }  // namespace mf
