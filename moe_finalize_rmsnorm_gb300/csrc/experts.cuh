@@ -14,6 +14,17 @@ __device__ __forceinline__ void expert_rows(const int32_t *offsets, int e, int r
     hi = min(max(__ldg(offsets + e + 1), lo), rows);
 }
 
+// One lane of the warp, the same one every time, known to the compiler as one:
+// the asynchronous copies and products take their operands from uniform
+// registers, and code that several lanes might enter is issued lane by lane.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 // ---------------------------------------------------------------------------
 // tensor-map copies (TMA).  PAIR: the completion goes to a barrier of either
 // CTA of a pair (`bar` is a shared::cluster address).

@@ -17,9 +17,10 @@
 //
 // One persistent CTA (or pair of CTAs: one tile of 256 columns over two SMs,
 // each holding half of either operand) per SM walks the tiles: a warp that
-// issues the copies (TMA, 128-byte swizzle, 64 summed values a step), a warp
-// that issues the products into one of two accumulators in TMEM, four warps that
-// move the other accumulator out.
+// issues the copies of whole blocks (TMA, 128-byte swizzle, 64 summed values a
+// step) and two that issue the copies of rows by number, a warp that issues the
+// products into one of two accumulators in TMEM, four warps that move the other
+// accumulator out.
 #include <cuda.h>
 
 #include "experts.cuh"
@@ -45,6 +46,7 @@ struct Shape {
 
 // Shared memory behind the stages and the epilogue's blocks.
 struct Control {
+    int4 list[2][32];            // rows by number, four a copy
     uint64_t full[6], empty[6], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int scan[8];
@@ -116,6 +118,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ Maps maps, const GroupedArgs a) {
     using S = Shape<CTAS>;
     constexpr bool PAIR = CTAS == 2;
+    // copies of rows by number: gathered rows, and a sum's last rows
+    constexpr bool kByNumber = GATHER || KIND == kWgrad;
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     uint8_t *aligned_raw = raw + (base - smem_u32(raw));
@@ -182,8 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t first_tile = blockIdx.x / CTAS, tile_step = gridDim.x / CTAS;
 
     if (warp == 0) {
-        // Copies.  Every lane waits for the stage; lane 0 issues the block copies,
-        // all lanes the copies of rows by number (four rows each).
+        // Copies of whole blocks, and each stage's byte count.
         const uint32_t full_at = PAIR ? map_to_cta(full, 0) : full;
         uint32_t it = 0;
         bool ok = true;
@@ -192,21 +195,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int half = d.n / CTAS;               // B rows of this CTA
             const int b0 = d.row0 + rank * half;
             const int m0 = d.m0 + rank * 128;
-            // the row of x that row i reads; -1 (zeros) where there is none
-            const int row_end = KIND == kWgrad ? d.sum0 + d.summed : d.row0 + d.nrows;
-            auto x_row = [&](int i) {
-                if (i >= row_end) return -1;
-                if (!GATHER) return i;
-                const int v = __ldg(a.row_index + i);
-                return v >= 0 && v < a.x_rows ? v : -1;
-            };
-            auto x_rows4 = [&](int i) {
-                return make_int4(x_row(i), x_row(i + 1), x_row(i + 2), x_row(i + 3));
-            };
-            int4 idx[2 / CTAS];                        // forward: this lane's rows of x
-            if (KIND == kForward && GATHER)
-#pragma unroll
-                for (int g = 0; g < 2 / CTAS; ++g) idx[g] = x_rows4(b0 + 4 * lane + 128 * g);
             const uint32_t b_bytes = KIND == kWgrad ? round_up(half, 64) * kStep * 2
                                      : GATHER       ? half * kStep * 2
                                                     : round_up(half, 32) * kStep * 2;
@@ -218,7 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t bar = full_at + 8 * stage;
                 const uint32_t sa = base + stage * S::kStageBytes, sb = sa + kABytes;
                 const int c0 = s * kStep;
-                if (lane == 0) {
+                const bool whole = KIND != kWgrad || c0 + kStep <= d.summed;
+                if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(full + 8 * stage, CTAS * (kABytes + b_bytes));
                     if (KIND == kForward) tma_3d<PAIR>(sa, &maps.a, c0, m0, d.expert, bar);
                     if (KIND == kDgrad)
@@ -227,38 +216,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (KIND != kWgrad && !GATHER)
                         for (int i = 0; i < half; i += 32)
                             tma_2d<PAIR>(sb + i * kStep * 2, &maps.b, c0, b0 + i, bar);
-                }
-                __syncwarp();
-                if (KIND == kForward && GATHER)
-#pragma unroll
-                    for (int g = 0; g < 2 / CTAS; ++g)
-                        if (4 * lane + 128 * g < half)
-                            tma_gather4<PAIR>(sb + lane * 512 + g * 16384, &maps.b4, c0, idx[g], bar);
-                if (KIND == kWgrad) {
-                    const bool whole = c0 + kStep <= d.summed;
-                    const int r = d.sum0 + c0;
-                    if (whole && lane == 0) {
+                    if (KIND == kWgrad && whole) {
+                        const int r = d.sum0 + c0;
                         if (!GATHER)
                             for (int i = 0; i < 2; ++i)
                                 tma_2d<PAIR>(sa + i * 8192, &maps.a, m0 + 64 * i, r, bar);
                         for (int i = 0; i < half; i += 64)
                             tma_2d<PAIR>(sb + i / 64 * 8192, &maps.b, b0 + i, r, bar);
                     }
-                    __syncwarp();
-                    // lanes 0-15 and 16-31: the two halves of a 128-column operand
-                    const int q = lane % 16, h = lane / 16;
-                    if (GATHER || !whole)
-                        tma_gather4<PAIR>(sa + h * 8192 + q * 512, &maps.a4, m0 + 64 * h,
-                                          x_rows4(r + 4 * q), bar);
-                    if (!whole) {
-                        auto row = [&](int i) { return i < row_end ? i : -1; };
-                        const int i = r + 4 * q;
-                        const int4 rows = make_int4(row(i), row(i + 1), row(i + 2), row(i + 3));
-                        for (int at = 64 * h; at < half; at += 128)
-                            tma_gather4<PAIR>(sb + at / 64 * 8192 + q * 512, &maps.b4, b0 + at, rows,
-                                              bar);
-                    }
                 }
+                __syncwarp();
             }
         }
         // The products have read every stage (and in a pair, the other CTA's
@@ -277,7 +244,83 @@ __global__ void __launch_bounds__(kThreads, 1)
                     (void)mbar_wait(full + 8 * (p % S::kStages), p / S::kStages & 1, a.timeout_ns);
                 }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (kByNumber && (warp == 2 || warp == 3)) {
+        // Copies of rows by number, four a copy, half of them each warp.  The
+        // numbers go through shared memory, so that one elected lane reads them with
+        // uniform addresses (copies issued by diverged lanes serialise at some
+        // 80 cycles each).
+        const int g = warp - 2;
+        int4 *list = c.list[g];
+        const uint32_t full_at = PAIR ? map_to_cta(full, 0) : full;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t t = first_tile; t < tiles && ok; t += tile_step) {
+            const Tile d = tile_of<KIND, CTAS>(a, c, t);
+            const int half = d.n / CTAS;
+            const int b0 = d.row0 + rank * half;
+            const int m0 = d.m0 + rank * 128;
+            // the row of x that row i reads; -1 (it arrives as zeros) where there is none
+            const int row_end = KIND == kWgrad ? d.sum0 + d.summed : d.row0 + d.nrows;
+            auto x_row = [&](int i) {
+                if (i >= row_end) return -1;
+                if (!GATHER) return i;
+                const int v = __ldg(a.row_index + i);
+                return v >= 0 && v < a.x_rows ? v : -1;
+            };
+            int next = -1;
+            if (KIND == kForward) {
+                for (int q = lane; q < half / 8; q += 32) {
+                    const int i = b0 + 4 * (2 * q + g);
+                    list[q] = make_int4(x_row(i), x_row(i + 1), x_row(i + 2), x_row(i + 3));
+                }
+                __syncwarp();
+            } else {
+                next = x_row(d.sum0 + 32 * g + lane);
+            }
+            for (int s = 0; s < d.steps; ++s, ++it) {
+                const uint32_t stage = it % S::kStages, phase = it / S::kStages & 1;
+                const int c0 = s * kStep;
+                if (KIND == kWgrad) {
+                    reinterpret_cast<int *>(list)[lane] = next;
+                    next = x_row(d.sum0 + c0 + kStep + 32 * g + lane);
+                    __syncwarp();
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * stage, phase ^ 1, a.timeout_ns));
+                if (!ok) break;
+                const uint32_t bar = full_at + 8 * stage;
+                const uint32_t sa = base + stage * S::kStageBytes, sb = sa + kABytes;
+                if (elect_one()) {
+                    if (KIND == kForward) {
+#pragma unroll 4
+                        for (int q = 0; q < half / 8; ++q)
+                            tma_gather4<PAIR>(sb + (2 * q + g) * 512, &maps.b4, c0, list[q], bar);
+                    } else {
+                        const bool whole = c0 + kStep <= d.summed;
+                        if (GATHER || !whole) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    tma_gather4<PAIR>(sa + h * 8192 + (8 * g + q) * 512, &maps.a4,
+                                                      m0 + 64 * h, list[q], bar);
+                        }
+                        if (!whole) {
+                            auto row = [&](int i) { return i < row_end ? i : -1; };
+                            for (int q = 0; q < 8; ++q) {
+                                const int i = d.sum0 + c0 + 4 * (8 * g + q);
+                                const int4 rows = make_int4(row(i), row(i + 1), row(i + 2), row(i + 3));
+                                for (int at = 0; at < half; at += 64)
+                                    tma_gather4<PAIR>(sb + at / 64 * 8192 + (8 * g + q) * 512,
+                                                      &maps.b4, b0 + at, rows, bar);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && lane == 0) atomicOr(a.status, kStatusWaitTimeout);
+    } else if (warp == 1 && rank == 0) {
         // Products.
         constexpr bool A_MN = KIND != kForward, B_MN = KIND == kWgrad;
         uint32_t it = 0, acc = 0;
@@ -285,32 +328,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t t = first_tile; t < tiles && ok; t += tile_step) {
             const Tile d = tile_of<KIND, CTAS>(a, c, t);
             if (d.steps == 0) continue;
-            ok = mbar_wait(acc_empty + 8 * (acc & 1), (acc >> 1 & 1) ^ 1, a.timeout_ns);
+            ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + 8 * (acc & 1), (acc >> 1 & 1) ^ 1,
+                                                   a.timeout_ns));
             if (!ok) break;
             tcgen05_fence_after();
             const uint32_t idesc = instr_desc(S::kM, d.n, A_MN, B_MN);
             const uint32_t dst = tmem + (acc & 1) * kRowsMax;
             for (int s = 0; s < d.steps; ++s, ++it) {
                 const uint32_t stage = it % S::kStages;
-                ok = mbar_wait(full + 8 * stage, it / S::kStages & 1, a.timeout_ns);
+                ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * stage, it / S::kStages & 1,
+                                                       a.timeout_ns));
                 if (!ok) break;
                 tcgen05_fence_after();
                 const uint32_t sa = base + stage * S::kStageBytes, sb = sa + kABytes;
-                const int parts = min(kStep, d.summed - s * kStep);
-                for (int p = 0; 16 * p < parts; ++p) {
-                    // 16 summed values: 32 bytes along a K-major row, 16 rows of an MN-major block
-                    const uint64_t da = A_MN ? smem_desc(sa + p * 2048, 8192, 1024)
-                                             : smem_desc(sa + p * 32, 16, 1024);
-                    const uint64_t db = B_MN ? smem_desc(sb + p * 2048, 8192, 1024)
-                                             : smem_desc(sb + p * 32, 16, 1024);
-                    mma_bf16<CTAS>(dst, da, db, idesc, s + p > 0);
+                // 16 summed values: 32 bytes along a K-major row, 16 rows of an MN-major block
+                const uint64_t da = smem_desc(sa, A_MN ? 8192 : 16, 1024);
+                const uint64_t db = smem_desc(sb, B_MN ? 8192 : 16, 1024);
+                const int parts = (min(kStep, d.summed - s * kStep) + 15) / 16;
+                if (elect_one()) {
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        if (p < parts)
+                            mma_bf16<CTAS>(dst, da + p * ((A_MN ? 2048 : 32) >> 4),
+                                           db + p * ((B_MN ? 2048 : 32) >> 4), idesc, s + p > 0);
+                    mma_commit<CTAS>(empty + 8 * stage);
+                    if (s + 1 == d.steps) mma_commit<CTAS>(acc_full + 8 * (acc & 1));
                 }
-                mma_commit<CTAS>(empty + 8 * stage);
+                __syncwarp();
             }
-            if (ok) mma_commit<CTAS>(acc_full + 8 * (acc & 1));
             ++acc;
         }
-        if (!ok) atomicOr(a.status, kStatusWaitTimeout);
+        if (!ok && lane == 0) atomicOr(a.status, kStatusWaitTimeout);
     } else if (warp >= 4) {
         // Results: lane = output column, register = output row.  Each warp turns
         // its 32 x 32 block in shared memory and stores 64 (BF16) or 128 bytes of
