@@ -94,6 +94,23 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
                  : "memory");
 }
 
+// 16 bytes global -> shared, or 16 zero bytes (src is not read).
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool read) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(read ? 16u : 0u)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Until at most `N` of this thread's groups are in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // tensor cores (tcgen05) and their accumulator memory (TMEM)
 

@@ -17,10 +17,9 @@
 //
 // One persistent CTA (or pair of CTAs: one tile of 256 columns over two SMs,
 // each holding half of either operand) per SM walks the tiles: a warp that
-// issues the copies of whole blocks (TMA, 128-byte swizzle, 64 summed values a
-// step) and two that issue the copies of rows by number, a warp that issues the
-// products into one of two accumulators in TMEM, four warps that move the other
-// accumulator out.
+// issues the copies of blocks (TMA, 128-byte swizzle, 64 summed values a step), a
+// warp that issues the products into one of two accumulators in TMEM, four warps
+// that move the other accumulator out, and one more per stage for rows that are gathered.
 #include <cuda.h>
 
 #include "experts.cuh"
@@ -42,11 +41,11 @@ struct Shape {
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kStages = CTAS == 2 ? 6 : 4;  // 192 KB either way
     static constexpr int kM = 128 * CTAS;
+    static constexpr int kGatherThreads = kThreads + 32 * kStages;  // a warp per stage
 };
 
 // Shared memory behind the stages and the epilogue's blocks.
 struct Control {
-    int4 list[2][32];            // rows by number, four a copy
     uint64_t full[6], empty[6], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int scan[8];
@@ -114,12 +113,10 @@ __device__ __forceinline__ Tile tile_of(const GroupedArgs &a, const Control &c, 
 }
 
 template <int KIND, int CTAS, bool GATHER>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(GATHER ? Shape<CTAS>::kGatherThreads : kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ Maps maps, const GroupedArgs a) {
     using S = Shape<CTAS>;
     constexpr bool PAIR = CTAS == 2;
-    // copies of rows by number: gathered rows, and a sum's last rows
-    constexpr bool kByNumber = GATHER || KIND == kWgrad;
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     uint8_t *aligned_raw = raw + (base - smem_u32(raw));
@@ -132,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(full + 8 * i, 1);
+            mbar_init(full + 8 * i, GATHER ? 1 + CTAS : 1);
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -147,7 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a run of experts).
     pdl_wait();
     const int per = (a.num_experts + kThreads - 1) / kThreads;
-    const int first = threadIdx.x * per, last = min(first + per, a.num_experts);
+    const int first = min(static_cast<int>(threadIdx.x) * per, a.num_experts);
+    const int last = min(first + per, a.num_experts);
     int sum = 0;
     for (int e = first; e < last; ++e) {
         int lo, hi;
@@ -162,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int v = __shfl_up_sync(0xffffffffu, before, o);
         if (lane >= o) before += v;
     }
-    if (lane == 31) c.scan[warp] = before;
+    if (lane == 31 && warp < 8) c.scan[warp] = before;
     before -= sum;
     __syncthreads();
     int total = 0;
@@ -195,8 +193,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int half = d.n / CTAS;               // B rows of this CTA
             const int b0 = d.row0 + rank * half;
             const int m0 = d.m0 + rank * 128;
+            // gathered rows are not counted in bytes
+            const uint32_t a_bytes = KIND == kWgrad && GATHER ? 0 : kABytes;
             const uint32_t b_bytes = KIND == kWgrad ? round_up(half, 64) * kStep * 2
-                                     : GATHER       ? half * kStep * 2
+                                     : GATHER       ? 0
                                                     : round_up(half, 32) * kStep * 2;
             for (int s = 0; s < d.steps; ++s, ++it) {
                 const uint32_t stage = it % S::kStages, phase = it / S::kStages & 1;
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int c0 = s * kStep;
                 const bool whole = KIND != kWgrad || c0 + kStep <= d.summed;
                 if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * stage, CTAS * (kABytes + b_bytes));
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * stage, CTAS * (a_bytes + b_bytes));
                     if (KIND == kForward) tma_3d<PAIR>(sa, &maps.a, c0, m0, d.expert, bar);
                     if (KIND == kDgrad)
                         for (int i = 0; i < 2; ++i)
@@ -244,13 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     (void)mbar_wait(full + 8 * (p % S::kStages), p / S::kStages & 1, a.timeout_ns);
                 }
         }
-    } else if (kByNumber && (warp == 2 || warp == 3)) {
-        // Copies of rows by number, four a copy, half of them each warp.  The
-        // numbers go through shared memory, so that one elected lane reads them with
-        // uniform addresses (copies issued by diverged lanes serialise at some
-        // 80 cycles each).
-        const int g = warp - 2;
-        int4 *list = c.list[g];
+    } else if (KIND == kWgrad && warp == 2) {
+        // Copies of rows by number (four a copy), only for the step that holds a
+        // sum's last rows: -1 behind them arrives as zeros.
         const uint32_t full_at = PAIR ? map_to_cta(full, 0) : full;
         uint32_t it = 0;
         bool ok = true;
@@ -259,65 +255,96 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int half = d.n / CTAS;
             const int b0 = d.row0 + rank * half;
             const int m0 = d.m0 + rank * 128;
-            // the row of x that row i reads; -1 (it arrives as zeros) where there is none
-            const int row_end = KIND == kWgrad ? d.sum0 + d.summed : d.row0 + d.nrows;
-            auto x_row = [&](int i) {
-                if (i >= row_end) return -1;
-                if (!GATHER) return i;
-                const int v = __ldg(a.row_index + i);
-                return v >= 0 && v < a.x_rows ? v : -1;
-            };
-            int next = -1;
-            if (KIND == kForward) {
-                for (int q = lane; q < half / 8; q += 32) {
-                    const int i = b0 + 4 * (2 * q + g);
-                    list[q] = make_int4(x_row(i), x_row(i + 1), x_row(i + 2), x_row(i + 3));
-                }
-                __syncwarp();
-            } else {
-                next = x_row(d.sum0 + 32 * g + lane);
-            }
+            const int row_end = d.sum0 + d.summed;
             for (int s = 0; s < d.steps; ++s, ++it) {
                 const uint32_t stage = it % S::kStages, phase = it / S::kStages & 1;
                 const int c0 = s * kStep;
-                if (KIND == kWgrad) {
-                    reinterpret_cast<int *>(list)[lane] = next;
-                    next = x_row(d.sum0 + c0 + kStep + 32 * g + lane);
-                    __syncwarp();
-                }
                 ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * stage, phase ^ 1, a.timeout_ns));
                 if (!ok) break;
                 const uint32_t bar = full_at + 8 * stage;
                 const uint32_t sa = base + stage * S::kStageBytes, sb = sa + kABytes;
-                if (elect_one()) {
-                    if (KIND == kForward) {
-#pragma unroll 4
-                        for (int q = 0; q < half / 8; ++q)
-                            tma_gather4<PAIR>(sb + (2 * q + g) * 512, &maps.b4, c0, list[q], bar);
-                    } else {
-                        const bool whole = c0 + kStep <= d.summed;
-                        if (GATHER || !whole) {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    tma_gather4<PAIR>(sa + h * 8192 + (8 * g + q) * 512, &maps.a4,
-                                                      m0 + 64 * h, list[q], bar);
-                        }
-                        if (!whole) {
-                            auto row = [&](int i) { return i < row_end ? i : -1; };
-                            for (int q = 0; q < 8; ++q) {
-                                const int i = d.sum0 + c0 + 4 * (8 * g + q);
-                                const int4 rows = make_int4(row(i), row(i + 1), row(i + 2), row(i + 3));
-                                for (int at = 0; at < half; at += 64)
-                                    tma_gather4<PAIR>(sb + at / 64 * 8192 + (8 * g + q) * 512,
-                                                      &maps.b4, b0 + at, rows, bar);
-                            }
-                        }
+                if (c0 + kStep > d.summed && elect_one()) {
+                    auto row = [&](int i) { return i < row_end ? i : -1; };
+                    for (int q = 0; q < kStep / 4; ++q) {
+                        const int i = d.sum0 + c0 + 4 * q;
+                        const int4 rows = make_int4(row(i), row(i + 1), row(i + 2), row(i + 3));
+                        if (!GATHER)
+                            for (int h = 0; h < 2; ++h)
+                                tma_gather4<PAIR>(sa + h * 8192 + q * 512, &maps.a4, m0 + 64 * h,
+                                                  rows, bar);
+                        for (int at = 0; at < half; at += 64)
+                            tma_gather4<PAIR>(sb + at / 64 * 8192 + q * 512, &maps.b4, b0 + at, rows,
+                                              bar);
                     }
                 }
                 __syncwarp();
             }
+        }
+        if (!ok && lane == 0) atomicOr(a.status, kStatusWaitTimeout);
+    } else if (GATHER && warp >= 8) {
+        // Rows of x chosen by row_index: 16-byte cp.async copies, eight lanes to a
+        // row's 128 bytes, into the swizzled layout that the block copies give.  One
+        // warp per stage: it issues a step's copies, waits for them, makes them
+        // visible to the tensor cores and hands the stage over, while the other
+        // warps' copies are in flight.  (Tensor-map row gathers took some 40 cycles
+        // per four rows, 1.4x the time of the whole step; and one group of warps
+        // with several steps in flight waits for all of them at the proxy fence.)
+        constexpr int kLists = KIND == kWgrad ? 2 : 8 / CTAS;  // of 32 rows
+        const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x);
+        const uint32_t stage = warp - 8;
+        const uint32_t full_at = (PAIR ? map_to_cta(full, 0) : full) + 8 * stage;
+        const int chunk = lane % 8, r0 = lane / 8;  // rows r0 + 4 j
+        const uint32_t swizzle[2] = {static_cast<uint32_t>((chunk ^ r0) << 4),
+                                     static_cast<uint32_t>((chunk ^ (r0 + 4)) << 4)};
+        const uint32_t dst = base + stage * S::kStageBytes + (KIND == kWgrad ? 0 : kABytes) + r0 * 128;
+        uint32_t it = stage;   // this warp's next step, counted over the tiles
+        uint32_t done = 0;     // steps of the tiles before
+        bool ok = true;
+        for (int64_t t = first_tile; t < tiles && ok; t += tile_step) {
+            const Tile d = tile_of<KIND, CTAS>(a, c, t);
+            const int half = d.n / CTAS;
+            const int row_end = KIND == kWgrad ? d.sum0 + d.summed : d.row0 + d.nrows;
+            const int m0 = d.m0 + rank * 128;
+            auto x_row = [&](int i) {
+                const int v = i < row_end ? __ldg(a.row_index + i) : -1;
+                return v >= 0 && v < a.x_rows ? v : -1;
+            };
+            int rows[kLists];
+            if (KIND != kWgrad && it < done + d.steps)
+#pragma unroll
+                for (int i = 0; i < kLists; ++i)
+                    rows[i] = x_row(d.row0 + rank * half + 32 * i + lane);
+            for (; it < done + d.steps; it += S::kStages) {
+                const int c0 = static_cast<int>(it - done) * kStep;
+                if (KIND == kWgrad)
+#pragma unroll
+                    for (int i = 0; i < kLists; ++i) rows[i] = x_row(d.sum0 + c0 + 32 * i + lane);
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(empty + 8 * stage, (it / S::kStages & 1) ^ 1, a.timeout_ns));
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < kLists; ++i) {
+                    if (KIND != kWgrad && 32 * i >= half) break;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int row = __shfl_sync(0xffffffffu, rows[i], r0 + 4 * j);
+                        const int64_t from = static_cast<int64_t>(row) * a.x_ld;
+#pragma unroll
+                        for (int h = 0; h < (KIND == kWgrad ? 2 : 1); ++h) {
+                            const int col = (KIND == kWgrad ? m0 + 64 * h : c0) + 8 * chunk;
+                            const bool in = row >= 0 && col < a.k;
+                            cp_async_16(dst + h * 8192 + i * 4096 + j * 512 + swizzle[j & 1],
+                                        in ? x + from + col : x, in);
+                        }
+                    }
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(full_at);
+            }
+            done += d.steps;
         }
         if (!ok && lane == 0) atomicOr(a.status, kStatusWaitTimeout);
     } else if (warp == 1 && rank == 0) {
@@ -359,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++acc;
         }
         if (!ok && lane == 0) atomicOr(a.status, kStatusWaitTimeout);
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
         // Results: lane = output column, register = output row.  Each warp turns
         // its 32 x 32 block in shared memory and stores 64 (BF16) or 128 bytes of
         // every row.
@@ -492,8 +519,8 @@ template <int KIND, int CTAS, bool GATHER>
 cudaError_t launch(const Maps &maps, const GroupedArgs &a, int64_t tiles, cudaStream_t s) {
     const unsigned ctas =
         static_cast<unsigned>(CTAS * min(tiles, int64_t{CTAS == 2 ? a.num_pairs : a.num_sms}));
-    return launch_ex(grouped_gemm_kernel<KIND, CTAS, GATHER>, dim3(ctas), dim3(kThreads),
-                     kSmemBytes, s, CTAS, a.programmatic, maps, a);
+    return launch_ex(grouped_gemm_kernel<KIND, CTAS, GATHER>, dim3(ctas),
+                     dim3(GATHER ? Shape<CTAS>::kGatherThreads : kThreads), kSmemBytes, s, CTAS, a.programmatic, maps, a);
 }
 
 template <int CTAS>
@@ -506,7 +533,6 @@ cudaError_t launch_ctas(const GroupedArgs &a, cudaStream_t s) {
         ok = encode(&m.a, a.w, 3, {k, n, E}, {a.w_ld, a.w_expert}, a.kind == kForward ? 128 : 64);
     if (a.kind == kForward) {
         ok = ok && encode(&m.b, a.x, 2, {k, xr, 1}, {a.x_ld, 0}, 32);
-        ok = ok && encode(&m.b4, a.x, 2, {k, xr, 1}, {a.x_ld, 0}, 1);
     } else if (a.kind == kDgrad) {
         ok = ok && encode(&m.b, a.dy, 2, {n, rows, 1}, {a.dy_ld, 0}, 32);
     } else {
