@@ -9,9 +9,11 @@
 namespace mf {
 cudaError_t prepare_permute_kernels();
 cudaError_t prepare_grouped_gemm(int *pairs);
+cudaError_t prepare_grouped_gemv();
 
 cudaError_t prepare_expert_kernels(int *pairs) {
-    const cudaError_t e = prepare_permute_kernels();
+    cudaError_t e = prepare_permute_kernels();
+    if (e == cudaSuccess) e = prepare_grouped_gemv();
     return e == cudaSuccess ? prepare_grouped_gemm(pairs) : e;
 }
 }  // namespace mf
@@ -270,7 +272,7 @@ mf_status moe_grouped_gemv_int4(const void *x, int64_t x_rows, int64_t x_stride,
     if (rows == 0) return MF_OK;
     if (!x || !weight || !scales || !output) return MF_ERR_NULL;
     if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(scales, 4) || !aligned(output, 4) ||
-        !aligned(expert_offsets, 4) || !aligned(row_index, 4))
+        !aligned(expert_offsets, 4) || !aligned(row_index, 4) || !aligned(zeros, 4))
         return MF_ERR_ALIGN;
     const mf::DeviceInfo *d = nullptr;
     mf_status st = mf::device_info(&d);

@@ -118,7 +118,7 @@ def test_gemv_int4_refusals(lib):
     for name in ("x", "w", "sc", "out"):
         assert gemv(lib, **{name: None}) == NULL, name
     assert gemv(lib, x=MIS) == ALIGN and gemv(lib, w=MIS) == ALIGN
-    for name in ("sc", "off", "out", "ri"):
+    for name in ("sc", "off", "out", "ri", "z"):
         assert gemv(lib, **{name: ODD}) == ALIGN, name
     assert gemv(lib, rows=0, x=None, w=None, sc=None, off=None, E=1, out=None) == OK
 
