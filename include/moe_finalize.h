@@ -399,7 +399,7 @@ mf_status moe_grouped_gemm_wgrad(const void *grad_output, int64_t grad_output_st
  *   scales           device, BF16 or FP32 [num_experts, n, k / group_size]
  *                    contiguous, 4-byte aligned.
  *   zeros            device, uint8 [num_experts, n, k / group_size] contiguous,
- *                    4-byte aligned, values 0 .. 15 (the low four bits are read),
+ *                    4-byte aligned, values 0 .. 15,
  *                    or NULL: 8 everywhere.
  *   group_size       32, 64 or 128; k is a multiple of it, at most 2^20.
  *   n                1 .. 2^20.

@@ -8,6 +8,8 @@
 // with so few rows the tensor cores only have to keep up with the conversion.
 // Each group's FP32 sum is scaled once.  Warps that share a column block split
 // the summed values between them and add up through shared memory, in warp order.
+#include <string.h>
+
 #include "experts.cuh"
 #include "experts.h"
 
@@ -86,9 +88,17 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 // Where a warp is in its sequence of (column block, stage) pairs.
 struct Cursor {
     int64_t item;
-    int stage;    // of the item's spans
+    int stage;  // of the item's spans
     int expert, n0, row0, rows;
-    int64_t line;  // expert * n + n0
+};
+
+// The same for the copies, with this lane's addresses.
+struct Copies {
+    int64_t item;
+    int stage;
+    const uint8_t *w;  // the 16 bytes that this lane copies of columns lane / 4 + 8 i
+    int64_t o;         // the lane's column: number of its first scale in the stage
+    unsigned columns;  // bit i: column lane / 4 + 8 i exists; bit 4: column `lane` does
 };
 
 template <int GROUP>
@@ -105,18 +115,38 @@ struct Gemv {
     float *sums;  // of the block's first warp
     const int barrier;
 
-    __device__ void locate(Cursor &p) const {
-        if (p.item >= items) return;
-        const int u = static_cast<int>(p.item / col_blocks);
+    // The pass over the weights that holds a column block, counted over the experts.
+    __device__ int pass_of(int64_t item) const { return static_cast<int>(item / col_blocks); }
+
+    __device__ int expert_of(int pass) const {
         int e = 0;
         for (int s = 512; s > 0; s /= 2)
-            if (e + s < a.num_experts && c.tiles[e + s] <= u) e += s;
-        p.expert = e;
+            if (e + s < a.num_experts && c.tiles[e + s] <= pass) e += s;
+        return e;
+    }
+
+    __device__ void locate(Cursor &p) const {
+        if (p.item >= items) return;
+        const int u = pass_of(p.item);
+        p.expert = expert_of(u);
         p.n0 = static_cast<int>(p.item - int64_t{u} * col_blocks) * kCols;
-        const int first_row = (u - c.tiles[e]) * kRowsPass;
-        p.row0 = c.lo[e] + first_row;
-        p.rows = min(kRowsPass, c.rows[e] - first_row);
-        p.line = int64_t{e} * a.n + p.n0;
+        const int first_row = (u - c.tiles[p.expert]) * kRowsPass;
+        p.row0 = c.lo[p.expert] + first_row;
+        p.rows = min(kRowsPass, c.rows[p.expert] - first_row);
+    }
+
+    __device__ void locate(Copies &p) const {
+        if (p.item >= items) return;
+        const int u = pass_of(p.item);
+        const int n0 = static_cast<int>(p.item - int64_t{u} * col_blocks) * kCols;
+        const int64_t line = int64_t{expert_of(u)} * a.n + n0;
+        p.w = a.w + (line + lane / 4) * (a.k / 2) + part * (kSpan / 2) + lane % 4 * 16;
+        p.o = (line + lane) * groups + part * kGroups;
+        p.columns = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n0 + lane / 4 + 8 * i < a.n) p.columns |= 1u << i;
+        if (n0 + lane < a.n) p.columns |= 16u;
     }
 
     __device__ void advance(Cursor &p) const {
@@ -128,47 +158,50 @@ struct Gemv {
         }
     }
 
-    // Start the copies of the cursor's stage (nothing behind the last item).
-    __device__ void issue(const Cursor &p, uint32_t slot) const {
+    // Start the copies of a stage (nothing behind the last item) and go on.
+    __device__ void issue(Copies &p, uint32_t slot) const {
         if (p.item < items) {
-            const int k0 = p.stage * kSpan;
             const uint32_t at = ring + slot * kStageBytes;
-            const int half_k = a.k / 2;
-            const uint8_t *w = a.w + p.line * half_k + k0 / 2;
+            const bool in_k = p.stage * kSpan + lane % 4 * 32 < a.k;
+            const uint32_t wd = at + lane / 4 * kPitch + lane % 4 * 16;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int row = lane / 4 + 8 * i, chunk = lane % 4;
-                const bool in = p.n0 + row < a.n && k0 + chunk * 32 < a.k;
-                cp_async_16(at + row * kPitch + chunk * 16,
-                            in ? w + int64_t{row} * half_k + chunk * 16 : a.w, in);
+                const bool in = in_k && (p.columns >> i & 1u);
+                cp_async_16(wd + 8 * i * kPitch, in ? p.w + int64_t{8 * i} * (a.k / 2) : a.w, in);
             }
-            if (p.n0 + lane < a.n) {
-                const int g0 = k0 / GROUP;
-                const int ng = min(kGroups, groups - g0);
-                const int64_t o = (p.line + lane) * groups + g0;
+            if (p.columns & 16u) {
+                const int ng = min(kGroups, groups - p.stage * kGroups);
                 const uint32_t sd = at + kScaleAt + lane * kScalePitch;
                 if (a.scale_fp32) {
-                    const float *s = static_cast<const float *>(a.scales) + o;
+                    const float *s = static_cast<const float *>(a.scales) + p.o;
 #pragma unroll
                     for (int i = 0; i < kGroups; ++i)
                         if (i < ng) cp_async_4(sd + 4 * i, s + i, 4);
                 } else {
                     // the aligned words that hold the scales
-                    const uint8_t *s = static_cast<const uint8_t *>(a.scales) + (o & ~int64_t{1}) * 2;
-                    const int bytes = (static_cast<int>(o & 1) + ng) * 2;
+                    const uint8_t *s =
+                        static_cast<const uint8_t *>(a.scales) + (p.o & ~int64_t{1}) * 2;
+                    const int bytes = (static_cast<int>(p.o & 1) + ng) * 2;
 #pragma unroll
                     for (int i = 0; i < kGroups / 2 + 1; ++i)
                         if (4 * i < bytes) cp_async_4(sd + 4 * i, s + 4 * i, min(4, bytes - 4 * i));
                 }
                 if (a.zeros) {
-                    const uint8_t *z = a.zeros + (o & ~int64_t{3});
-                    const int bytes = static_cast<int>(o & 3) + ng;
+                    const uint8_t *z = a.zeros + (p.o & ~int64_t{3});
+                    const int bytes = static_cast<int>(p.o & 3) + ng;
+                    const uint32_t zd = at + kZeroAt + lane * kZeroPitch;
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        if (4 * i < bytes)
-                            cp_async_4(at + kZeroAt + lane * kZeroPitch + 4 * i, z + 4 * i,
-                                       min(4, bytes - 4 * i));
+                        if (4 * i < bytes) cp_async_4(zd + 4 * i, z + 4 * i, min(4, bytes - 4 * i));
                 }
+            }
+            p.stage += share;
+            p.w += share * (kSpan / 2);
+            p.o += share * kGroups;
+            if (p.stage >= spans) {
+                p.stage = part;
+                p.item += step;
+                locate(p);
             }
         }
         cp_async_commit();
@@ -182,141 +215,151 @@ struct Gemv {
             static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
     }
 
-    // One column block with up to 8 NT rows.
-    template <int NT>
-    __device__ void item(Cursor &now, Cursor &ahead, uint32_t &slot) const {
+    // One column block with up to 8 NT HALVES rows; with two halves each stage is
+    // converted twice, for the rows' first and second half (registers).
+    template <int NT, int HALVES>
+    __device__ void item(Cursor &now, Copies &ahead, uint32_t &slot) const {
         const Cursor d = now;
-        const __nv_bfloat16 *x[NT];  // the rows this thread feeds (row g of every eight)
-        bool live[NT];
+        constexpr int kTiles = NT * HALVES;
+        const __nv_bfloat16 *x[kTiles];  // the rows this thread feeds (row g of every eight)
+        unsigned live = 0;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
+        for (int i = 0; i < kTiles; ++i) {
             const int r = 8 * i + g;
             int64_t row = -1;
             if (r < d.rows) row = a.row_index ? __ldg(a.row_index + d.row0 + r) : d.row0 + r;
-            live[i] = row >= 0 && row < a.x_rows;
-            x[i] = static_cast<const __nv_bfloat16 *>(a.x) + (live[i] ? row * a.x_ld : 0) + 8 * t;
+            const bool in = row >= 0 && row < a.x_rows;
+            live |= unsigned{in} << i;
+            x[i] = static_cast<const __nv_bfloat16 *>(a.x) + (in ? row * a.x_ld : 0) + 8 * t;
         }
-        float acc[2][NT][4] = {};
+        // The rows' values of one stage, loaded a stage (or half) before they are used:
+        // they come from the L2, some 800 cycles away.
+        uint4 xv[4][NT];
+        auto load_x = [&](int b, int half, int k) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                xv[b][i] = (live >> (half * NT + i) & 1u) && k < a.k
+                               ? __ldg(reinterpret_cast<const uint4 *>(x[half * NT + i] + k))
+                               : make_uint4(0, 0, 0, 0);
+        };
+#pragma unroll
+        for (int b = 0; b < 4; ++b) load_x(b, 0, now.stage * kSpan + 32 * b);
+        // number of the first scale of column g + 8 i, modulo 4: where the copied words hold it
+        const unsigned skip0 = static_cast<unsigned>((int64_t{d.expert} * a.n + d.n0 + g) * groups);
+        float acc[HALVES][2][NT][4] = {};
         while (now.item == d.item) {
             const int k0 = now.stage * kSpan;
             const int blocks = min(kSpan, a.k - k0) / 32;
-            uint4 xv[4][NT];
-            auto load_x = [&](int b) {
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    xv[b][i] = live[i] && b < blocks
-                                   ? __ldg(reinterpret_cast<const uint4 *>(x[i] + k0 + 32 * b))
-                                   : make_uint4(0, 0, 0, 0);
-            };
-#pragma unroll
-            for (int b = 0; b < 4; ++b) load_x(b);
             cp_async_wait<kStages - 2>();
             __syncwarp();
             issue(ahead, (slot + kStages - 1) % kStages);
-            advance(ahead);
             const uint32_t at = ring + slot * kStageBytes;
-            // element offsets of this stage's first scale, for its place in the copied words
-            const int64_t o0 = d.line * groups + k0 / GROUP;
-            float sum[2][NT][4];
-            uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
+            const uint32_t wd = at + g * kPitch + t * 4;
+            const unsigned skip = skip0 + now.stage * kGroups;
+            advance(now);
+            const int k_next = now.item == d.item ? now.stage * kSpan : a.k;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (b >= blocks) break;
-                constexpr int kPer = GROUP / 32;
-                if (b % kPer == 0) {
+            for (int half = 0; half < HALVES; ++half) {
+                float sum[2][NT][4];
+                uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                for (int b = 0; b < 4; ++b) {
+                    if (b >= blocks) break;
+                    constexpr int kPer = GROUP / 32;  // blocks of a group
+                    const int group = b / kPer;
+                    if (b % kPer == 0) {
 #pragma unroll
-                        for (int i = 0; i < NT; ++i)
+                        for (int m = 0; m < 2; ++m)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) sum[m][i][j] = 0.f;
-                    if (a.zeros) {
+                            for (int i = 0; i < NT; ++i)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = g + 8 * i;
-                            const uint32_t skip =
-                                static_cast<uint32_t>(o0 + int64_t{row} * groups) & 3u;
-                            const uint32_t z =
-                                lds_u8(at + kZeroAt + row * kZeroPitch + skip + b / kPer) & 15u;
-                            zero[i] = 0x43004300u | z | (z << 16);
+                                for (int j = 0; j < 4; ++j) sum[m][i][j] = 0.f;
+                        if (a.zeros) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t z = lds_u8(at + kZeroAt + (g + 8 * i) * kZeroPitch +
+                                                          ((skip + 8 * i * groups) & 3u) + group);
+                                zero[i] = __byte_perm(z, 0x43u, 0x4040);  // 128 + z, twice
+                            }
                         }
                     }
-                }
-                // 0x4300 | q is 128 + q in BF16; minus 128 + z is exact
-                uint32_t q[4][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t w = lds_32(at + (g + 8 * i) * kPitch + b * 16 + t * 4);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        q[i][j] = sub_bf16x2(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u, zero[i]);
-                }
-                // q[.][j] holds columns j and j + 4 of the thread's eight
-                const uint32_t a0[2][4] = {{q[0][0], q[1][0], q[0][1], q[1][1]},
-                                           {q[2][0], q[3][0], q[2][1], q[3][1]}};
-                const uint32_t a1[2][4] = {{q[0][2], q[1][2], q[0][3], q[1][3]},
-                                           {q[2][2], q[3][2], q[2][3], q[3][3]}};
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const uint4 v = xv[b][i];
-                    const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410);
-                    const uint32_t b1 = __byte_perm(v.x, v.z, 0x7632);
-                    const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410);
-                    const uint32_t b3 = __byte_perm(v.y, v.w, 0x7632);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        mma_16816(sum[m][i], a0[m], b0, b1);
-                        mma_16816(sum[m][i], a1[m], b2, b3);
-                    }
-                }
-                if (b % kPer == kPer - 1) {
-                    float s[4];
+                    // 0x4300 | q is 128 + q in BF16; minus 128 + z is exact
+                    uint32_t q[4][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int row = g + 8 * i;
-                        const uint32_t sa = at + kScaleAt + row * kScalePitch;
-                        if (a.scale_fp32) {
-                            s[i] = __uint_as_float(lds_32(sa + 4 * (b / kPer)));
-                        } else {
-                            const uint32_t skip =
-                                static_cast<uint32_t>(o0 + int64_t{row} * groups) & 1u;
-                            s[i] = __uint_as_float(lds_u16(sa + 2 * (skip + b / kPer)) << 16);
+                        const uint32_t w = lds_32(wd + 8 * i * kPitch + b * 16);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            q[i][j] =
+                                sub_bf16x2(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u, zero[i]);
+                    }
+                    // q[.][j] holds summed values j and j + 4 of the thread's eight
+                    const uint32_t a0[2][4] = {{q[0][0], q[1][0], q[0][1], q[1][1]},
+                                               {q[2][0], q[3][0], q[2][1], q[3][1]}};
+                    const uint32_t a1[2][4] = {{q[0][2], q[1][2], q[0][3], q[1][3]},
+                                               {q[2][2], q[3][2], q[2][3], q[3][3]}};
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const uint4 v = xv[b][i];
+                        const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410);
+                        const uint32_t b1 = __byte_perm(v.x, v.z, 0x7632);
+                        const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410);
+                        const uint32_t b3 = __byte_perm(v.y, v.w, 0x7632);
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            mma_16816(sum[m][i], a0[m], b0, b1);
+                            mma_16816(sum[m][i], a1[m], b2, b3);
                         }
                     }
+                    if (half + 1 < HALVES)
+                        load_x(b, half + 1, k0 + 32 * b);
+                    else
+                        load_x(b, 0, k_next + 32 * b);
+                    if (b % kPer == kPer - 1) {
+                        float s[4];
+                        const uint32_t sa = at + kScaleAt + g * kScalePitch;
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                        for (int i = 0; i < 4; ++i)
+                            if (a.scale_fp32)
+                                s[i] = __uint_as_float(lds_32(sa + 8 * i * kScalePitch + 4 * group));
+                            else
+                                s[i] = __uint_as_float(
+                                    lds_u16(sa + 8 * i * kScalePitch +
+                                            2 * (((skip + 8 * i * groups) & 1u) + group))
+                                    << 16);
 #pragma unroll
-                        for (int i = 0; i < NT; ++i)
+                        for (int m = 0; m < 2; ++m)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                acc[m][i][j] = fmaf(s[2 * m + j / 2], sum[m][i][j], acc[m][i][j]);
+                            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    acc[half][m][i][j] =
+                                        fmaf(s[2 * m + j / 2], sum[m][i][j], acc[half][m][i][j]);
+                    }
                 }
             }
             __syncwarp();
             slot = (slot + 1) % kStages;
-            advance(now);
         }
-        // acc[m][i][j]: n = 16 m + g + 8 (j / 2), row = 8 i + 2 t + j % 2
-        if (share == 1) {
+        // acc[h][m][i][j]: n = 16 m + g + 8 (j / 2), row = 8 (h NT + i) + 2 t + j % 2
+        float *mine = sums + part * (kCols * kRowsPass);
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int n = 16 * m + g + 8 * (j / 2), r = 8 * i + 2 * t + j % 2;
-                        if (r < d.rows && d.n0 + n < a.n) store(d.row0 + r, d.n0 + n, acc[m][i][j]);
+                        const int n = 16 * m + g + 8 * (j / 2);
+                        const int r = 8 * (h * NT + i) + 2 * t + j % 2;
+                        const float v = acc[h][m][i][j];
+                        if (share > 1)
+                            mine[r * kCols + n] = v;
+                        else if (r < d.rows && d.n0 + n < a.n)
+                            store(d.row0 + r, d.n0 + n, v);
                     }
-            return;
-        }
-        float *mine = sums + part * (kCols * kRowsPass);
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    mine[(8 * i + 2 * t + j % 2) * kCols + 16 * m + g + 8 * (j / 2)] = acc[m][i][j];
+        if (share == 1) return;
         meet();
         if (d.n0 + lane < a.n)
             for (int r = part; r < d.rows; r += share) {
@@ -391,21 +434,19 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
                         reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes) +
                             block * share * (kCols * kRowsPass),
                         1 + block};
-    Cursor now{k.first, k.part, 0, 0, 0, 0, 0};
+    Cursor now{k.first, k.part, 0, 0, 0, 0};
     k.locate(now);
-    Cursor ahead = now;
-    for (int s = 0; s < kStages - 1; ++s) {
-        k.issue(ahead, s);
-        k.advance(ahead);
-    }
+    Copies ahead{k.first, k.part, nullptr, 0, 0};
+    k.locate(ahead);
+    for (int s = 0; s < kStages - 1; ++s) k.issue(ahead, s);
     uint32_t slot = 0;
     while (now.item < k.items) {
         if (now.rows <= 8)
-            k.template item<1>(now, ahead, slot);
+            k.template item<1, 1>(now, ahead, slot);
         else if (now.rows <= 16)
-            k.template item<2>(now, ahead, slot);
+            k.template item<2, 1>(now, ahead, slot);
         else
-            k.template item<4>(now, ahead, slot);
+            k.template item<2, 2>(now, ahead, slot);
     }
     cp_async_wait<0>();
 }
