@@ -1,7 +1,7 @@
 // Products of few rows per expert with 4-bit weights and group scales.
 //
-// Bound by the weights' bytes: each is read once for every 32 rows of its
-// expert.  A warp takes 32 columns n and up to 32 rows.  It streams 128 summed
+// Bound by the weights' bytes: each is read once for every 16 rows of its
+// expert.  A warp takes 32 columns n and up to 16 rows.  It streams 128 summed
 // values of its 32 columns a stage (64 bytes a column) through its own ring in
 // shared memory (cp.async), turns the nibbles into BF16 integers q - z (exact),
 // and multiplies with the rows in mma.m16n8k16, n along M, the rows along N:
@@ -19,7 +19,7 @@ namespace {
 constexpr int kWarps = 12;
 constexpr int kGemvThreads = 32 * kWarps;
 constexpr int kCols = 32;      // n of a warp
-constexpr int kRowsPass = 32;  // rows of one pass over the weights
+constexpr int kRowsPass = 16;  // rows of one pass over the weights
 constexpr int kSpan = 128;     // summed values of a stage
 constexpr int kStages = 4;
 // A stage: 32 columns of 64 bytes, 80 apart (the quad reads of eight columns
@@ -49,28 +49,9 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src, int by
                  : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds_32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -92,13 +73,14 @@ struct Cursor {
     int expert, n0, row0, rows;
 };
 
-// The same for the copies, with this lane's addresses.
+// The same for the copies, with this lane's addresses.  Columns behind the last
+// one stand for the last one: their results are not stored.
 struct Copies {
     int64_t item;
     int stage;
-    const uint8_t *w;  // the 16 bytes that this lane copies of columns lane / 4 + 8 i
-    int64_t o;         // the lane's column: number of its first scale in the stage
-    unsigned columns;  // bit i: column lane / 4 + 8 i exists; bit 4: column `lane` does
+    const uint8_t *w;  // the lane's 16 bytes of the block's first column in this stage
+    int at[4];         // and from there to columns lane / 4 + 8 i
+    int64_t o;         // number of the first scale of column `lane` in this stage
 };
 
 template <int GROUP>
@@ -111,7 +93,9 @@ struct Gemv {
     const int share, part;  // warps of a column block, this one's number
     const int64_t first, step, items;
     const int col_blocks, spans, groups;
-    const uint32_t ring;
+    const uint8_t *ring;
+    const uint32_t ring_addr;
+    const int search;  // first step of the search for an expert
     float *sums;  // of the block's first warp
     const int barrier;
 
@@ -120,7 +104,7 @@ struct Gemv {
 
     __device__ int expert_of(int pass) const {
         int e = 0;
-        for (int s = 512; s > 0; s /= 2)
+        for (int s = search; s > 0; s /= 2)
             if (e + s < a.num_experts && c.tiles[e + s] <= pass) e += s;
         return e;
     }
@@ -140,13 +124,10 @@ struct Gemv {
         const int u = pass_of(p.item);
         const int n0 = static_cast<int>(p.item - int64_t{u} * col_blocks) * kCols;
         const int64_t line = int64_t{expert_of(u)} * a.n + n0;
-        p.w = a.w + (line + lane / 4) * (a.k / 2) + part * (kSpan / 2) + lane % 4 * 16;
-        p.o = (line + lane) * groups + part * kGroups;
-        p.columns = 0;
+        p.w = a.w + line * (a.k / 2) + part * (kSpan / 2) + lane % 4 * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n0 + lane / 4 + 8 * i < a.n) p.columns |= 1u << i;
-        if (n0 + lane < a.n) p.columns |= 16u;
+        for (int i = 0; i < 4; ++i) p.at[i] = min(lane / 4 + 8 * i, a.n - 1 - n0) * (a.k / 2);
+        p.o = (line + min(lane, a.n - 1 - n0)) * groups + part * kGroups;
     }
 
     __device__ void advance(Cursor &p) const {
@@ -161,39 +142,33 @@ struct Gemv {
     // Start the copies of a stage (nothing behind the last item) and go on.
     __device__ void issue(Copies &p, uint32_t slot) const {
         if (p.item < items) {
-            const uint32_t at = ring + slot * kStageBytes;
-            const bool in_k = p.stage * kSpan + lane % 4 * 32 < a.k;
+            const uint32_t at = ring_addr + slot * kStageBytes;
             const uint32_t wd = at + lane / 4 * kPitch + lane % 4 * 16;
+            if (p.stage * kSpan + lane % 4 * 32 < a.k)  // later blocks are not multiplied
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool in = in_k && (p.columns >> i & 1u);
-                cp_async_16(wd + 8 * i * kPitch, in ? p.w + int64_t{8 * i} * (a.k / 2) : a.w, in);
+                for (int i = 0; i < 4; ++i) cp_async_16(wd + 8 * i * kPitch, p.w + p.at[i], true);
+            const int ng = min(kGroups, groups - p.stage * kGroups);
+            const uint32_t sd = at + kScaleAt + lane * kScalePitch;
+            if (a.scale_fp32) {
+                const float *s = static_cast<const float *>(a.scales) + p.o;
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i)
+                    if (i < ng) cp_async_4(sd + 4 * i, s + i, 4);
+            } else {
+                // the aligned words that hold the scales
+                const uint8_t *s = static_cast<const uint8_t *>(a.scales) + (p.o & ~int64_t{1}) * 2;
+                const int bytes = (static_cast<int>(p.o & 1) + ng) * 2;
+#pragma unroll
+                for (int i = 0; i < kGroups / 2 + 1; ++i)
+                    if (4 * i < bytes) cp_async_4(sd + 4 * i, s + 4 * i, min(4, bytes - 4 * i));
             }
-            if (p.columns & 16u) {
-                const int ng = min(kGroups, groups - p.stage * kGroups);
-                const uint32_t sd = at + kScaleAt + lane * kScalePitch;
-                if (a.scale_fp32) {
-                    const float *s = static_cast<const float *>(a.scales) + p.o;
+            if (a.zeros) {
+                const uint8_t *z = a.zeros + (p.o & ~int64_t{3});
+                const int bytes = static_cast<int>(p.o & 3) + ng;
+                const uint32_t zd = at + kZeroAt + lane * kZeroPitch;
 #pragma unroll
-                    for (int i = 0; i < kGroups; ++i)
-                        if (i < ng) cp_async_4(sd + 4 * i, s + i, 4);
-                } else {
-                    // the aligned words that hold the scales
-                    const uint8_t *s =
-                        static_cast<const uint8_t *>(a.scales) + (p.o & ~int64_t{1}) * 2;
-                    const int bytes = (static_cast<int>(p.o & 1) + ng) * 2;
-#pragma unroll
-                    for (int i = 0; i < kGroups / 2 + 1; ++i)
-                        if (4 * i < bytes) cp_async_4(sd + 4 * i, s + 4 * i, min(4, bytes - 4 * i));
-                }
-                if (a.zeros) {
-                    const uint8_t *z = a.zeros + (p.o & ~int64_t{3});
-                    const int bytes = static_cast<int>(p.o & 3) + ng;
-                    const uint32_t zd = at + kZeroAt + lane * kZeroPitch;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (4 * i < bytes) cp_async_4(zd + 4 * i, z + 4 * i, min(4, bytes - 4 * i));
-                }
+                for (int i = 0; i < 2; ++i)
+                    if (4 * i < bytes) cp_async_4(zd + 4 * i, z + 4 * i, min(4, bytes - 4 * i));
             }
             p.stage += share;
             p.w += share * (kSpan / 2);
@@ -207,165 +182,175 @@ struct Gemv {
         cp_async_commit();
     }
 
-    __device__ void store(int r, int n, float v) const {
-        const int64_t at = r * a.out_ld + n;
+    // Row of x that row r of a pass reads, -1 if it is outside.
+    __device__ int x_row(const Cursor &d, int r) const {
+        const int row = a.row_index ? __ldg(a.row_index + d.row0 + r) : d.row0 + r;
+        return row < a.x_rows ? row : -1;
+    }
+
+    __device__ void store(const Cursor &d, int r, int n, float v) const {
+        if (a.row_index && x_row(d, r) < 0) v = 0.f;  // a row of zeros
+        const int64_t at = (int64_t{d.row0} + r) * a.out_ld + d.n0 + n;
         if (a.out_fp32)
             static_cast<float *>(a.out)[at] = v;
         else
             static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
     }
 
-    // One column block with up to 8 NT HALVES rows; with two halves each stage is
-    // converted twice, for the rows' first and second half (registers).
-    template <int NT, int HALVES>
+    // One column block with up to 8 NT rows.
+    template <int NT>
     __device__ void item(Cursor &now, Copies &ahead, uint32_t &slot) const {
         const Cursor d = now;
-        constexpr int kTiles = NT * HALVES;
-        const __nv_bfloat16 *x[kTiles];  // the rows this thread feeds (row g of every eight)
-        unsigned live = 0;
+        // The rows this thread feeds (row g of every eight).  Where there is none, any
+        // row will do: its results are not stored, or stored as zeros.
+        const __nv_bfloat16 *x[NT];
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-            const int r = 8 * i + g;
-            int64_t row = -1;
-            if (r < d.rows) row = a.row_index ? __ldg(a.row_index + d.row0 + r) : d.row0 + r;
-            const bool in = row >= 0 && row < a.x_rows;
-            live |= unsigned{in} << i;
-            x[i] = static_cast<const __nv_bfloat16 *>(a.x) + (in ? row * a.x_ld : 0) + 8 * t;
+        for (int i = 0; i < NT; ++i) {
+            const int row = x_row(d, min(8 * i + g, d.rows - 1));
+            x[i] = static_cast<const __nv_bfloat16 *>(a.x) + max(row, 0) * a.x_ld + 8 * t +
+                   now.stage * kSpan;
         }
-        // The rows' values of one stage, loaded a stage (or half) before they are used:
-        // they come from the L2, some 800 cycles away.
+        // The rows' values of one stage, loaded a stage before they are used: they come
+        // from the L2, some 800 cycles away.
         uint4 xv[4][NT];
-        auto load_x = [&](int b, int half, int k) {
+        auto load_x = [&](int b, int k) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-                xv[b][i] = (live >> (half * NT + i) & 1u) && k < a.k
-                               ? __ldg(reinterpret_cast<const uint4 *>(x[half * NT + i] + k))
-                               : make_uint4(0, 0, 0, 0);
+                xv[b][i] = __ldg(reinterpret_cast<const uint4 *>(x[i] + k + 32 * b));
         };
+        {
+            const int blocks = min(kSpan, a.k - now.stage * kSpan) / 32;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) load_x(b, 0, now.stage * kSpan + 32 * b);
-        // number of the first scale of column g + 8 i, modulo 4: where the copied words hold it
+            for (int b = 0; b < 4; ++b)
+                if (b < blocks) load_x(b, 0);
+        }
+        // Where the copied words hold the scale and zero of column g + 8 i: from its
+        // number modulo 4 on.  (A stage of four groups keeps it, of two moves it by
+        // two, of one by one.)
         const unsigned skip0 = static_cast<unsigned>((int64_t{d.expert} * a.n + d.n0 + g) * groups);
-        float acc[HALVES][2][NT][4] = {};
+        // columns behind the last stand for it
+        unsigned skips[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            skips[i] = skip0 + (min(g + 8 * i, a.n - 1 - d.n0) - g) * groups;
+        float acc[2][NT][4] = {};
         while (now.item == d.item) {
             const int k0 = now.stage * kSpan;
             const int blocks = min(kSpan, a.k - k0) / 32;
             cp_async_wait<kStages - 2>();
             __syncwarp();
             issue(ahead, (slot + kStages - 1) % kStages);
-            const uint32_t at = ring + slot * kStageBytes;
-            const uint32_t wd = at + g * kPitch + t * 4;
-            const unsigned skip = skip0 + now.stage * kGroups;
+            const uint8_t *at = ring + slot * kStageBytes;
+            const uint8_t *wd = at + g * kPitch + t * 4;
+            const unsigned moved = now.stage * kGroups;
             advance(now);
-            const int k_next = now.item == d.item ? now.stage * kSpan : a.k;
+            // blocks of the item's next stage
+            const int next = now.item == d.item ? min(kSpan, a.k - now.stage * kSpan) / 32 : 0;
+            float sum[2][NT][4];
+            uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
 #pragma unroll
-            for (int half = 0; half < HALVES; ++half) {
-                float sum[2][NT][4];
-                uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
+            for (int b = 0; b < 4; ++b) {
+                if (b >= blocks) break;
+                constexpr int kPer = GROUP / 32;  // blocks of a group
+                const int group = b / kPer;
+                if (b % kPer == 0) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (b >= blocks) break;
-                    constexpr int kPer = GROUP / 32;  // blocks of a group
-                    const int group = b / kPer;
-                    if (b % kPer == 0) {
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
+                        for (int i = 0; i < NT; ++i)
 #pragma unroll
-                            for (int i = 0; i < NT; ++i)
+                            for (int j = 0; j < 4; ++j) sum[m][i][j] = 0.f;
+                    if (a.zeros) {
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) sum[m][i][j] = 0.f;
-                        if (a.zeros) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t z = lds_u8(at + kZeroAt + (g + 8 * i) * kZeroPitch +
-                                                          ((skip + 8 * i * groups) & 3u) + group);
-                                zero[i] = __byte_perm(z, 0x43u, 0x4040);  // 128 + z, twice
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t z = at[kZeroAt + (g + 8 * i) * kZeroPitch +
+                                                  ((skips[i] + moved) & 3u) + group];
+                            zero[i] = __byte_perm(z, 0x43u, 0x4040);  // 128 + z, twice
                         }
                     }
-                    // 0x4300 | q is 128 + q in BF16; minus 128 + z is exact
-                    uint32_t q[4][4];
+                }
+                // 0x4300 | q is 128 + q in BF16; minus 128 + z is exact
+                uint32_t q[4][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t w = lds_32(wd + 8 * i * kPitch + b * 16);
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w =
+                        *reinterpret_cast<const uint32_t *>(wd + 8 * i * kPitch + b * 16);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            q[i][j] =
-                                sub_bf16x2(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u, zero[i]);
+                    for (int j = 0; j < 4; ++j)
+                        q[i][j] =
+                            sub_bf16x2(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u, zero[i]);
+                }
+                // q[.][j] holds summed values j and j + 4 of the thread's eight
+                const uint32_t a0[2][4] = {{q[0][0], q[1][0], q[0][1], q[1][1]},
+                                           {q[2][0], q[3][0], q[2][1], q[3][1]}};
+                const uint32_t a1[2][4] = {{q[0][2], q[1][2], q[0][3], q[1][3]},
+                                           {q[2][2], q[3][2], q[2][3], q[3][3]}};
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const uint4 v = xv[b][i];
+                    const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410);
+                    const uint32_t b1 = __byte_perm(v.x, v.z, 0x7632);
+                    const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410);
+                    const uint32_t b3 = __byte_perm(v.y, v.w, 0x7632);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        mma_16816(sum[m][i], a0[m], b0, b1);
+                        mma_16816(sum[m][i], a1[m], b2, b3);
                     }
-                    // q[.][j] holds summed values j and j + 4 of the thread's eight
-                    const uint32_t a0[2][4] = {{q[0][0], q[1][0], q[0][1], q[1][1]},
-                                               {q[2][0], q[3][0], q[2][1], q[3][1]}};
-                    const uint32_t a1[2][4] = {{q[0][2], q[1][2], q[0][3], q[1][3]},
-                                               {q[2][2], q[3][2], q[2][3], q[3][3]}};
+                }
+                if (b < next) load_x(b, share * kSpan);
+                if (b % kPer == kPer - 1) {
+                    float s[4];
+                    const uint8_t *sa = at + kScaleAt + g * kScalePitch;
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        const uint4 v = xv[b][i];
-                        const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410);
-                        const uint32_t b1 = __byte_perm(v.x, v.z, 0x7632);
-                        const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410);
-                        const uint32_t b3 = __byte_perm(v.y, v.w, 0x7632);
+                    for (int i = 0; i < 4; ++i)
+                        if (a.scale_fp32)
+                            s[i] = *reinterpret_cast<const float *>(sa + 8 * i * kScalePitch +
+                                                                    4 * group);
+                        else
+                            s[i] = __uint_as_float(
+                                uint32_t{*reinterpret_cast<const uint16_t *>(
+                                    sa + 8 * i * kScalePitch +
+                                    2 * (((skips[i] + moved) & 1u) + group))}
+                                << 16);
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            mma_16816(sum[m][i], a0[m], b0, b1);
-                            mma_16816(sum[m][i], a1[m], b2, b3);
-                        }
-                    }
-                    if (half + 1 < HALVES)
-                        load_x(b, half + 1, k0 + 32 * b);
-                    else
-                        load_x(b, 0, k_next + 32 * b);
-                    if (b % kPer == kPer - 1) {
-                        float s[4];
-                        const uint32_t sa = at + kScaleAt + g * kScalePitch;
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (a.scale_fp32)
-                                s[i] = __uint_as_float(lds_32(sa + 8 * i * kScalePitch + 4 * group));
-                            else
-                                s[i] = __uint_as_float(
-                                    lds_u16(sa + 8 * i * kScalePitch +
-                                            2 * (((skip + 8 * i * groups) & 1u) + group))
-                                    << 16);
+                        for (int i = 0; i < NT; ++i)
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    acc[half][m][i][j] =
-                                        fmaf(s[2 * m + j / 2], sum[m][i][j], acc[half][m][i][j]);
-                    }
+                            for (int j = 0; j < 4; ++j)
+                                acc[m][i][j] =
+                                    fmaf(s[2 * m + j / 2], sum[m][i][j], acc[m][i][j]);
                 }
             }
             __syncwarp();
             slot = (slot + 1) % kStages;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) x[i] += share * kSpan;
         }
-        // acc[h][m][i][j]: n = 16 m + g + 8 (j / 2), row = 8 (h NT + i) + 2 t + j % 2
+        // acc[m][i][j]: n = 16 m + g + 8 (j / 2), row = 8 i + 2 t + j % 2
         float *mine = sums + part * (kCols * kRowsPass);
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int n = 16 * m + g + 8 * (j / 2);
-                        const int r = 8 * (h * NT + i) + 2 * t + j % 2;
-                        const float v = acc[h][m][i][j];
-                        if (share > 1)
-                            mine[r * kCols + n] = v;
-                        else if (r < d.rows && d.n0 + n < a.n)
-                            store(d.row0 + r, d.n0 + n, v);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const int n = 16 * m + g + 8 * (j / 2);
+                    const int r = 8 * i + 2 * t + j % 2;
+                    const float v = acc[m][i][j];
+                    if (share > 1)
+                        mine[r * kCols + n] = v;
+                    else if (r < d.rows && d.n0 + n < a.n)
+                        store(d, r, n, v);
+                }
         if (share == 1) return;
         meet();
         if (d.n0 + lane < a.n)
             for (int r = part; r < d.rows; r += share) {
                 float v = 0.f;
                 for (int s = 0; s < share; ++s) v += sums[s * (kCols * kRowsPass) + r * kCols + lane];
-                store(d.row0 + r, d.n0 + lane, v);
+                store(d, r, lane, v);
             }
         meet();
     }
@@ -430,7 +415,9 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
                         col_blocks,
                         (a.k + kSpan - 1) / kSpan,
                         a.k / GROUP,
+                        smem + warp * (kStages * kStageBytes),
                         smem_u32(smem) + warp * (kStages * kStageBytes),
+                        1 << (31 - __clz(a.num_experts)),
                         reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes) +
                             block * share * (kCols * kRowsPass),
                         1 + block};
@@ -442,11 +429,9 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     uint32_t slot = 0;
     while (now.item < k.items) {
         if (now.rows <= 8)
-            k.template item<1, 1>(now, ahead, slot);
-        else if (now.rows <= 16)
-            k.template item<2, 1>(now, ahead, slot);
+            k.template item<1>(now, ahead, slot);
         else
-            k.template item<2, 2>(now, ahead, slot);
+            k.template item<2>(now, ahead, slot);
     }
     cp_async_wait<0>();
 }
