@@ -84,6 +84,8 @@ struct GemvArgs {
     int out_fp32;
     int64_t out_ld;
     int num_sms;
+    unsigned *status;
+    uint64_t timeout_ns;
     bool programmatic;
 };
 

@@ -296,6 +296,8 @@ mf_status moe_grouped_gemv_int4(const void *x, int64_t x_rows, int64_t x_stride,
     a.out_fp32 = output_dtype == MF_DTYPE_FP32;
     a.out_ld = output_stride;
     a.num_sms = d->num_sms;
+    a.status = d->status;
+    a.timeout_ns = mf::kWaitLimitNs;
     a.programmatic = mf::programmatic_launch();
     return from_launch(
         mf::launch_grouped_gemv_int4(a, reinterpret_cast<cudaStream_t>(stream)));

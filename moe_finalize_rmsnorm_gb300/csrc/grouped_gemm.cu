@@ -20,10 +20,9 @@
 // issues the copies of blocks (TMA, 128-byte swizzle, 64 summed values a step), a
 // warp that issues the products into one of two accumulators in TMEM, four warps
 // that move the other accumulator out, and one more per stage for rows that are gathered.
-#include <cuda.h>
-
 #include "experts.cuh"
 #include "experts.h"
+#include "tensor_map.h"
 
 namespace mf {
 namespace {
@@ -501,18 +500,13 @@ using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, vo
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeFn g_encode = nullptr;  // the driver's encoder, found once (prepare)
 
-// Tensor map of BF16 values: `dims` sizes fastest first, `strides` (elements) of
-// the slower ones, boxes of 64 values by `rows`.
-bool encode(CUtensorMap *m, const void *p, int rank, const cuuint64_t (&dims)[3],
+// BF16 values, strides in elements, boxes of one step by `rows`.
+bool encode(CUtensorMap *m, const void *p, int rank, const cuuint64_t (&sizes)[3],
             const int64_t (&strides)[2], int rows) {
-    cuuint64_t bytes[2] = {static_cast<cuuint64_t>(strides[0]) * 2,
-                           static_cast<cuuint64_t>(strides[1]) * 2};
-    cuuint32_t box[3] = {kStep, static_cast<cuuint32_t>(rows), 1};
-    cuuint32_t ones[3] = {1, 1, 1};
-    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(p), dims, bytes,
-                    box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_map(
+        m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, rank, sizes,
+        {static_cast<cuuint64_t>(strides[0]) * 2, static_cast<cuuint64_t>(strides[1]) * 2}, kStep,
+        rows);
 }
 
 template <int KIND, int CTAS, bool GATHER>
@@ -576,6 +570,17 @@ cudaError_t prepare_ctas() {
 }
 
 }  // namespace
+
+bool encode_map(CUtensorMap *m, CUtensorMapDataType type, const void *p, int rank,
+                const cuuint64_t (&sizes)[3], const cuuint64_t (&strides)[2], int columns,
+                int rows) {
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(columns), static_cast<cuuint32_t>(rows), 1};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return g_encode(m, type, rank, const_cast<void *>(p), sizes, strides, box, ones,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t prepare_grouped_gemm(int *pairs) {
     if (!g_encode) {

@@ -1,17 +1,19 @@
 // Products of few rows per expert with 4-bit weights and group scales.
 //
 // Bound by the weights' bytes: each is read once for every 16 rows of its
-// expert.  A warp takes 32 columns n and up to 16 rows.  It streams 128 summed
-// values of its 32 columns a stage (64 bytes a column) through its own ring in
-// shared memory (cp.async), turns the nibbles into BF16 integers q - z (exact),
-// and multiplies with the rows in mma.m16n8k16, n along M, the rows along N:
-// with so few rows the tensor cores only have to keep up with the conversion.
-// Each group's FP32 sum is scaled once.  Warps that share a column block split
-// the summed values between them and add up through shared memory, in warp order.
+// expert.  A warp takes 32 columns n and up to 16 rows.  It streams 256 summed
+// values of its 32 columns a stage (128 bytes a column) through its own ring in
+// shared memory, one tensor-map copy a stage, turns the nibbles into BF16 integers
+// q - z (exact), and multiplies with the rows in mma.m16n8k16, n along M, the rows
+// along N: with so few rows the tensor cores only have to keep up with the
+// conversion.  Each group's FP32 sum is scaled once.  Warps that share a column
+// block split the summed values between them and add up through shared memory, in
+// warp order.
 #include <string.h>
 
 #include "experts.cuh"
 #include "experts.h"
+#include "tensor_map.h"
 
 namespace mf {
 namespace {
@@ -20,27 +22,26 @@ constexpr int kWarps = 12;
 constexpr int kGemvThreads = 32 * kWarps;
 constexpr int kCols = 32;      // n of a warp
 constexpr int kRowsPass = 16;  // rows of one pass over the weights
-constexpr int kSpan = 128;     // summed values of a stage
-constexpr int kStages = 4;
-// A stage: 32 columns of 64 bytes, 80 apart (the quad reads of eight columns
-// then fall into different banks), and per column up to four scales and zeros.
-constexpr int kPitch = 80;
-constexpr int kScalePitch = 16;  // four FP32 scales, or four BF16 from either half of a word on
-constexpr int kZeroPitch = 8;    // four bytes from any byte of a word on
-constexpr int kScaleAt = kCols * kPitch;
-constexpr int kZeroAt = kScaleAt + kCols * kScalePitch;
-constexpr int kStageBytes = kZeroAt + kCols * kZeroPitch;
+constexpr int kSpan = 256;     // summed values of a stage: 128 bytes of a column
+constexpr int kStages = 3;
+constexpr int kWeightBytes = kCols * kSpan / 2;
+// Per column and stage up to eight scales and zeros: FP32, or the words that hold
+// eight BF16 from either half of a word on, or eight bytes from any byte on.
+constexpr int kScalePitch = 32;
+constexpr int kZeroPitch = 12;
+constexpr int kZeroAt = kCols * kScalePitch;
+constexpr int kGroupBytes = kZeroAt + kCols * kZeroPitch;
 constexpr int kSumBytes = kCols * kRowsPass * 4;  // one warp's partial results
 
 struct GemvControl {
+    uint64_t full[kWarps][kStages];
     int scan[kWarps];
-    int tiles[kMaxExperts + 1];
-    int lo[kMaxExperts];
-    int rows[kMaxExperts];
+    int tiles[kMaxExperts + 1];  // passes of the experts before this one
+    int lo[kMaxExperts + 1];     // first row
 };
 
-constexpr int kGemvSmem =
-    kWarps * (kStages * kStageBytes + kSumBytes) + static_cast<int>(sizeof(GemvControl));
+constexpr int kGemvSmem = 1024 + kWarps * (kStages * (kWeightBytes + kGroupBytes) + kSumBytes) +
+                          static_cast<int>(sizeof(GemvControl));
 static_assert(kGemvSmem <= 227 * 1024, "shared memory of one CTA");
 
 // 4 bytes global -> shared, the bytes behind `bytes` (0..4) as zeros.
@@ -55,6 +56,13 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// (a & b) | c in one instruction (written out: two constants otherwise cost two).
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
@@ -73,14 +81,12 @@ struct Cursor {
     int expert, n0, row0, rows;
 };
 
-// The same for the copies, with this lane's addresses.  Columns behind the last
-// one stand for the last one: their results are not stored.
+// The same for the copies.
 struct Copies {
     int64_t item;
     int stage;
-    const uint8_t *w;  // the lane's 16 bytes of the block's first column in this stage
-    int at[4];         // and from there to columns lane / 4 + 8 i
-    int64_t o;         // number of the first scale of column `lane` in this stage
+    int expert, n0;
+    int64_t o;  // number of the first scale of the lane's column in this stage
 };
 
 template <int GROUP>
@@ -88,20 +94,20 @@ struct Gemv {
     static constexpr int kGroups = kSpan / GROUP;  // of a stage
 
     const GemvArgs &a;
+    const CUtensorMap &map;
     const GemvControl &c;
     const int lane, g, t;
     const int share, part;  // warps of a column block, this one's number
-    const int64_t first, step, items;
+    const int64_t step, items;
     const int col_blocks, spans, groups;
-    const uint8_t *ring;
-    const uint32_t ring_addr;
-    const int search;  // first step of the search for an expert
+    const int search;           // first step of the search for an expert
+    const uint8_t *weights;     // this warp's stages
+    const uint8_t *group_data;
+    const uint32_t weights_at, group_at, full;
     float *sums;  // of the block's first warp
     const int barrier;
 
-    // The pass over the weights that holds a column block, counted over the experts.
-    __device__ int pass_of(int64_t item) const { return static_cast<int>(item / col_blocks); }
-
+    // The expert of a pass over the weights (they are counted over the experts).
     __device__ int expert_of(int pass) const {
         int e = 0;
         for (int s = search; s > 0; s /= 2)
@@ -111,23 +117,21 @@ struct Gemv {
 
     __device__ void locate(Cursor &p) const {
         if (p.item >= items) return;
-        const int u = pass_of(p.item);
-        p.expert = expert_of(u);
-        p.n0 = static_cast<int>(p.item - int64_t{u} * col_blocks) * kCols;
-        const int first_row = (u - c.tiles[p.expert]) * kRowsPass;
+        const int pass = static_cast<int>(p.item / col_blocks);
+        p.expert = expert_of(pass);
+        p.n0 = static_cast<int>(p.item - int64_t{pass} * col_blocks) * kCols;
+        const int first_row = (pass - c.tiles[p.expert]) * kRowsPass;
         p.row0 = c.lo[p.expert] + first_row;
-        p.rows = min(kRowsPass, c.rows[p.expert] - first_row);
+        p.rows = min(kRowsPass, c.lo[p.expert + 1] - p.row0);
     }
 
     __device__ void locate(Copies &p) const {
         if (p.item >= items) return;
-        const int u = pass_of(p.item);
-        const int n0 = static_cast<int>(p.item - int64_t{u} * col_blocks) * kCols;
-        const int64_t line = int64_t{expert_of(u)} * a.n + n0;
-        p.w = a.w + line * (a.k / 2) + part * (kSpan / 2) + lane % 4 * 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p.at[i] = min(lane / 4 + 8 * i, a.n - 1 - n0) * (a.k / 2);
-        p.o = (line + min(lane, a.n - 1 - n0)) * groups + part * kGroups;
+        const int pass = static_cast<int>(p.item / col_blocks);
+        p.expert = expert_of(pass);
+        p.n0 = static_cast<int>(p.item - int64_t{pass} * col_blocks) * kCols;
+        // columns behind the last stand for it: their results are not stored
+        p.o = (int64_t{p.expert} * a.n + min(p.n0 + lane, a.n - 1)) * groups + part * kGroups;
     }
 
     __device__ void advance(Cursor &p) const {
@@ -142,13 +146,14 @@ struct Gemv {
     // Start the copies of a stage (nothing behind the last item) and go on.
     __device__ void issue(Copies &p, uint32_t slot) const {
         if (p.item < items) {
-            const uint32_t at = ring_addr + slot * kStageBytes;
-            const uint32_t wd = at + lane / 4 * kPitch + lane % 4 * 16;
-            if (p.stage * kSpan + lane % 4 * 32 < a.k)  // later blocks are not multiplied
-#pragma unroll
-                for (int i = 0; i < 4; ++i) cp_async_16(wd + 8 * i * kPitch, p.w + p.at[i], true);
+            if (elect_one()) {
+                mbar_arrive_expect_tx(full + 8 * slot, kWeightBytes);
+                tma_3d<false>(weights_at + slot * kWeightBytes, &map, p.stage * (kSpan / 2), p.n0,
+                              p.expert, full + 8 * slot);
+            }
+            __syncwarp();
             const int ng = min(kGroups, groups - p.stage * kGroups);
-            const uint32_t sd = at + kScaleAt + lane * kScalePitch;
+            const uint32_t sd = group_at + slot * kGroupBytes + lane * kScalePitch;
             if (a.scale_fp32) {
                 const float *s = static_cast<const float *>(a.scales) + p.o;
 #pragma unroll
@@ -165,13 +170,13 @@ struct Gemv {
             if (a.zeros) {
                 const uint8_t *z = a.zeros + (p.o & ~int64_t{3});
                 const int bytes = static_cast<int>(p.o & 3) + ng;
-                const uint32_t zd = at + kZeroAt + lane * kZeroPitch;
+                const uint32_t zd =
+                    group_at + slot * kGroupBytes + kZeroAt + lane * kZeroPitch;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < (kGroups + 6) / 4; ++i)
                     if (4 * i < bytes) cp_async_4(zd + 4 * i, z + 4 * i, min(4, bytes - 4 * i));
             }
             p.stage += share;
-            p.w += share * (kSpan / 2);
             p.o += share * kGroups;
             if (p.stage >= spans) {
                 p.stage = part;
@@ -197,9 +202,11 @@ struct Gemv {
             static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
     }
 
-    // One column block with up to 8 NT rows.
+    // One column block with up to 8 NT rows.  A copy that does not arrive within
+    // `limit` sets the status and the limit to zero: the warp goes on (the others
+    // wait for it at the block's barrier), with results of no meaning.
     template <int NT>
-    __device__ void item(Cursor &now, Copies &ahead, uint32_t &slot) const {
+    __device__ void item(Cursor &now, Copies &ahead, uint32_t &it, uint64_t &limit) const {
         const Cursor d = now;
         // The rows this thread feeds (row g of every eight).  Where there is none, any
         // row will do: its results are not stored, or stored as zeros.
@@ -210,8 +217,8 @@ struct Gemv {
             x[i] = static_cast<const __nv_bfloat16 *>(a.x) + max(row, 0) * a.x_ld + 8 * t +
                    now.stage * kSpan;
         }
-        // The rows' values of one stage, loaded a stage before they are used: they come
-        // from the L2, some 800 cycles away.
+        // The rows' values of half a stage, loaded half a stage before they are used:
+        // they come from the L2, some 800 cycles away.
         uint4 xv[4][NT];
         auto load_x = [&](int b, int k) {
 #pragma unroll
@@ -224,109 +231,117 @@ struct Gemv {
             for (int b = 0; b < 4; ++b)
                 if (b < blocks) load_x(b, 0);
         }
-        // Where the copied words hold the scale and zero of column g + 8 i: from its
-        // number modulo 4 on.  (A stage of four groups keeps it, of two moves it by
-        // two, of one by one.)
-        const unsigned skip0 = static_cast<unsigned>((int64_t{d.expert} * a.n + d.n0 + g) * groups);
-        // columns behind the last stand for it
+        // Number of the first scale of columns g + 8 i: modulo 2 and 4 it says where the
+        // copied words hold the scale and the zero.
         unsigned skips[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            skips[i] = skip0 + (min(g + 8 * i, a.n - 1 - d.n0) - g) * groups;
+            skips[i] = static_cast<unsigned>(
+                (int64_t{d.expert} * a.n + min(d.n0 + g + 8 * i, a.n - 1)) * groups);
         float acc[2][NT][4] = {};
         while (now.item == d.item) {
-            const int k0 = now.stage * kSpan;
-            const int blocks = min(kSpan, a.k - k0) / 32;
+            const int blocks = min(kSpan, a.k - now.stage * kSpan) / 32;
+            const uint32_t slot = it % kStages;
             cp_async_wait<kStages - 2>();
-            __syncwarp();
-            issue(ahead, (slot + kStages - 1) % kStages);
-            const uint8_t *at = ring + slot * kStageBytes;
-            const uint8_t *wd = at + g * kPitch + t * 4;
+            if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * slot, it / kStages & 1, limit))) {
+                limit = 0;
+                if (lane == 0) atomicOr(a.status, kStatusWaitTimeout);
+            }
+            issue(ahead, (it + kStages - 1) % kStages);
+            const uint8_t *wd = weights + slot * kWeightBytes + g * 128 + t * 4;
+            const uint8_t *gd = group_data + slot * kGroupBytes;
             const unsigned moved = now.stage * kGroups;
             advance(now);
             // blocks of the item's next stage
             const int next = now.item == d.item ? min(kSpan, a.k - now.stage * kSpan) / 32 : 0;
-            float sum[2][NT][4];
-            uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const int left = blocks - 4 * half;  // blocks from here on
+                const int after = half ? next : blocks - 4;
+                const int x_next = half ? share * kSpan - 128 : 128;
+                float sum[2][NT][4];
+                uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (b >= blocks) break;
-                constexpr int kPer = GROUP / 32;  // blocks of a group
-                const int group = b / kPer;
-                if (b % kPer == 0) {
+                for (int b = 0; b < 4; ++b) {
+                    if (b >= left) break;
+                    constexpr int kPer = GROUP / 32;  // blocks of a group
+                    const int group = (4 * half + b) / kPer;
+                    if (b % kPer == 0) {
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                        for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int i = 0; i < NT; ++i)
+                            for (int i = 0; i < NT; ++i)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) sum[m][i][j] = 0.f;
-                    if (a.zeros) {
+                                for (int j = 0; j < 4; ++j) sum[m][i][j] = 0.f;
+                        if (a.zeros) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t z = at[kZeroAt + (g + 8 * i) * kZeroPitch +
-                                                  ((skips[i] + moved) & 3u) + group];
-                            zero[i] = __byte_perm(z, 0x43u, 0x4040);  // 128 + z, twice
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t z = gd[kZeroAt + (g + 8 * i) * kZeroPitch +
+                                                      ((skips[i] + moved) & 3u) + group];
+                                zero[i] = __byte_perm(z, 0x43u, 0x4040);  // 128 + z, twice
+                            }
                         }
                     }
-                }
-                // 0x4300 | q is 128 + q in BF16; minus 128 + z is exact
-                uint32_t q[4][4];
+                    // 0x4300 | q is 128 + q in BF16; minus 128 + z is exact.  The copy's
+                    // swizzle keeps the eight columns' words in different banks.
+                    uint32_t q[4][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t w =
-                        *reinterpret_cast<const uint32_t *>(wd + 8 * i * kPitch + b * 16);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                            wd + 1024 * i + (((4 * half + b) ^ g) << 4));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        q[i][j] =
-                            sub_bf16x2(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u, zero[i]);
-                }
-                // q[.][j] holds summed values j and j + 4 of the thread's eight
-                const uint32_t a0[2][4] = {{q[0][0], q[1][0], q[0][1], q[1][1]},
-                                           {q[2][0], q[3][0], q[2][1], q[3][1]}};
-                const uint32_t a1[2][4] = {{q[0][2], q[1][2], q[0][3], q[1][3]},
-                                           {q[2][2], q[3][2], q[2][3], q[3][3]}};
+                        for (int j = 0; j < 4; ++j)
+                            q[i][j] =
+                                sub_bf16x2(and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u), zero[i]);
+                    }
+                    // q[.][j] holds summed values j and j + 4 of the thread's eight
+                    const uint32_t a0[2][4] = {{q[0][0], q[1][0], q[0][1], q[1][1]},
+                                               {q[2][0], q[3][0], q[2][1], q[3][1]}};
+                    const uint32_t a1[2][4] = {{q[0][2], q[1][2], q[0][3], q[1][3]},
+                                               {q[2][2], q[3][2], q[2][3], q[3][3]}};
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const uint4 v = xv[b][i];
-                    const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410);
-                    const uint32_t b1 = __byte_perm(v.x, v.z, 0x7632);
-                    const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410);
-                    const uint32_t b3 = __byte_perm(v.y, v.w, 0x7632);
+                    for (int i = 0; i < NT; ++i) {
+                        const uint4 v = xv[b][i];
+                        const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410);
+                        const uint32_t b1 = __byte_perm(v.x, v.z, 0x7632);
+                        const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410);
+                        const uint32_t b3 = __byte_perm(v.y, v.w, 0x7632);
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        mma_16816(sum[m][i], a0[m], b0, b1);
-                        mma_16816(sum[m][i], a1[m], b2, b3);
+                        for (int m = 0; m < 2; ++m) {
+                            mma_16816(sum[m][i], a0[m], b0, b1);
+                            mma_16816(sum[m][i], a1[m], b2, b3);
+                        }
+                    }
+                    if (b < after) load_x(b, x_next);
+                    if (b % kPer == kPer - 1) {
+                        float s[4];
+                        const uint8_t *sa = gd + g * kScalePitch;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (a.scale_fp32)
+                                s[i] = *reinterpret_cast<const float *>(sa + 8 * i * kScalePitch +
+                                                                        4 * group);
+                            else
+                                s[i] = __uint_as_float(
+                                    uint32_t{*reinterpret_cast<const uint16_t *>(
+                                        sa + 8 * i * kScalePitch +
+                                        2 * (((skips[i] + moved) & 1u) + group))}
+                                    << 16);
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    acc[m][i][j] =
+                                        fmaf(s[2 * m + j / 2], sum[m][i][j], acc[m][i][j]);
                     }
                 }
-                if (b < next) load_x(b, share * kSpan);
-                if (b % kPer == kPer - 1) {
-                    float s[4];
-                    const uint8_t *sa = at + kScaleAt + g * kScalePitch;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (a.scale_fp32)
-                            s[i] = *reinterpret_cast<const float *>(sa + 8 * i * kScalePitch +
-                                                                    4 * group);
-                        else
-                            s[i] = __uint_as_float(
-                                uint32_t{*reinterpret_cast<const uint16_t *>(
-                                    sa + 8 * i * kScalePitch +
-                                    2 * (((skips[i] + moved) & 1u) + group))}
-                                << 16);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int i = 0; i < NT; ++i)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                acc[m][i][j] =
-                                    fmaf(s[2 * m + j / 2], sum[m][i][j], acc[m][i][j]);
-                }
+                for (int i = 0; i < NT; ++i) x[i] += x_next;
             }
             __syncwarp();
-            slot = (slot + 1) % kStages;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) x[i] += share * kSpan;
+            ++it;
         }
         // acc[m][i][j]: n = 16 m + g + 8 (j / 2), row = 8 i + 2 t + j % 2
         float *mine = sums + part * (kCols * kRowsPass);
@@ -363,11 +378,16 @@ struct Gemv {
 
 template <int GROUP>
 __global__ void __launch_bounds__(kGemvThreads, 1)
-    grouped_gemv_int4_kernel(const GemvArgs a, const int share) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    GemvControl &c =
-        *reinterpret_cast<GemvControl *>(smem + kWarps * (kStages * kStageBytes + kSumBytes));
+    grouped_gemv_int4_kernel(const __grid_constant__ CUtensorMap map, const GemvArgs a,
+                             const int share) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = raw + (((smem_u32(raw) + 1023u) & ~1023u) - smem_u32(raw));
+    uint8_t *group_data = smem + kWarps * kStages * kWeightBytes;
+    uint8_t *sums = group_data + kWarps * kStages * kGroupBytes;
+    GemvControl &c = *reinterpret_cast<GemvControl *>(sums + kWarps * kSumBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (lane < kStages) mbar_init(smem_u32(&c.full[warp][lane]), 1);
+    fence_mbar_init();
     pdl_wait();
 
     // The experts' rows and the numbers of their passes (exclusive scan).
@@ -379,7 +399,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
         int lo = 0, hi = static_cast<int>(a.rows);
         if (a.offsets) expert_rows(a.offsets, e, static_cast<int>(a.rows), lo, hi);
         c.lo[e] = lo;
-        c.rows[e] = hi - lo;
+        if (e + 1 == a.num_experts) c.lo[e + 1] = hi;
         c.tiles[e] = sum;
         sum += (hi - lo + kRowsPass - 1) / kRowsPass;
     }
@@ -402,52 +422,77 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
 
     const int block = warp / share;
     const int col_blocks = (a.n + kCols - 1) / kCols;
+    const int64_t item0 = blockIdx.x + int64_t{gridDim.x} * block;
+    uint8_t *weights = smem + warp * (kStages * kWeightBytes);
+    uint8_t *groups = group_data + warp * (kStages * kGroupBytes);
     const Gemv<GROUP> k{a,
+                        map,
                         c,
                         lane,
                         lane / 4,
                         lane % 4,
                         share,
                         warp % share,
-                        blockIdx.x + int64_t{gridDim.x} * block,
                         int64_t{gridDim.x} * (kWarps / share),
                         int64_t{total} * col_blocks,
                         col_blocks,
                         (a.k + kSpan - 1) / kSpan,
                         a.k / GROUP,
-                        smem + warp * (kStages * kStageBytes),
-                        smem_u32(smem) + warp * (kStages * kStageBytes),
                         1 << (31 - __clz(a.num_experts)),
-                        reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes) +
-                            block * share * (kCols * kRowsPass),
+                        weights,
+                        groups,
+                        smem_u32(weights),
+                        smem_u32(groups),
+                        smem_u32(&c.full[warp][0]),
+                        reinterpret_cast<float *>(sums) + block * share * (kCols * kRowsPass),
                         1 + block};
-    Cursor now{k.first, k.part, 0, 0, 0, 0};
+    Cursor now{item0, k.part, 0, 0, 0, 0};
     k.locate(now);
-    Copies ahead{k.first, k.part, nullptr, 0, 0};
+    Copies ahead{item0, k.part, 0, 0, 0};
     k.locate(ahead);
     for (int s = 0; s < kStages - 1; ++s) k.issue(ahead, s);
-    uint32_t slot = 0;
+    uint32_t it = 0;
+    uint64_t limit = a.timeout_ns;
     while (now.item < k.items) {
         if (now.rows <= 8)
-            k.template item<1>(now, ahead, slot);
+            k.template item<1>(now, ahead, it, limit);
         else
-            k.template item<2>(now, ahead, slot);
+            k.template item<2>(now, ahead, it, limit);
     }
+    if (limit == 0)  // copies may still be in flight: wait once more before the memory goes
+        for (uint32_t s = 1; s <= kStages && s <= it; ++s)
+            (void)mbar_wait(k.full + 8 * ((it - s) % kStages), (it - s) / kStages & 1, a.timeout_ns);
     cp_async_wait<0>();
 }
 
 template <int GROUP>
 cudaError_t launch(const GemvArgs &a, cudaStream_t s) {
-    // Warps to a column block: the summed values are split until every warp of the
-    // device has work.
+    CUtensorMap map;
+    const cuuint64_t row = static_cast<cuuint64_t>(a.k) / 2;
+    if (!encode_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, 3,
+                    {row, static_cast<cuuint64_t>(a.n), static_cast<cuuint64_t>(a.num_experts)},
+                    {row, row * a.n}, kSpan / 2, kCols))
+        return cudaErrorInvalidValue;
+    // Warps to a column block: as many as make the longest warp's work shortest,
+    // counted in stages (the experts' sizes are known on the device only: at most
+    // this many blocks).
     const int64_t blocks = (a.n + kCols - 1) / kCols *
                            (a.rows / kRowsPass + min(int64_t{a.num_experts}, a.rows));
     const int spans = (a.k + kSpan - 1) / kSpan;
     int share = 1;
-    while (share < 4 && 2 * share <= spans && blocks * share < int64_t{a.num_sms} * kWarps) share *= 2;
+    int64_t best = INT64_MAX;
+    for (int w : {1, 2, 3, 4, 6, 12}) {
+        if (w > spans) break;
+        const int64_t at_once = int64_t{a.num_sms} * (kWarps / w);
+        const int64_t cost = (blocks + at_once - 1) / at_once * ((spans + w - 1) / w);
+        if (cost < best) {
+            best = cost;
+            share = w;
+        }
+    }
     return launch_ex(grouped_gemv_int4_kernel<GROUP>,
                      dim3(static_cast<unsigned>(min(blocks, int64_t{a.num_sms}))),
-                     dim3(kGemvThreads), kGemvSmem, s, 1, a.programmatic, a, share);
+                     dim3(kGemvThreads), kGemvSmem, s, 1, a.programmatic, map, a, share);
 }
 
 }  // namespace
