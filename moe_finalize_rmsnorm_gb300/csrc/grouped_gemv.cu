@@ -18,20 +18,23 @@
 namespace mf {
 namespace {
 
-constexpr int kWarps = 12;
+constexpr int kWarps = 16;
 constexpr int kGemvThreads = 32 * kWarps;
 constexpr int kCols = 32;      // n of a warp
-constexpr int kRowsPass = 16;  // rows of one pass over the weights
 constexpr int kSpan = 256;     // summed values of a stage: 128 bytes of a column
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kWeightBytes = kCols * kSpan / 2;
-// Per column and stage up to eight scales and zeros: FP32, or the words that hold
-// eight BF16 from either half of a word on, or eight bytes from any byte on.
-constexpr int kScalePitch = 32;
-constexpr int kZeroPitch = 12;
-constexpr int kZeroAt = kCols * kScalePitch;
-constexpr int kGroupBytes = kZeroAt + kCols * kZeroPitch;
-constexpr int kSumBytes = kCols * kRowsPass * 4;  // one warp's partial results
+
+// A stage's scales and zeros per column: FP32, or the words that hold the BF16 from
+// either half of a word on, or the bytes from any byte on.
+template <int GROUP>
+struct GroupData {
+    static constexpr int kGroups = kSpan / GROUP;
+    static constexpr int kScalePitch = 4 * kGroups;
+    static constexpr int kZeroPitch = (kGroups + 6) / 4 * 4;
+    static constexpr int kZeroAt = kCols * kScalePitch;
+    static constexpr int kBytes = kZeroAt + kCols * kZeroPitch;
+};
 
 struct GemvControl {
     uint64_t full[kWarps][kStages];
@@ -40,9 +43,15 @@ struct GemvControl {
     int lo[kMaxExperts + 1];     // first row
 };
 
-constexpr int kGemvSmem = 1024 + kWarps * (kStages * (kWeightBytes + kGroupBytes) + kSumBytes) +
-                          static_cast<int>(sizeof(GemvControl));
-static_assert(kGemvSmem <= 227 * 1024, "shared memory of one CTA");
+// One CTA: the stages, the partial results of 8 TILES rows for every warp, the control.
+template <int GROUP, int TILES>
+struct GemvSmem {
+    static constexpr int kSumBytes = kCols * 8 * TILES * 4;
+    static constexpr int kBytes =
+        1024 + kWarps * (kStages * (kWeightBytes + GroupData<GROUP>::kBytes) + kSumBytes) +
+        static_cast<int>(sizeof(GemvControl));
+    static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
+};
 
 // 4 bytes global -> shared, the bytes behind `bytes` (0..4) as zeros.
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src, int bytes) {
@@ -76,30 +85,34 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 
 // Where a warp is in its sequence of (column block, stage) pairs.
 struct Cursor {
-    int64_t item;
+    int item;
     int stage;  // of the item's spans
     int expert, n0, row0, rows;
 };
 
 // The same for the copies.
 struct Copies {
-    int64_t item;
+    int item;
     int stage;
     int expert, n0;
     int64_t o;  // number of the first scale of the lane's column in this stage
 };
 
-template <int GROUP>
+// TILES: a pass takes up to 8 TILES rows.
+template <int GROUP, int TILES>
 struct Gemv {
-    static constexpr int kGroups = kSpan / GROUP;  // of a stage
+    using G = GroupData<GROUP>;
+    static constexpr int kGroups = G::kGroups;
+    static constexpr int kRowsPass = 8 * TILES;
 
     const GemvArgs &a;
     const CUtensorMap &map;
     const GemvControl &c;
     const int lane, g, t;
     const int share, part;  // warps of a column block, this one's number
-    const int64_t step, items;
-    const int col_blocks, spans, groups;
+    const int step, items;
+    const unsigned col_blocks;
+    const int spans, groups;
     const int search;           // first step of the search for an expert
     const uint8_t *weights;     // this warp's stages
     const uint8_t *group_data;
@@ -117,9 +130,9 @@ struct Gemv {
 
     __device__ void locate(Cursor &p) const {
         if (p.item >= items) return;
-        const int pass = static_cast<int>(p.item / col_blocks);
+        const int pass = p.item / col_blocks;
         p.expert = expert_of(pass);
-        p.n0 = static_cast<int>(p.item - int64_t{pass} * col_blocks) * kCols;
+        p.n0 = (p.item - pass * col_blocks) * kCols;
         const int first_row = (pass - c.tiles[p.expert]) * kRowsPass;
         p.row0 = c.lo[p.expert] + first_row;
         p.rows = min(kRowsPass, c.lo[p.expert + 1] - p.row0);
@@ -127,9 +140,9 @@ struct Gemv {
 
     __device__ void locate(Copies &p) const {
         if (p.item >= items) return;
-        const int pass = static_cast<int>(p.item / col_blocks);
+        const int pass = p.item / col_blocks;
         p.expert = expert_of(pass);
-        p.n0 = static_cast<int>(p.item - int64_t{pass} * col_blocks) * kCols;
+        p.n0 = (p.item - pass * col_blocks) * kCols;
         // columns behind the last stand for it: their results are not stored
         p.o = (int64_t{p.expert} * a.n + min(p.n0 + lane, a.n - 1)) * groups + part * kGroups;
     }
@@ -153,7 +166,7 @@ struct Gemv {
             }
             __syncwarp();
             const int ng = min(kGroups, groups - p.stage * kGroups);
-            const uint32_t sd = group_at + slot * kGroupBytes + lane * kScalePitch;
+            const uint32_t sd = group_at + slot * G::kBytes + lane * G::kScalePitch;
             if (a.scale_fp32) {
                 const float *s = static_cast<const float *>(a.scales) + p.o;
 #pragma unroll
@@ -171,7 +184,7 @@ struct Gemv {
                 const uint8_t *z = a.zeros + (p.o & ~int64_t{3});
                 const int bytes = static_cast<int>(p.o & 3) + ng;
                 const uint32_t zd =
-                    group_at + slot * kGroupBytes + kZeroAt + lane * kZeroPitch;
+                    group_at + slot * G::kBytes + G::kZeroAt + lane * G::kZeroPitch;
 #pragma unroll
                 for (int i = 0; i < (kGroups + 6) / 4; ++i)
                     if (4 * i < bytes) cp_async_4(zd + 4 * i, z + 4 * i, min(4, bytes - 4 * i));
@@ -194,7 +207,6 @@ struct Gemv {
     }
 
     __device__ void store(const Cursor &d, int r, int n, float v) const {
-        if (a.row_index && x_row(d, r) < 0) v = 0.f;  // a row of zeros
         const int64_t at = (int64_t{d.row0} + r) * a.out_ld + d.n0 + n;
         if (a.out_fp32)
             static_cast<float *>(a.out)[at] = v;
@@ -211,24 +223,27 @@ struct Gemv {
         // The rows this thread feeds (row g of every eight).  Where there is none, any
         // row will do: its results are not stored, or stored as zeros.
         const __nv_bfloat16 *x[NT];
+        unsigned outside[NT];  // bit 4 j: row j of every eight is not in x
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int row = x_row(d, min(8 * i + g, d.rows - 1));
+            outside[i] = __ballot_sync(0xffffffffu, row < 0);
             x[i] = static_cast<const __nv_bfloat16 *>(a.x) + max(row, 0) * a.x_ld + 8 * t +
                    now.stage * kSpan;
         }
-        // The rows' values of half a stage, loaded half a stage before they are used:
-        // they come from the L2, some 800 cycles away.
-        uint4 xv[4][NT];
+        // The rows' values of the next kAhead blocks of 32, loaded that long before they
+        // are used: they come from the L2, some 800 cycles away.
+        constexpr int kAhead = 4 / NT;
+        uint4 xv[kAhead][NT];
         auto load_x = [&](int b, int k) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-                xv[b][i] = __ldg(reinterpret_cast<const uint4 *>(x[i] + k + 32 * b));
+                xv[b % kAhead][i] = __ldg(reinterpret_cast<const uint4 *>(x[i] + k + 32 * b));
         };
         {
             const int blocks = min(kSpan, a.k - now.stage * kSpan) / 32;
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
+            for (int b = 0; b < kAhead; ++b)
                 if (b < blocks) load_x(b, 0);
         }
         // Number of the first scale of columns g + 8 i: modulo 2 and 4 it says where the
@@ -249,7 +264,7 @@ struct Gemv {
             }
             issue(ahead, (it + kStages - 1) % kStages);
             const uint8_t *wd = weights + slot * kWeightBytes + g * 128 + t * 4;
-            const uint8_t *gd = group_data + slot * kGroupBytes;
+            const uint8_t *gd = group_data + slot * G::kBytes;
             const unsigned moved = now.stage * kGroups;
             advance(now);
             // blocks of the item's next stage
@@ -276,7 +291,7 @@ struct Gemv {
                         if (a.zeros) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const uint32_t z = gd[kZeroAt + (g + 8 * i) * kZeroPitch +
+                                const uint32_t z = gd[G::kZeroAt + (g + 8 * i) * G::kZeroPitch +
                                                       ((skips[i] + moved) & 3u) + group];
                                 zero[i] = __byte_perm(z, 0x43u, 0x4040);  // 128 + z, twice
                             }
@@ -301,7 +316,7 @@ struct Gemv {
                                                {q[2][2], q[3][2], q[2][3], q[3][3]}};
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
-                        const uint4 v = xv[b][i];
+                        const uint4 v = xv[b % kAhead][i];
                         const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410);
                         const uint32_t b1 = __byte_perm(v.x, v.z, 0x7632);
                         const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410);
@@ -312,19 +327,23 @@ struct Gemv {
                             mma_16816(sum[m][i], a1[m], b2, b3);
                         }
                     }
-                    if (b < after) load_x(b, x_next);
+                    if (b + kAhead < 4) {
+                        if (b + kAhead < left) load_x(b + kAhead, 0);
+                    } else if (b + kAhead - 4 < after) {
+                        load_x(b + kAhead - 4, x_next);
+                    }
                     if (b % kPer == kPer - 1) {
                         float s[4];
-                        const uint8_t *sa = gd + g * kScalePitch;
+                        const uint8_t *sa = gd + g * G::kScalePitch;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (a.scale_fp32)
-                                s[i] = *reinterpret_cast<const float *>(sa + 8 * i * kScalePitch +
+                                s[i] = *reinterpret_cast<const float *>(sa + 8 * i * G::kScalePitch +
                                                                         4 * group);
                             else
                                 s[i] = __uint_as_float(
                                     uint32_t{*reinterpret_cast<const uint16_t *>(
-                                        sa + 8 * i * kScalePitch +
+                                        sa + 8 * i * G::kScalePitch +
                                         2 * (((skips[i] + moved) & 1u) + group))}
                                     << 16);
 #pragma unroll
@@ -353,7 +372,8 @@ struct Gemv {
                 for (int j = 0; j < 4; ++j) {
                     const int n = 16 * m + g + 8 * (j / 2);
                     const int r = 8 * i + 2 * t + j % 2;
-                    const float v = acc[m][i][j];
+                    const float v =
+                        outside[i] >> (4 * (2 * t + j % 2)) & 1u ? 0.f : acc[m][i][j];
                     if (share > 1)
                         mine[r * kCols + n] = v;
                     else if (r < d.rows && d.n0 + n < a.n)
@@ -376,15 +396,16 @@ struct Gemv {
     }
 };
 
-template <int GROUP>
+template <int GROUP, int TILES>
 __global__ void __launch_bounds__(kGemvThreads, 1)
     grouped_gemv_int4_kernel(const __grid_constant__ CUtensorMap map, const GemvArgs a,
                              const int share) {
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + (((smem_u32(raw) + 1023u) & ~1023u) - smem_u32(raw));
     uint8_t *group_data = smem + kWarps * kStages * kWeightBytes;
-    uint8_t *sums = group_data + kWarps * kStages * kGroupBytes;
-    GemvControl &c = *reinterpret_cast<GemvControl *>(sums + kWarps * kSumBytes);
+    uint8_t *sums = group_data + kWarps * kStages * GroupData<GROUP>::kBytes;
+    GemvControl &c =
+        *reinterpret_cast<GemvControl *>(sums + kWarps * GemvSmem<GROUP, TILES>::kSumBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (lane < kStages) mbar_init(smem_u32(&c.full[warp][lane]), 1);
     fence_mbar_init();
@@ -401,7 +422,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
         c.lo[e] = lo;
         if (e + 1 == a.num_experts) c.lo[e + 1] = hi;
         c.tiles[e] = sum;
-        sum += (hi - lo + kRowsPass - 1) / kRowsPass;
+        sum += (hi - lo + 8 * TILES - 1) / (8 * TILES);
     }
     int before = sum;
     for (int o = 1; o < 32; o *= 2) {
@@ -421,11 +442,11 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     __syncthreads();
 
     const int block = warp / share;
-    const int col_blocks = (a.n + kCols - 1) / kCols;
-    const int64_t item0 = blockIdx.x + int64_t{gridDim.x} * block;
+    const unsigned col_blocks = (a.n + kCols - 1) / kCols;
+    const int item0 = blockIdx.x + gridDim.x * block;
     uint8_t *weights = smem + warp * (kStages * kWeightBytes);
-    uint8_t *groups = group_data + warp * (kStages * kGroupBytes);
-    const Gemv<GROUP> k{a,
+    uint8_t *groups = group_data + warp * (kStages * GroupData<GROUP>::kBytes);
+    const Gemv<GROUP, TILES> k{a,
                         map,
                         c,
                         lane,
@@ -433,8 +454,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
                         lane % 4,
                         share,
                         warp % share,
-                        int64_t{gridDim.x} * (kWarps / share),
-                        int64_t{total} * col_blocks,
+                        static_cast<int>(gridDim.x) * (kWarps / share),
+                        total * static_cast<int>(col_blocks),
                         col_blocks,
                         (a.k + kSpan - 1) / kSpan,
                         a.k / GROUP,
@@ -444,8 +465,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
                         smem_u32(weights),
                         smem_u32(groups),
                         smem_u32(&c.full[warp][0]),
-                        reinterpret_cast<float *>(sums) + block * share * (kCols * kRowsPass),
-                        1 + block};
+                        reinterpret_cast<float *>(sums) + block * share * (kCols * 8 * TILES),
+                        block};
     Cursor now{item0, k.part, 0, 0, 0, 0};
     k.locate(now);
     Copies ahead{item0, k.part, 0, 0, 0};
@@ -454,10 +475,10 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     uint32_t it = 0;
     uint64_t limit = a.timeout_ns;
     while (now.item < k.items) {
-        if (now.rows <= 8)
+        if (TILES == 1 || now.rows <= 8)
             k.template item<1>(now, ahead, it, limit);
         else
-            k.template item<2>(now, ahead, it, limit);
+            k.template item<TILES>(now, ahead, it, limit);
     }
     if (limit == 0)  // copies may still be in flight: wait once more before the memory goes
         for (uint32_t s = 1; s <= kStages && s <= it; ++s)
@@ -465,7 +486,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     cp_async_wait<0>();
 }
 
-template <int GROUP>
+template <int GROUP, int TILES>
 cudaError_t launch(const GemvArgs &a, cudaStream_t s) {
     CUtensorMap map;
     const cuuint64_t row = static_cast<cuuint64_t>(a.k) / 2;
@@ -474,42 +495,58 @@ cudaError_t launch(const GemvArgs &a, cudaStream_t s) {
                     {row, row * a.n}, kSpan / 2, kCols))
         return cudaErrorInvalidValue;
     // Warps to a column block: as many as make the longest warp's work shortest,
-    // counted in stages (the experts' sizes are known on the device only: at most
-    // this many blocks).
+    // counted in stages, a block's beginning and end as two (the experts' sizes are
+    // known on the device only: at most this many blocks).
     const int64_t blocks = (a.n + kCols - 1) / kCols *
-                           (a.rows / kRowsPass + min(int64_t{a.num_experts}, a.rows));
+                           (a.rows / (8 * TILES) + min(int64_t{a.num_experts}, a.rows));
     const int spans = (a.k + kSpan - 1) / kSpan;
     int share = 1;
     int64_t best = INT64_MAX;
-    for (int w : {1, 2, 3, 4, 6, 12}) {
+    for (int w = 1; w <= kWarps; w *= 2) {
         if (w > spans) break;
         const int64_t at_once = int64_t{a.num_sms} * (kWarps / w);
-        const int64_t cost = (blocks + at_once - 1) / at_once * ((spans + w - 1) / w);
+        const int64_t cost = (blocks + at_once - 1) / at_once * ((spans + w - 1) / w + 2);
         if (cost < best) {
             best = cost;
             share = w;
         }
     }
-    return launch_ex(grouped_gemv_int4_kernel<GROUP>,
+    // work items are counted in 32 bits (a buffer of so many results does not fit)
+    if (blocks > INT32_MAX - int64_t{a.num_sms} * kWarps) return cudaErrorInvalidValue;
+    return launch_ex(grouped_gemv_int4_kernel<GROUP, TILES>,
                      dim3(static_cast<unsigned>(min(blocks, int64_t{a.num_sms}))),
-                     dim3(kGemvThreads), kGemvSmem, s, 1, a.programmatic, map, a, share);
+                     dim3(kGemvThreads), GemvSmem<GROUP, TILES>::kBytes, s, 1, a.programmatic, map, a, share);
+}
+
+template <int GROUP>
+cudaError_t launch_group(const GemvArgs &a, cudaStream_t s) {
+    // More than five rows an expert on average: passes of 16 rows.
+    return a.rows > 5 * int64_t{a.num_experts} ? launch<GROUP, 2>(a, s) : launch<GROUP, 1>(a, s);
+}
+
+template <int GROUP>
+cudaError_t prepare() {
+    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    const cudaError_t e = cudaFuncSetAttribute(grouped_gemv_int4_kernel<GROUP, 1>, attr,
+                                               GemvSmem<GROUP, 1>::kBytes);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(grouped_gemv_int4_kernel<GROUP, 2>, attr,
+                                                   GemvSmem<GROUP, 2>::kBytes);
 }
 
 }  // namespace
 
 cudaError_t prepare_grouped_gemv() {
-    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(grouped_gemv_int4_kernel<32>, attr, kGemvSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemv_int4_kernel<64>, attr, kGemvSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemv_int4_kernel<128>, attr, kGemvSmem);
-    return e;
+    cudaError_t e = prepare<32>();
+    if (e == cudaSuccess) e = prepare<64>();
+    return e == cudaSuccess ? prepare<128>() : e;
 }
 
 cudaError_t launch_grouped_gemv_int4(const GemvArgs &a, cudaStream_t s) {
     switch (a.group) {
-        case 32: return launch<32>(a, s);
-        case 64: return launch<64>(a, s);
-        default: return launch<128>(a, s);
+        case 32: return launch_group<32>(a, s);
+        case 64: return launch_group<64>(a, s);
+        default: return launch_group<128>(a, s);
     }
 }
 
