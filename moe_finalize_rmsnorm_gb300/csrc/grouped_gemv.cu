@@ -3,14 +3,12 @@
 // Bound by the weights' bytes: each is read once for every 16 rows of its
 // expert.  A warp takes 32 columns n and up to 16 rows.  It streams 256 summed
 // values of its 32 columns a stage (128 bytes a column) through its own ring in
-// shared memory, one tensor-map copy a stage, turns the nibbles into BF16 integers
-// q - z (exact), and multiplies with the rows in mma.m16n8k16, n along M, the rows
+// shared memory, one tensor-map copy a stage, turns the nibbles into (q - z) / 64 in
+// BF16 (exact), and multiplies with the rows in mma.m16n8k16, n along M, the rows
 // along N: with so few rows the tensor cores only have to keep up with the
-// conversion.  Each group's FP32 sum is scaled once.  Warps that share a column
+// conversion.  Each group's FP32 sum is scaled once (and by 64 at the end).  Warps that share a column
 // block split the summed values between them and add up through shared memory, in
 // warp order.
-#include <string.h>
-
 #include "experts.cuh"
 #include "experts.h"
 #include "tensor_map.h"
@@ -67,20 +65,16 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// (a & b) | c in one instruction (written out: two constants otherwise cost two).
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+// a * b + c on two BF16, one rounding.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
 
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-    __nv_bfloat162 x, y;
-    memcpy(&x, &a, 4);
-    memcpy(&y, &b, 4);
-    x = __hsub2(x, y);
-    memcpy(&a, &x, 4);
-    return a;
+template <typename T>
+__device__ __forceinline__ T lds(uint32_t addr) {
+    return *reinterpret_cast<const T *>(__cvta_shared_to_generic(addr));
 }
 
 // Where a warp is in its sequence of (column block, stage) pairs.
@@ -114,9 +108,7 @@ struct Gemv {
     const unsigned col_blocks;
     const int spans, groups;
     const int search;           // first step of the search for an expert
-    const uint8_t *weights;     // this warp's stages
-    const uint8_t *group_data;
-    const uint32_t weights_at, group_at, full;
+    const uint32_t weights_at, group_at, full;  // this warp's stages and barriers
     float *sums;  // of the block's first warp
     const int barrier;
 
@@ -246,13 +238,10 @@ struct Gemv {
             for (int b = 0; b < kAhead; ++b)
                 if (b < blocks) load_x(b, 0);
         }
-        // Number of the first scale of columns g + 8 i: modulo 2 and 4 it says where the
-        // copied words hold the scale and the zero.
-        unsigned skips[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            skips[i] = static_cast<unsigned>(
-                (int64_t{d.expert} * a.n + min(d.n0 + g + 8 * i, a.n - 1)) * groups);
+        // Number of the first scale of column g (those of columns g + 8 i differ by
+        // multiples of 8): modulo 2 and 4 it says where the copied words hold the scales
+        // and the zeros.  A stage moves it by an even number.
+        const unsigned skip = static_cast<unsigned>((int64_t{d.expert} * a.n + d.n0 + g) * groups);
         float acc[2][NT][4] = {};
         while (now.item == d.item) {
             const int blocks = min(kSpan, a.k - now.stage * kSpan) / 32;
@@ -263,9 +252,11 @@ struct Gemv {
                 if (lane == 0) atomicOr(a.status, kStatusWaitTimeout);
             }
             issue(ahead, (it + kStages - 1) % kStages);
-            const uint8_t *wd = weights + slot * kWeightBytes + g * 128 + t * 4;
-            const uint8_t *gd = group_data + slot * G::kBytes;
-            const unsigned moved = now.stage * kGroups;
+            const uint32_t wd = weights_at + slot * kWeightBytes + g * 128 + t * 4 + (g << 4);
+            const uint32_t gd = group_at + slot * G::kBytes;
+            const uint32_t sd = gd + g * G::kScalePitch + (a.scale_fp32 ? 0 : (skip & 1u) * 2);
+            const uint32_t zd =
+                gd + G::kZeroAt + g * G::kZeroPitch + ((skip + now.stage * kGroups) & 3u);
             advance(now);
             // blocks of the item's next stage
             const int next = now.item == d.item ? min(kSpan, a.k - now.stage * kSpan) / 32 : 0;
@@ -274,8 +265,10 @@ struct Gemv {
                 const int left = blocks - 4 * half;  // blocks from here on
                 const int after = half ? next : blocks - 4;
                 const int x_next = half ? share * kSpan - 128 : 128;
+                const uint32_t wh = wd ^ half << 6;
                 float sum[2][NT][4];
-                uint32_t zero[4] = {0x43084308u, 0x43084308u, 0x43084308u, 0x43084308u};
+                // minus the zero, in 64ths
+                uint32_t zero[4] = {0xBE00BE00u, 0xBE00BE00u, 0xBE00BE00u, 0xBE00BE00u};
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     if (b >= left) break;
@@ -291,23 +284,25 @@ struct Gemv {
                         if (a.zeros) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const uint32_t z = gd[G::kZeroAt + (g + 8 * i) * G::kZeroPitch +
-                                                      ((skips[i] + moved) & 3u) + group];
-                                zero[i] = __byte_perm(z, 0x43u, 0x4040);  // 128 + z, twice
+                                const float z = lds<uint8_t>(zd + 8 * i * G::kZeroPitch + group);
+                                const float m = z * -0.015625f;
+                                zero[i] = pack2_rn(m, m);
                             }
                         }
                     }
-                    // 0x4300 | q is 128 + q in BF16; minus 128 + z is exact.  The copy's
+                    // A nibble in the low byte of a BF16 is 2^-133 (or 16 times that) times
+                    // its value, linear through the subnormals and the first binade, so one
+                    // multiply-add by 2^127 (2^123) gives (q - z) / 64, exact.  The copy's
                     // swizzle keeps the eight columns' words in different banks.
                     uint32_t q[4][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t w = *reinterpret_cast<const uint32_t *>(
-                            wd + 1024 * i + (((4 * half + b) ^ g) << 4));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            q[i][j] =
-                                sub_bf16x2(and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u), zero[i]);
+                        const uint32_t w = lds<uint32_t>((wh ^ b << 4) + 1024 * i);
+                        const uint32_t v = w >> 8;
+                        q[i][0] = fma_bf16x2(w & 0x000F000Fu, 0x7F007F00u, zero[i]);
+                        q[i][1] = fma_bf16x2(w & 0x00F000F0u, 0x7D007D00u, zero[i]);
+                        q[i][2] = fma_bf16x2(v & 0x000F000Fu, 0x7F007F00u, zero[i]);
+                        q[i][3] = fma_bf16x2(v & 0x00F000F0u, 0x7D007D00u, zero[i]);
                     }
                     // q[.][j] holds summed values j and j + 4 of the thread's eight
                     const uint32_t a0[2][4] = {{q[0][0], q[1][0], q[0][1], q[1][1]},
@@ -334,18 +329,13 @@ struct Gemv {
                     }
                     if (b % kPer == kPer - 1) {
                         float s[4];
-                        const uint8_t *sa = gd + g * G::kScalePitch;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (a.scale_fp32)
-                                s[i] = *reinterpret_cast<const float *>(sa + 8 * i * G::kScalePitch +
-                                                                        4 * group);
-                            else
-                                s[i] = __uint_as_float(
-                                    uint32_t{*reinterpret_cast<const uint16_t *>(
-                                        sa + 8 * i * G::kScalePitch +
-                                        2 * (((skips[i] + moved) & 1u) + group))}
-                                    << 16);
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t at = sd + 8 * i * G::kScalePitch;
+                            s[i] = a.scale_fp32
+                                       ? lds<float>(at + 4 * group)
+                                       : __uint_as_float(uint32_t{lds<uint16_t>(at + 2 * group)} << 16);
+                        }
 #pragma unroll
                         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -373,7 +363,7 @@ struct Gemv {
                     const int n = 16 * m + g + 8 * (j / 2);
                     const int r = 8 * i + 2 * t + j % 2;
                     const float v =
-                        outside[i] >> (4 * (2 * t + j % 2)) & 1u ? 0.f : acc[m][i][j];
+                        outside[i] >> (4 * (2 * t + j % 2)) & 1u ? 0.f : 64.f * acc[m][i][j];
                     if (share > 1)
                         mine[r * kCols + n] = v;
                     else if (r < d.rows && d.n0 + n < a.n)
@@ -444,8 +434,6 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     const int block = warp / share;
     const unsigned col_blocks = (a.n + kCols - 1) / kCols;
     const int item0 = blockIdx.x + gridDim.x * block;
-    uint8_t *weights = smem + warp * (kStages * kWeightBytes);
-    uint8_t *groups = group_data + warp * (kStages * GroupData<GROUP>::kBytes);
     const Gemv<GROUP, TILES> k{a,
                         map,
                         c,
@@ -460,10 +448,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
                         (a.k + kSpan - 1) / kSpan,
                         a.k / GROUP,
                         1 << (31 - __clz(a.num_experts)),
-                        weights,
-                        groups,
-                        smem_u32(weights),
-                        smem_u32(groups),
+                        smem_u32(smem) + warp * (kStages * kWeightBytes),
+                        smem_u32(group_data) + warp * (kStages * GroupData<GROUP>::kBytes),
                         smem_u32(&c.full[warp][0]),
                         reinterpret_cast<float *>(sums) + block * share * (kCols * 8 * TILES),
                         block};
