@@ -65,6 +65,15 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same with nothing to add to.
+__device__ __forceinline__ void mma_16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // a * b + c on two BF16, one rounding.
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
@@ -267,27 +276,18 @@ struct Gemv {
                 const int x_next = half ? share * kSpan - 128 : 128;
                 const uint32_t wh = wd ^ half << 6;
                 float sum[2][NT][4];
-                // minus the zero, in 64ths
+                // minus the zero, in 64ths (made as the nibbles are)
                 uint32_t zero[4] = {0xBE00BE00u, 0xBE00BE00u, 0xBE00BE00u, 0xBE00BE00u};
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     if (b >= left) break;
                     constexpr int kPer = GROUP / 32;  // blocks of a group
                     const int group = (4 * half + b) / kPer;
-                    if (b % kPer == 0) {
+                    if (b % kPer == 0 && a.zeros) {
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) sum[m][i][j] = 0.f;
-                        if (a.zeros) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float z = lds<uint8_t>(zd + 8 * i * G::kZeroPitch + group);
-                                const float m = z * -0.015625f;
-                                zero[i] = pack2_rn(m, m);
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t z = lds<uint8_t>(zd + 8 * i * G::kZeroPitch + group);
+                            zero[i] = fma_bf16x2(__byte_perm(z, 0, 0x4040), 0xFF00FF00u, 0);
                         }
                     }
                     // A nibble in the low byte of a BF16 is 2^-133 (or 16 times that) times
@@ -318,7 +318,10 @@ struct Gemv {
                         const uint32_t b3 = __byte_perm(v.y, v.w, 0x7632);
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
-                            mma_16816(sum[m][i], a0[m], b0, b1);
+                            if (b % kPer == 0)
+                                mma_16816_first(sum[m][i], a0[m], b0, b1);
+                            else
+                                mma_16816(sum[m][i], a0[m], b0, b1);
                             mma_16816(sum[m][i], a1[m], b2, b3);
                         }
                     }
