@@ -4,9 +4,17 @@ from __future__ import annotations
 import torch
 
 
+# The current stream's handle, without a Stream object around it (0.1 against 2 us
+# on the host, of some 10 a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_ptr(stream, device) -> int:
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _on_device(dev: torch.device, fn, *args) -> int:

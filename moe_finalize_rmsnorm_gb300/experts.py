@@ -23,37 +23,46 @@ read on the host.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
+
 import torch
 
 from ._abi import MF_DTYPE_BF16, MF_DTYPE_FP32, check, lib
 from ._binding import _on_device, _req, _stream_ptr
 
 _BF16 = torch.bfloat16
+_ROW_DTYPES = (torch.bfloat16,)
 _VALUE_DTYPES = {torch.bfloat16: MF_DTYPE_BF16, torch.float32: MF_DTYPE_FP32}
 
 
-def _rows(t: torch.Tensor, name: str, dtypes=(_BF16,)) -> int:
+def _rows(t: torch.Tensor, name: str, dtypes=_ROW_DTYPES) -> int:
     """Check a 2-D row-major operand; returns its row stride in elements."""
-    _req(t.dim() == 2 and t.dtype in dtypes and (t.stride(1) == 1 or t.shape[1] <= 1),
-         f"{name} must be a 2-D tensor of {' or '.join(str(d) for d in dtypes)} with unit "
-         "last-dim stride")
+    if t.dim() != 2 or t.dtype not in dtypes or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a 2-D tensor of {' or '.join(map(str, dtypes))} with "
+                         "unit last-dim stride")
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]  # one row: no stride to keep
 
 
 def _output_rows(t: torch.Tensor, name: str) -> int:
-    ld = _rows(t, name, tuple(_VALUE_DTYPES))
-    _req(t.shape[0] <= 1 or ld >= t.shape[1], f"{name}'s rows must not overlap")
+    ld = _rows(t, name, _VALUE_DTYPES)
+    if t.shape[0] > 1 and ld < t.shape[1]:
+        raise ValueError(f"{name}'s rows must not overlap")
     return ld
 
 
-def _index(t: torch.Tensor, name: str, shape) -> None:
-    _req(t.dtype == torch.int32 and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-         f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+def _index(t: torch.Tensor, name: str, shape: tuple) -> None:
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
 
 
 def _same_device(dev: torch.device, *tensors) -> None:
-    _req(dev.type == "cuda" and all(t is None or t.device == dev for t in tensors),
-         "all tensors must be on the same CUDA device")
+    if dev.type == "cuda":
+        for t in tensors:
+            if t is not None and t.device != dev:
+                break
+        else:
+            return
+    raise ValueError("all tensors must be on the same CUDA device")
 
 
 def _ptr(t):
@@ -80,20 +89,26 @@ def moe_expert_permutation(expert_ids: torch.Tensor, num_experts: int, *, packed
     dev = expert_ids.device
     T, K = expert_ids.shape
     num_experts = int(num_experts)
-    given = (expert_offsets, expanded_idx, row_tokens)
-    _same_device(dev, *given)
-    shapes = ((max(num_experts, 0) + 1,), (T, K), (T * K,))
-    for t, shape, name in zip(given, shapes, ("expert_offsets", "expanded_idx", "row_tokens")):
-        if t is not None:
-            _index(t, name, shape)
+    _same_device(dev, expert_offsets, expanded_idx, row_tokens)
+    if expert_offsets is not None:
+        _index(expert_offsets, "expert_offsets", (num_experts + 1,))
+    if expanded_idx is not None:
+        _index(expanded_idx, "expanded_idx", (T, K))
+    if row_tokens is not None:
+        _index(row_tokens, "row_tokens", (T * K,))
     # memory allocated here belongs to the stream that writes it
-    with torch.cuda.stream(torch.cuda.current_stream(dev) if stream is None else stream):
-        out = tuple(torch.empty(shape, dtype=torch.int32, device=dev) if t is None else t
-                    for t, shape in zip(given, shapes))
+    with nullcontext() if stream is None else torch.cuda.stream(stream):
+        if expert_offsets is None:
+            expert_offsets = torch.empty(max(num_experts, 0) + 1, dtype=torch.int32, device=dev)
+        if expanded_idx is None:
+            expanded_idx = torch.empty((T, K), dtype=torch.int32, device=dev)
+        if row_tokens is None:
+            row_tokens = torch.empty(T * K, dtype=torch.int32, device=dev)
     st = _on_device(dev, lib().moe_expert_permutation, expert_ids.data_ptr(), int(bool(packed)),
-                    T, K, num_experts, *(t.data_ptr() for t in out), _stream_ptr(stream, dev))
+                    T, K, num_experts, expert_offsets.data_ptr(), expanded_idx.data_ptr(),
+                    row_tokens.data_ptr(), _stream_ptr(stream, dev))
     check(st, "moe_expert_permutation")
-    return out
+    return expert_offsets, expanded_idx, row_tokens
 
 
 def moe_permuted_row_sum(permuted: torch.Tensor, expanded_idx: torch.Tensor, output: torch.Tensor,
