@@ -45,12 +45,12 @@ struct Shape {
 
 // Shared memory behind the stages and the epilogue's blocks.
 struct Control {
+    int4 list[256];              // rows by number, four a copy; a part for each stage
     uint64_t full[6], empty[6], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int scan[8];
     int tiles[kMaxExperts + 1];  // row tiles of the experts before this one
-    int lo[kMaxExperts];
-    int rows[kMaxExperts];
+    int lo[kMaxExperts + 1];     // first row; the next expert's is the end
 };
 
 constexpr int kSmemBytes = 1024 + 192 * 1024 + kEpilogueBytes + sizeof(Control);
@@ -87,7 +87,7 @@ __device__ __forceinline__ Tile tile_of(const GroupedArgs &a, const Control &c, 
         r.m0 = local % mt * M;
         r.row0 = local / mt * kRowsMax;
         r.nrows = min(kRowsMax, a.n - r.row0);
-        r.summed = c.rows[r.expert];
+        r.summed = max(c.lo[r.expert + 1] - c.lo[r.expert], 0);
         r.sum0 = c.lo[r.expert];
     } else {
         const int u = static_cast<int>(t / mt);
@@ -95,7 +95,7 @@ __device__ __forceinline__ Tile tile_of(const GroupedArgs &a, const Control &c, 
         for (int step = 512; step > 0; step /= 2)
             if (e + step < a.num_experts && c.tiles[e + step] <= u) e += step;
         r.expert = e;
-        const int rows = c.rows[e];
+        const int rows = c.lo[e + 1] - c.lo[e];
         const int rt = c.tiles[e + 1] - c.tiles[e];
         const int local = static_cast<int>(t - c.tiles[e] * int64_t{mt});
         const int each = round_up((rows + rt - 1) / rt, 16);
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(GATHER ? Shape<CTAS>::kGatherThreads : kThread
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(full + 8 * i, GATHER ? 1 + CTAS : 1);
+            mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(GATHER ? Shape<CTAS>::kGatherThreads : kThread
         int lo, hi;
         expert_rows(a.offsets, e, static_cast<int>(a.rows), lo, hi);
         c.lo[e] = lo;
-        c.rows[e] = hi - lo;
+        if (e + 1 == a.num_experts) c.lo[e + 1] = hi;
         c.tiles[e] = sum;
         sum += (hi - lo + kRowsMax - 1) / kRowsMax;
     }
@@ -192,10 +192,9 @@ __global__ void __launch_bounds__(GATHER ? Shape<CTAS>::kGatherThreads : kThread
             const int half = d.n / CTAS;               // B rows of this CTA
             const int b0 = d.row0 + rank * half;
             const int m0 = d.m0 + rank * 128;
-            // gathered rows are not counted in bytes
-            const uint32_t a_bytes = KIND == kWgrad && GATHER ? 0 : kABytes;
+            const uint32_t a_bytes = kABytes;
             const uint32_t b_bytes = KIND == kWgrad ? round_up(half, 64) * kStep * 2
-                                     : GATHER       ? 0
+                                     : GATHER       ? half * kStep * 2
                                                     : round_up(half, 32) * kStep * 2;
             for (int s = 0; s < d.steps; ++s, ++it) {
                 const uint32_t stage = it % S::kStages, phase = it / S::kStages & 1;
@@ -281,21 +280,17 @@ __global__ void __launch_bounds__(GATHER ? Shape<CTAS>::kGatherThreads : kThread
         }
         if (!ok && lane == 0) atomicOr(a.status, kStatusWaitTimeout);
     } else if (GATHER && warp >= 8) {
-        // Rows of x chosen by row_index: 16-byte cp.async copies, eight lanes to a
-        // row's 128 bytes, into the swizzled layout that the block copies give.  One
-        // warp per stage: it issues a step's copies, waits for them, makes them
-        // visible to the tensor cores and hands the stage over, while the other
-        // warps' copies are in flight.  (Tensor-map row gathers took some 40 cycles
-        // per four rows, 1.4x the time of the whole step; and one group of warps
-        // with several steps in flight waits for all of them at the proxy fence.)
-        constexpr int kLists = KIND == kWgrad ? 2 : 8 / CTAS;  // of 32 rows
-        const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x);
+        // Rows of x chosen by row_index, four a copy (-1, no such row, arrives as
+        // zeros), one warp per stage: a warp issues one copy in some 80 cycles, and a
+        // stage takes 32 of them in 512.  Two warps for all stages: 1321 us for a
+        // prefill of 32768 rows at 4096 x 4096, one per stage: 751; 16-byte cp.async by
+        // one warp per stage: 997 (the proxy fence waits for the copies).
+        // The numbers go through shared memory, so that the elected lane reads them with
+        // uniform addresses.
         const uint32_t stage = warp - 8;
-        const uint32_t full_at = (PAIR ? map_to_cta(full, 0) : full) + 8 * stage;
-        const int chunk = lane % 8, r0 = lane / 8;  // rows r0 + 4 j
-        const uint32_t swizzle[2] = {static_cast<uint32_t>((chunk ^ r0) << 4),
-                                     static_cast<uint32_t>((chunk ^ (r0 + 4)) << 4)};
-        const uint32_t dst = base + stage * S::kStageBytes + (KIND == kWgrad ? 0 : kABytes) + r0 * 128;
+        const uint32_t bar = (PAIR ? map_to_cta(full, 0) : full) + 8 * stage;
+        int4 *list = c.list + stage * (64 / CTAS);
+        const uint32_t dst = base + stage * S::kStageBytes + (KIND == kWgrad ? 0 : kABytes);
         uint32_t it = stage;   // this warp's next step, counted over the tiles
         uint32_t done = 0;     // steps of the tiles before
         bool ok = true;
@@ -308,40 +303,36 @@ __global__ void __launch_bounds__(GATHER ? Shape<CTAS>::kGatherThreads : kThread
                 const int v = i < row_end ? __ldg(a.row_index + i) : -1;
                 return v >= 0 && v < a.x_rows ? v : -1;
             };
-            int rows[kLists];
-            if (KIND != kWgrad && it < done + d.steps)
-#pragma unroll
-                for (int i = 0; i < kLists; ++i)
-                    rows[i] = x_row(d.row0 + rank * half + 32 * i + lane);
+            if (KIND != kWgrad && it < done + d.steps) {
+                for (int i = lane; i < half; i += 32)
+                    reinterpret_cast<int *>(list)[i] = x_row(d.row0 + rank * half + i);
+                __syncwarp();
+            }
             for (; it < done + d.steps; it += S::kStages) {
                 const int c0 = static_cast<int>(it - done) * kStep;
-                if (KIND == kWgrad)
-#pragma unroll
-                    for (int i = 0; i < kLists; ++i) rows[i] = x_row(d.sum0 + c0 + 32 * i + lane);
+                if (KIND == kWgrad) {
+                    for (int i = lane; i < 64; i += 32)
+                        reinterpret_cast<int *>(list)[i] = x_row(d.sum0 + c0 + i);
+                    __syncwarp();
+                }
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(empty + 8 * stage, (it / S::kStages & 1) ^ 1, a.timeout_ns));
                 if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < kLists; ++i) {
-                    if (KIND != kWgrad && 32 * i >= half) break;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int row = __shfl_sync(0xffffffffu, rows[i], r0 + 4 * j);
-                        const int64_t from = static_cast<int64_t>(row) * a.x_ld;
-#pragma unroll
-                        for (int h = 0; h < (KIND == kWgrad ? 2 : 1); ++h) {
-                            const int col = (KIND == kWgrad ? m0 + 64 * h : c0) + 8 * chunk;
-                            const bool in = row >= 0 && col < a.k;
-                            cp_async_16(dst + h * 8192 + i * 4096 + j * 512 + swizzle[j & 1],
-                                        in ? x + from + col : x, in);
+                if (elect_one()) {
+                    if (KIND == kForward) {
+#pragma unroll 8
+                        for (int q = 0; q < half / 4; ++q)
+                            tma_gather4<PAIR>(dst + q * 512, &maps.b4, c0, list[q], bar);
+                    } else {
+#pragma unroll 8
+                        for (int q = 0; q < 16; ++q) {
+                            const int4 r = list[q];
+                            tma_gather4<PAIR>(dst + q * 512, &maps.a4, m0, r, bar);
+                            tma_gather4<PAIR>(dst + 8192 + q * 512, &maps.a4, m0 + 64, r, bar);
                         }
                     }
                 }
-                cp_async_commit();
-                cp_async_wait<0>();
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(full_at);
             }
             done += d.steps;
         }
@@ -527,6 +518,7 @@ cudaError_t launch_ctas(const GroupedArgs &a, cudaStream_t s) {
         ok = encode(&m.a, a.w, 3, {k, n, E}, {a.w_ld, a.w_expert}, a.kind == kForward ? 128 : 64);
     if (a.kind == kForward) {
         ok = ok && encode(&m.b, a.x, 2, {k, xr, 1}, {a.x_ld, 0}, 32);
+        ok = ok && encode(&m.b4, a.x, 2, {k, xr, 1}, {a.x_ld, 0}, 1);
     } else if (a.kind == kDgrad) {
         ok = ok && encode(&m.b, a.dy, 2, {n, rows, 1}, {a.dy_ld, 0}, 32);
     } else {
