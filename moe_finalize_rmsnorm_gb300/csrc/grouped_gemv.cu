@@ -29,7 +29,7 @@ template <int GROUP>
 struct GroupData {
     static constexpr int kGroups = kSpan / GROUP;
     static constexpr int kScalePitch = 4 * kGroups;
-    static constexpr int kZeroPitch = (kGroups + 6) / 4 * 4;
+    static constexpr int kZeroPitch = kGroups == 8 ? 16 : 8;
     static constexpr int kZeroAt = kCols * kScalePitch;
     static constexpr int kBytes = kZeroAt + kCols * kZeroPitch;
 };
@@ -50,6 +50,13 @@ struct GemvSmem {
         static_cast<int>(sizeof(GemvControl));
     static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
 };
+
+// 4, 8 or 16 bytes global -> shared.
+template <int BYTES>
+__device__ __forceinline__ void cp_async_ca(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+                 : "memory");
+}
 
 // 4 bytes global -> shared, the bytes behind `bytes` (0..4) as zeros.
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src, int bytes) {
@@ -86,6 +93,24 @@ __device__ __forceinline__ T lds(uint32_t addr) {
     return *reinterpret_cast<const T *>(__cvta_shared_to_generic(addr));
 }
 
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&v)[N]) {
+    if constexpr (N == 1) {
+        v[0] = lds<uint32_t>(addr);
+    } else if constexpr (N == 2) {
+        const uint2 q = lds<uint2>(addr);
+        v[0] = q.x;
+        v[1] = q.y;
+    } else {
+        static_assert(N == 4, "");
+        const uint4 q = lds<uint4>(addr);
+        v[0] = q.x;
+        v[1] = q.y;
+        v[2] = q.z;
+        v[3] = q.w;
+    }
+}
+
 // Where a warp is in its sequence of (column block, stage) pairs.
 struct Cursor {
     int item;
@@ -101,12 +126,15 @@ struct Copies {
     int64_t o;  // number of the first scale of the lane's column in this stage
 };
 
-// TILES: a pass takes up to 8 TILES rows.
-template <int GROUP, int TILES>
+// TILES: a pass takes up to 8 TILES rows.  WHOLE: the summed values are whole
+// stages, so that a stage's scales are aligned to their size (and its zeros, where
+// a group is at most 64 long).
+template <int GROUP, int TILES, bool WHOLE>
 struct Gemv {
     using G = GroupData<GROUP>;
     static constexpr int kGroups = G::kGroups;
     static constexpr int kRowsPass = 8 * TILES;
+    static constexpr bool kWholeZeros = WHOLE && kGroups >= 4;
 
     const GemvArgs &a;
     const CUtensorMap &map;
@@ -166,13 +194,23 @@ struct Gemv {
                               p.expert, full + 8 * slot);
             }
             __syncwarp();
-            const int ng = min(kGroups, groups - p.stage * kGroups);
+            const int ng = WHOLE ? kGroups : min(kGroups, groups - p.stage * kGroups);
             const uint32_t sd = group_at + slot * G::kBytes + lane * G::kScalePitch;
+            const uint32_t zd = group_at + slot * G::kBytes + G::kZeroAt + lane * G::kZeroPitch;
             if (a.scale_fp32) {
                 const float *s = static_cast<const float *>(a.scales) + p.o;
+                if constexpr (WHOLE) {
+                    constexpr int kBytes = kGroups == 2 ? 8 : 16;
 #pragma unroll
-                for (int i = 0; i < kGroups; ++i)
-                    if (i < ng) cp_async_4(sd + 4 * i, s + i, 4);
+                    for (int i = 0; i < 4 * kGroups / kBytes; ++i)
+                        cp_async_ca<kBytes>(sd + kBytes * i, s + kBytes / 4 * i);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kGroups; ++i)
+                        if (i < ng) cp_async_4(sd + 4 * i, s + i, 4);
+                }
+            } else if constexpr (WHOLE) {
+                cp_async_ca<2 * kGroups>(sd, static_cast<const uint16_t *>(a.scales) + p.o);
             } else {
                 // the aligned words that hold the scales
                 const uint8_t *s = static_cast<const uint8_t *>(a.scales) + (p.o & ~int64_t{1}) * 2;
@@ -182,13 +220,15 @@ struct Gemv {
                     if (4 * i < bytes) cp_async_4(sd + 4 * i, s + 4 * i, min(4, bytes - 4 * i));
             }
             if (a.zeros) {
-                const uint8_t *z = a.zeros + (p.o & ~int64_t{3});
-                const int bytes = static_cast<int>(p.o & 3) + ng;
-                const uint32_t zd =
-                    group_at + slot * G::kBytes + G::kZeroAt + lane * G::kZeroPitch;
+                if constexpr (kWholeZeros) {
+                    cp_async_ca<kGroups>(zd, a.zeros + p.o);
+                } else {
+                    const uint8_t *z = a.zeros + (p.o & ~int64_t{3});
+                    const int bytes = static_cast<int>(p.o & 3) + ng;
 #pragma unroll
-                for (int i = 0; i < (kGroups + 6) / 4; ++i)
-                    if (4 * i < bytes) cp_async_4(zd + 4 * i, z + 4 * i, min(4, bytes - 4 * i));
+                    for (int i = 0; i < (kGroups + 6) / 4; ++i)
+                        if (4 * i < bytes) cp_async_4(zd + 4 * i, z + 4 * i, min(4, bytes - 4 * i));
+                }
             }
             p.stage += share;
             p.o += share * kGroups;
@@ -242,7 +282,7 @@ struct Gemv {
                 xv[b % kAhead][i] = __ldg(reinterpret_cast<const uint4 *>(x[i] + k + 32 * b));
         };
         {
-            const int blocks = min(kSpan, a.k - now.stage * kSpan) / 32;
+            const int blocks = WHOLE ? 8 : min(kSpan, a.k - now.stage * kSpan) / 32;
 #pragma unroll
             for (int b = 0; b < kAhead; ++b)
                 if (b < blocks) load_x(b, 0);
@@ -253,7 +293,7 @@ struct Gemv {
         const unsigned skip = static_cast<unsigned>((int64_t{d.expert} * a.n + d.n0 + g) * groups);
         float acc[2][NT][4] = {};
         while (now.item == d.item) {
-            const int blocks = min(kSpan, a.k - now.stage * kSpan) / 32;
+            const int blocks = WHOLE ? 8 : min(kSpan, a.k - now.stage * kSpan) / 32;
             const uint32_t slot = it % kStages;
             cp_async_wait<kStages - 2>();
             if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * slot, it / kStages & 1, limit))) {
@@ -263,16 +303,50 @@ struct Gemv {
             issue(ahead, (it + kStages - 1) % kStages);
             const uint32_t wd = weights_at + slot * kWeightBytes + g * 128 + t * 4 + (g << 4);
             const uint32_t gd = group_at + slot * G::kBytes;
-            const uint32_t sd = gd + g * G::kScalePitch + (a.scale_fp32 ? 0 : (skip & 1u) * 2);
-            const uint32_t zd =
-                gd + G::kZeroAt + g * G::kZeroPitch + ((skip + now.stage * kGroups) & 3u);
+            const uint32_t sd =
+                gd + g * G::kScalePitch + (WHOLE || a.scale_fp32 ? 0 : (skip & 1u) * 2);
+            const uint32_t zd = gd + G::kZeroAt + g * G::kZeroPitch +
+                                (kWholeZeros ? 0 : (skip + now.stage * kGroups) & 3u);
             advance(now);
             // blocks of the item's next stage
-            const int next = now.item == d.item ? min(kSpan, a.k - now.stage * kSpan) / 32 : 0;
+            const int next = now.item != d.item ? 0
+                             : WHOLE            ? 8
+                                                : min(kSpan, a.k - now.stage * kSpan) / 32;
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-                const int left = blocks - 4 * half;  // blocks from here on
+                const int left = WHOLE ? 4 : blocks - 4 * half;  // blocks from here on
                 const int after = half ? next : blocks - 4;
+                // the scales and zeros of the half's groups, as they lie in memory
+                constexpr int kHere = kGroups / 2;
+                constexpr int kPer = GROUP / 32;  // blocks of a group
+                uint32_t sv[4][kHere], zv[4];
+                if constexpr (WHOLE) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t at = sd + 8 * i * G::kScalePitch;
+                        if (a.scale_fp32) {
+                            lds_words<kHere>(at + 4 * kHere * half, sv[i]);
+                        } else if constexpr (kHere == 1) {
+                            sv[i][0] = uint32_t{lds<uint16_t>(at + 2 * half)} << 16;
+                        } else {
+                            uint32_t two[kHere / 2];
+                            lds_words<kHere / 2>(at + 2 * kHere * half, two);
+#pragma unroll
+                            for (int j = 0; j < kHere; ++j)
+                                sv[i][j] = j & 1 ? two[j / 2] & 0xFFFF0000u : two[j / 2] << 16;
+                        }
+                    }
+                }
+                if (kWholeZeros && a.zeros) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t at = zd + 8 * i * G::kZeroPitch + kHere * half;
+                        if constexpr (kHere == 4)
+                            zv[i] = lds<uint32_t>(at);
+                        else
+                            zv[i] = lds<uint16_t>(at);
+                    }
+                }
                 const int x_next = half ? share * kSpan - 128 : 128;
                 const uint32_t wh = wd ^ half << 6;
                 float sum[2][NT][4];
@@ -281,13 +355,15 @@ struct Gemv {
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     if (b >= left) break;
-                    constexpr int kPer = GROUP / 32;  // blocks of a group
                     const int group = (4 * half + b) / kPer;
                     if (b % kPer == 0 && a.zeros) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint32_t z = lds<uint8_t>(zd + 8 * i * G::kZeroPitch + group);
-                            zero[i] = fma_bf16x2(__byte_perm(z, 0, 0x4040), 0xFF00FF00u, 0);
+                            const uint32_t z =
+                                kWholeZeros ? zv[i] : lds<uint8_t>(zd + 8 * i * G::kZeroPitch + group);
+                            const uint32_t two =
+                                __byte_perm(z, 0, 0x4040 + (kWholeZeros ? 0x0101 * (b / kPer) : 0));
+                            zero[i] = fma_bf16x2(two, 0xFF00FF00u, 0);
                         }
                     }
                     // A nibble in the low byte of a BF16 is 2^-133 (or 16 times that) times
@@ -335,7 +411,8 @@ struct Gemv {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t at = sd + 8 * i * G::kScalePitch;
-                            s[i] = a.scale_fp32
+                            s[i] = WHOLE ? __uint_as_float(sv[i][b / kPer])
+                                   : a.scale_fp32
                                        ? lds<float>(at + 4 * group)
                                        : __uint_as_float(uint32_t{lds<uint16_t>(at + 2 * group)} << 16);
                         }
@@ -389,7 +466,7 @@ struct Gemv {
     }
 };
 
-template <int GROUP, int TILES>
+template <int GROUP, int TILES, bool WHOLE>
 __global__ void __launch_bounds__(kGemvThreads, 1)
     grouped_gemv_int4_kernel(const __grid_constant__ CUtensorMap map, const GemvArgs a,
                              const int share) {
@@ -436,8 +513,13 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
 
     const int block = warp / share;
     const unsigned col_blocks = (a.n + kCols - 1) / kCols;
-    const int item0 = blockIdx.x + gridDim.x * block;
-    const Gemv<GROUP, TILES> k{a,
+    // Column blocks that lie together to one CTA's warps (they read the same rows of x),
+    // unless there are so few that this would leave CTAs without.
+    const int at_once = kWarps / share, items = total * static_cast<int>(col_blocks);
+    const int item0 = items >= 4 * static_cast<int>(gridDim.x) * at_once
+                          ? blockIdx.x * at_once + block
+                          : blockIdx.x + gridDim.x * block;
+    const Gemv<GROUP, TILES, WHOLE> k{a,
                         map,
                         c,
                         lane,
@@ -445,8 +527,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
                         lane % 4,
                         share,
                         warp % share,
-                        static_cast<int>(gridDim.x) * (kWarps / share),
-                        total * static_cast<int>(col_blocks),
+                        static_cast<int>(gridDim.x) * at_once,
+                        items,
                         col_blocks,
                         (a.k + kSpan - 1) / kSpan,
                         a.k / GROUP,
@@ -475,7 +557,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     cp_async_wait<0>();
 }
 
-template <int GROUP, int TILES>
+template <int GROUP, int TILES, bool WHOLE>
 cudaError_t launch(const GemvArgs &a, cudaStream_t s) {
     CUtensorMap map;
     const cuuint64_t row = static_cast<cuuint64_t>(a.k) / 2;
@@ -502,7 +584,7 @@ cudaError_t launch(const GemvArgs &a, cudaStream_t s) {
     }
     // work items are counted in 32 bits (a buffer of so many results does not fit)
     if (blocks > INT32_MAX - int64_t{a.num_sms} * kWarps) return cudaErrorInvalidValue;
-    return launch_ex(grouped_gemv_int4_kernel<GROUP, TILES>,
+    return launch_ex(grouped_gemv_int4_kernel<GROUP, TILES, WHOLE>,
                      dim3(static_cast<unsigned>(min(blocks, int64_t{a.num_sms}))),
                      dim3(kGemvThreads), GemvSmem<GROUP, TILES>::kBytes, s, 1, a.programmatic, map, a, share);
 }
@@ -510,25 +592,33 @@ cudaError_t launch(const GemvArgs &a, cudaStream_t s) {
 template <int GROUP>
 cudaError_t launch_group(const GemvArgs &a, cudaStream_t s) {
     // More than five rows an expert on average: passes of 16 rows.
-    return a.rows > 5 * int64_t{a.num_experts} ? launch<GROUP, 2>(a, s) : launch<GROUP, 1>(a, s);
+    const bool many = a.rows > 5 * int64_t{a.num_experts};
+    const bool whole = a.k % kSpan == 0 && reinterpret_cast<uintptr_t>(a.scales) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.zeros) % 8 == 0;
+    if (whole) return many ? launch<GROUP, 2, true>(a, s) : launch<GROUP, 1, true>(a, s);
+    return many ? launch<GROUP, 2, false>(a, s) : launch<GROUP, 1, false>(a, s);
 }
 
-template <int GROUP>
+template <int GROUP, int TILES>
 cudaError_t prepare() {
     const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    const cudaError_t e = cudaFuncSetAttribute(grouped_gemv_int4_kernel<GROUP, 1>, attr,
-                                               GemvSmem<GROUP, 1>::kBytes);
-    return e != cudaSuccess ? e
-                            : cudaFuncSetAttribute(grouped_gemv_int4_kernel<GROUP, 2>, attr,
-                                                   GemvSmem<GROUP, 2>::kBytes);
+    const int bytes = GemvSmem<GROUP, TILES>::kBytes;
+    const cudaError_t e =
+        cudaFuncSetAttribute(grouped_gemv_int4_kernel<GROUP, TILES, false>, attr, bytes);
+    return e != cudaSuccess
+               ? e
+               : cudaFuncSetAttribute(grouped_gemv_int4_kernel<GROUP, TILES, true>, attr, bytes);
 }
 
 }  // namespace
 
 cudaError_t prepare_grouped_gemv() {
-    cudaError_t e = prepare<32>();
-    if (e == cudaSuccess) e = prepare<64>();
-    return e == cudaSuccess ? prepare<128>() : e;
+    cudaError_t e = prepare<32, 1>();
+    if (e == cudaSuccess) e = prepare<32, 2>();
+    if (e == cudaSuccess) e = prepare<64, 1>();
+    if (e == cudaSuccess) e = prepare<64, 2>();
+    if (e == cudaSuccess) e = prepare<128, 1>();
+    return e == cudaSuccess ? prepare<128, 2>() : e;
 }
 
 cudaError_t launch_grouped_gemv_int4(const GemvArgs &a, cudaStream_t s) {
