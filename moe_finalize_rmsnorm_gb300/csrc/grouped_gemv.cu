@@ -88,6 +88,14 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
     return r;
 }
 
+// c += a * b on two FP32.
+__device__ __forceinline__ void fma_f32x2(float &c0, float &c1, float a, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "mov.b64 c, {%0, %1};\n\tfma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "+f"(c0), "+f"(c1)
+        : "f"(a), "f"(b0), "f"(b1));
+}
+
 template <typename T>
 __device__ __forceinline__ T lds(uint32_t addr) {
     return *reinterpret_cast<const T *>(__cvta_shared_to_generic(addr));
@@ -421,9 +429,9 @@ struct Gemv {
 #pragma unroll
                             for (int i = 0; i < NT; ++i)
 #pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    acc[m][i][j] =
-                                        fmaf(s[2 * m + j / 2], sum[m][i][j], acc[m][i][j]);
+                                for (int j = 0; j < 4; j += 2)
+                                    fma_f32x2(acc[m][i][j], acc[m][i][j + 1], s[2 * m + j / 2],
+                                              sum[m][i][j], sum[m][i][j + 1]);
                     }
                 }
 #pragma unroll
@@ -516,7 +524,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     // Column blocks that lie together to one CTA's warps (they read the same rows of x),
     // unless there are so few that this would leave CTAs without.
     const int at_once = kWarps / share, items = total * static_cast<int>(col_blocks);
-    const int item0 = items >= 4 * static_cast<int>(gridDim.x) * at_once
+    const int item0 = block >= at_once ? items  // a warp that is left over
+                      : items >= 4 * static_cast<int>(gridDim.x) * at_once
                           ? blockIdx.x * at_once + block
                           : blockIdx.x + gridDim.x * block;
     const Gemv<GROUP, TILES, WHOLE> k{a,
@@ -573,7 +582,7 @@ cudaError_t launch(const GemvArgs &a, cudaStream_t s) {
     const int spans = (a.k + kSpan - 1) / kSpan;
     int share = 1;
     int64_t best = INT64_MAX;
-    for (int w = 1; w <= kWarps; w *= 2) {
+    for (int w : {1, 2, 3, 4, 5, 8, 16}) {
         if (w > spans) break;
         const int64_t at_once = int64_t{a.num_sms} * (kWarps / w);
         const int64_t cost = (blocks + at_once - 1) / at_once * ((spans + w - 1) / w + 2);
