@@ -89,15 +89,11 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
     return remote;
 }
 
+// Arrive on a barrier of either CTA of a pair.  Release at CTA scope: what it orders
+// here are reads of TMEM, by the tcgen05 fence before it; at cluster scope it would
+// also wait for the thread's global stores to land.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
-                 : "memory");
-}
-
-// 16 bytes global -> shared, or 16 zero bytes (src is not read).
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool read) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(read ? 16u : 0u)
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
                  : "memory");
 }
 

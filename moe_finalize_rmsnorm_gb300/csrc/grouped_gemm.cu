@@ -244,11 +244,12 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
         }
         fence_mbar_init();
     }
+    // After the wait, not before: a kernel that this one waits for may want TMEM.
+    pdl_wait();
     if (warp == 2) tmem_alloc<CTAS>(smem_u32(&c.tmem), kTmemColumns);
 
     // The experts' rows and their tiles' numbers (an exclusive scan, each thread
     // a run of experts).
-    pdl_wait();
     const int per = divide_up(a.num_experts, kScanThreads);
     const int first = min(static_cast<int>(threadIdx.x) * per, a.num_experts);
     const int last = min(first + per, a.num_experts);
@@ -530,20 +531,29 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
                                                            (it / kStages & 1) ^ 1, a.timeout_ns));
                     if (!ok) break;
                     if (elect_one()) {
-                        if (KIND == kForward) {
-#pragma unroll 8
-                            for (int q = 0; q < half / (4 * W::kShare); ++q)
-                                tma_gather4<PAIR>(sb + (W::kShare * q + sub) * 512, &maps.b4, c0,
-                                                  list[q], bar);
-                        } else {
-#pragma unroll 8
-                            for (int q = 0; q < kStep / 4; ++q) {
-                                const int4 rows = list[q];
+                        // eight at a time: the numbers are read before the first copy
+                        constexpr int kBatch = 8;
+                        const int quads = KIND == kForward ? half / (4 * W::kShare) : kStep / 4;
+                        for (int q0 = 0; q0 < quads; q0 += kBatch) {
+                            int4 rows[kBatch];
 #pragma unroll
-                                for (int h = sub; h < 2; h += W::kShare)
-                                    tma_gather4<PAIR>(sa + h * 8192 + q * 512, &maps.a4, m0 + 64 * h,
-                                                      rows, bar);
+                            for (int q = 0; q < kBatch; ++q)
+                                if (q0 + q < quads) rows[q] = list[q0 + q];
+#pragma unroll
+                            for (int q = 0; q < kBatch; ++q) {
+                                if (q0 + q >= quads) break;
+                                if (KIND == kForward)
+                                    tma_gather4<PAIR>(sb + (W::kShare * (q0 + q) + sub) * 512,
+                                                      &maps.b4, c0, rows[q], bar);
+                                else
+#pragma unroll
+                                    for (int h = 0; h < 2; h += W::kShare)
+                                        tma_gather4<PAIR>(sa + (h + sub) * 8192 + (q0 + q) * 512,
+                                                          &maps.a4, m0 + 64 * (h + sub), rows[q],
+                                                          bar);
                             }
+                        }
+                        if (KIND == kWgrad) {
                             if (c0 + kStep > d.summed)
                                 dy_tail<PAIR>(maps, sb, d.sum0 + c0, row_end, b0, half, sub,
                                               W::kShare, bar);
