@@ -9,19 +9,23 @@ namespace {
 //
 // Latency bound: 12 bytes a slot move in under a microsecond even for 262144
 // slots, so what counts is the number of dependent steps.  Up to kOneCta slots one
-// CTA does everything.  Beyond, three launches: every chunk of the slots is counted
-// by a CTA, a cluster turns the counts into each chunk's first row per expert, and
-// the chunks are placed.  The counts need no workspace: a chunk is at least as long
-// as there are experts, so its counts, then its first rows, lie in its own part of
-// the slot-to-row map until its CTA has read them and writes the map itself.
+// CTA does everything (2.8 us for 256 slots).  Beyond, two launches: a cluster
+// counts the slots chunk by chunk and turns the counts into each chunk's first row
+// per expert, and a CTA for every chunk places its slots.  The first rows need no
+// workspace: a chunk is at least as long as there are experts, so they lie in its
+// own part of the slot-to-row map until its CTA has read them and writes the map
+// itself.
 
 constexpr int kPermuteThreads = 1024;
 constexpr int kPermuteWarps = kPermuteThreads / 32;
 constexpr int kOneCta = 8192;
 constexpr int kChunk = 2048;      // slots of a chunk, at least (the last up to twice as many)
 constexpr int kMaxChunks = 152;
-constexpr int kScanCtas = 8;      // the cluster of the scan
-static_assert(kChunk >= kMaxExperts, "a chunk's counts lie in its part of the map");
+// CTAs of the cluster that counts: 8, from kManySlots on 16, the largest there is
+// (64000 slots 12.0 against 13.3 us, 262144 slots 13.8 against 11.7 us).
+constexpr int kCountCtas = 8;
+constexpr int64_t kManySlots = 131072;
+static_assert(kChunk >= kMaxExperts, "a chunk's first rows lie in its part of the map");
 
 // Expert of a slot, -1 when it has none among [0, E).
 __device__ __forceinline__ int slot_expert(int word, int packed, int num_experts) {
@@ -132,81 +136,66 @@ __device__ __forceinline__ void chunk_slots(const PermuteArgs &a, int c, int chu
     end = c + 1 == chunks ? a.slots : begin + each;
 }
 
-__global__ void __launch_bounds__(kPermuteThreads) permute_count_kernel(PermuteArgs a) {
-    __shared__ int32_t counts[kMaxExperts];
-    for (int e = threadIdx.x; e < a.num_experts; e += kPermuteThreads) counts[e] = 0;
-    __syncthreads();
-    pdl_wait();
-    int64_t begin, end;
-    chunk_slots(a, blockIdx.x, gridDim.x, begin, end);
-    for (int64_t s = begin + threadIdx.x; s < end; s += kPermuteThreads) {
-        const int e = slot_expert(a.ids[s], a.packed, a.num_experts);
-        if (e >= 0) atomicAdd(counts + e, 1);
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.num_experts; e += kPermuteThreads)
-        a.slot_to_row[begin + e] = counts[e];
-}
-
-// The chunks' counts to their first rows.  Each CTA of the cluster takes a run of
-// experts, with several runs of chunks side by side.
-__global__ void __launch_bounds__(kPermuteThreads) permute_scan_kernel(PermuteArgs a, int chunks) {
-    __shared__ int32_t parts[kPermuteThreads];
-    __shared__ int32_t totals[kMaxExperts / kScanCtas];
+// Every chunk's first row per expert.  Each CTA of the cluster counts a run of
+// chunks; the CTAs read each other's sums and scan them all over the experts.
+__global__ void __launch_bounds__(kPermuteThreads) permute_count_kernel(PermuteArgs a, int chunks,
+                                                                        int ctas) {
+    extern __shared__ int32_t counts[];  // [chunks of the CTA][E]
+    __shared__ int32_t sums[kMaxExperts];
     __shared__ int32_t scratch[32];
     const int rank = static_cast<int>(cluster_ctarank());
     const int E = a.num_experts;
-    const int mine = (E + kScanCtas - 1) / kScanCtas;  // experts of a CTA
-    const int first = min(rank * mine, E), here = min(mine, E - first);
-    const int runs = min(kPermuteThreads / mine, 32);
-    const int run = threadIdx.x / mine, local = threadIdx.x % mine;
-    const int each = (chunks + runs - 1) / runs;
-    const int c0 = min(run * each, chunks), c1 = min(c0 + each, chunks);
-    const bool live = local < here && run < runs;
-    const int64_t stride = a.slots / chunks;
-    int32_t *column = a.slot_to_row + first + local;
-    pdl_wait();
-    int sum = 0;
-    if (live)
-#pragma unroll 8
-        for (int c = c0; c < c1; ++c) sum += column[c * stride];
-    parts[threadIdx.x] = sum;
+    const int c0 = chunks * rank / ctas, c1 = chunks * (rank + 1) / ctas;
+    for (int i = threadIdx.x; i < (c1 - c0) * E; i += kPermuteThreads) counts[i] = 0;
     __syncthreads();
-    if (run == 0 && local < here) {
-        int before = 0;
-        for (int r = 0; r < runs; ++r) {
-            const int v = parts[r * mine + local];
-            parts[r * mine + local] = before;
-            before += v;
+    pdl_wait();
+    const uint32_t each = static_cast<uint32_t>(a.slots / chunks);  // as chunk_slots
+    const uint32_t begin = each * c0;
+    const uint32_t end = c1 == chunks ? static_cast<uint32_t>(a.slots) : each * c1;
+    constexpr int kLoads = 8;  // in flight
+    for (uint32_t s0 = begin + threadIdx.x; s0 < end; s0 += kLoads * kPermuteThreads) {
+        int word[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            if (s0 + i * kPermuteThreads < end) word[i] = __ldg(a.ids + s0 + i * kPermuteThreads);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t s = s0 + i * kPermuteThreads;
+            if (s >= end) break;
+            const int e = slot_expert(word[i], a.packed, E);
+            const int c = min(static_cast<int>(s / each), chunks - 1);
+            if (e >= 0) atomicAdd(counts + (c - c0) * E + e, 1);
         }
-        totals[local] = before;
     }
+    __syncthreads();
+    const int e = threadIdx.x;
+    int sum = 0;
+    if (e < E)
+        for (int c = 0; c < c1 - c0; ++c) sum += counts[c * E + e];
+    sums[e] = sum;
     __syncthreads();
     cluster_barrier();
-    // every CTA scans the totals of all experts
-    int v = 0;
-    if (threadIdx.x < E)
-        v = __float_as_int(ld_dsmem_f32(smem_u32(totals + threadIdx.x % mine), threadIdx.x / mine));
-    int total;
-    const int offset = block_scan(v, scratch, total);
-    __shared__ int32_t base[kMaxExperts];
-    base[threadIdx.x] = offset;
-    __syncthreads();
-    if (rank == 0) {
-        if (threadIdx.x < E) a.offsets[threadIdx.x] = offset;
-        if (threadIdx.x == 0) a.offsets[E] = total;
-    }
-    if (live) {
-        int row = base[first + local] + parts[threadIdx.x];
+    int before = 0, all = 0;
+    if (e < E)
 #pragma unroll 8
-        for (int c = c0; c < c1; ++c) {
-            const int n = column[c * stride];
-            column[c * stride] = row;
-            row += n;
+        for (int r = 0; r < ctas; ++r) {
+            const int v = __float_as_int(ld_dsmem_f32(smem_u32(sums + e), r));
+            before += r < rank ? v : 0;
+            all += v;
         }
+    int total;
+    const int offset = block_scan(all, scratch, total);
+    if (e < E) {
+        int row = offset + before;
+        for (int c = c0; c < c1; ++c) {
+            a.slot_to_row[a.slots / chunks * c + e] = row;
+            row += counts[(c - c0) * E + e];
+        }
+        if (rank == 0) a.offsets[e] = offset;
     }
+    if (rank == 0 && e == 0) a.offsets[E] = total;
     __syncthreads();
-    cluster_barrier_exit();  // the totals are read
+    cluster_barrier_exit();  // the sums are read
 }
 
 __global__ void __launch_bounds__(kPermuteThreads) permute_place_kernel(PermuteArgs a) {
@@ -314,7 +303,13 @@ __global__ void __launch_bounds__(256) permuted_row_sum_kernel(RowSumArgs a) {
 cudaError_t prepare_permute_kernels() {
     const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
     const int bytes = kPermuteWarps * kMaxExperts * 4;
-    const cudaError_t e = cudaFuncSetAttribute(permute_one_cta_kernel, attr, bytes);
+    cudaError_t e = cudaFuncSetAttribute(permute_one_cta_kernel, attr, bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(permute_count_kernel,
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(permute_count_kernel, attr,
+                                 (kMaxChunks + kCountCtas - 1) / kCountCtas * kMaxExperts * 4);
     return e == cudaSuccess ? cudaFuncSetAttribute(permute_place_kernel, attr, bytes) : e;
 }
 
@@ -328,10 +323,10 @@ cudaError_t launch_expert_permutation(const PermuteArgs &a, cudaStream_t s) {
                          warps);
     }
     const int chunks = static_cast<int>(min(a.slots / kChunk, int64_t{kMaxChunks}));
-    cudaError_t e = launch_ex(permute_count_kernel, dim3(chunks), block, 0, s, 1, a.programmatic, a);
-    if (e == cudaSuccess)
-        e = launch_ex(permute_scan_kernel, dim3(kScanCtas), block, 0, s, kScanCtas, a.programmatic, a,
-                      chunks);
+    const int ctas = a.slots < kManySlots ? kCountCtas : 2 * kCountCtas;
+    cudaError_t e = launch_ex(permute_count_kernel, dim3(ctas), block,
+                              sizeof(int32_t) * ((chunks + ctas - 1) / ctas) * a.num_experts, s,
+                              ctas, a.programmatic, a, chunks, ctas);
     if (e == cudaSuccess)
         e = launch_ex(permute_place_kernel, dim3(chunks), block,
                       sizeof(int32_t) * kPermuteWarps * a.num_experts, s, 1, a.programmatic, a);
