@@ -120,6 +120,25 @@ def test_permutation_extremes(cuda_lib, T, K, E):
         assert torch.equal(tok.cpu(), tokens)
 
 
+@pytest.mark.parametrize("slots", [8191, 8192, 8193, 10239, 10240, 131071, 131072, 131073, 311296,
+                                   400001])
+@pytest.mark.parametrize("E", [1, 7, 1024])
+def test_permutation_at_the_edges_of_its_launches(cuda_lib, slots, E):
+    """Where one CTA hands over to several, and the chunks' and the cluster's sizes change."""
+    ids = torch.randint(-1, E + 1, (slots, 1), generator=gen(slots), dtype=torch.int32)
+    off, idx, tok = mf.moe_expert_permutation(ids.cuda(), E)
+    live = (ids >= 0) & (ids < E)
+    key = torch.where(live, ids, E).flatten()
+    order = key.argsort(stable=True).int()
+    n = int(live.sum())
+    counts = torch.bincount(key, minlength=E + 1)[:E]
+    assert torch.equal(off.cpu()[1:], counts.cumsum(0).int()) and off[0] == 0
+    assert torch.equal(tok.cpu()[:n], order[:n]) and (tok.cpu()[n:] == -1).all()
+    want = torch.full((slots,), -1, dtype=torch.int32)
+    want[order[:n].long()] = torch.arange(n, dtype=torch.int32)
+    assert torch.equal(idx.cpu().flatten(), want)
+
+
 def test_permutation_of_packed_words(cuda_lib):
     # ids above 32767 make negative words; 65535 is outside any range
     ids = torch.randint(0, 1000, (400, 8), generator=gen(3), dtype=torch.int32)
@@ -335,6 +354,68 @@ def test_wgrad(cuda_lib, which, n, k):
     check_wgrad(SIZES[which], n, k, BF16, gather=True, accumulate=True, pad=16, seed=30)
 
 
+def test_weights_gradient_of_no_rows(cuda_lib):
+    dy = torch.empty((0, 24), dtype=BF16, device="cuda")
+    x = torch.empty((0, 40), dtype=BF16, device="cuda")
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for dtype in (BF16, FP32):
+        dw = torch.full((3, 24, 40), CANARY, dtype=dtype, device="cuda")
+        mf.moe_grouped_gemm_wgrad(dy, x, off, dw, accumulate=True)
+        assert (dw == CANARY).all()
+        mf.moe_grouped_gemm_wgrad(dy, x, off, dw)
+        assert (dw == 0).all()
+
+
+def test_every_other_expert(cuda_lib):
+    """A weight view that skips experts and starts inside its buffer."""
+    sizes, n, k = [5, 0, 130, 9], 136, 264
+    w = weights(9, n, k, 1, 8, 1)[1::2]
+    x = padded(144, k, 2, 8)
+    out = torch.empty((144, n), dtype=FP32, device="cuda")
+    mf.moe_grouped_gemm(x, w, offsets_of(sizes), out)
+    lo = 0
+    for e, m in enumerate(sizes):
+        r, we = x[lo:lo + m].double(), w[e].double()
+        within(out[lo:lo + m], r @ we.t(), r.abs() @ we.abs().t(), k, FP32)
+        lo += m
+
+
+@pytest.mark.parametrize("n,k", [(65536, 8), (8, 65536), (40000, 72)])
+def test_wide_and_flat_matrices(cuda_lib, n, k):
+    check_forward([3, 0, 20], n, k, FP32)
+    check_dgrad([3, 0, 20], n, k, BF16)
+    check_wgrad([3, 0, 20], n, k, BF16)
+
+
+def test_fp32_sums_over_long_dimensions(cuda_lib):
+    """FP32 results are summed outside the tensor cores every 640 values.  Inside, each
+    of the 40 products of 16 values that are added to one sum loses at most 2^-22 of
+    the running magnitude (two truncated bits), outside each addition 2^-24: C values
+    lose (40 + C / 640) * 2^-22 of S, not C * 2^-23."""
+    n, k, rows = 264, 16384, 300
+    w, x = weights(1, n, k, 1), padded(rows, k, 2, 0)
+    off = offsets_of([rows])
+    out = torch.empty((rows, n), dtype=FP32, device="cuda")
+    dw = torch.empty((1, n, 264), dtype=FP32, device="cuda")
+    index = torch.arange(rows, dtype=torch.int32, device="cuda")
+    terms = 2 * (40 + k // 640 + 1)
+    for ix in (None, index):
+        mf.moe_grouped_gemm(x, w, off, out, row_index=ix)
+        within(out, x.double() @ w[0].double().t(), x.double().abs() @ w[0].double().abs().t(),
+               terms, FP32)
+        rel = (out.double() - x.double() @ w[0].double().t()).norm() / out.double().norm()
+        assert rel < 1e-6, rel
+    many = 9000
+    dy, xx = padded(many, n, 3, 0), padded(many, 264, 4, 0)
+    off = offsets_of([many])
+    index = torch.arange(many, dtype=torch.int32, device="cuda")
+    terms = 2 * (40 + many // 640 + 1)
+    for ix in (None, index):
+        mf.moe_grouped_gemm_wgrad(dy, xx, off, dw, row_index=ix)
+        within(dw[0], dy.double().t() @ xx.double(), dy.double().abs().t() @ xx.double().abs(),
+               terms, FP32)
+
+
 def test_non_finite_rows_stay_in_their_expert(cuda_lib):
     """A NaN row touches its own output row, and its own expert's gradient only."""
     sizes, n, k = [70, 3, 90], 136, 200
@@ -428,6 +509,42 @@ def test_int4(cuda_lib, sizes, group):
 def test_int4_dense(cuda_lib, rows, n, k, group):
     check_int4([rows], n, k, group, BF16, dense=True, zeros=True)
     check_int4([rows], n, k, group, FP32, dense=True, scale_dtype=FP32, seed=3)
+
+
+@pytest.mark.parametrize("group,k", [(32, 512), (64, 512), (128, 512), (32, 96), (128, 384)])
+def test_int4_scales_at_any_word(cuda_lib, group, k):
+    """Scales and zeros that start at any 4-byte boundary."""
+    sizes, n = [3, 20, 1], 45
+    for scale_dtype, skip in ((BF16, 2), (BF16, 6), (FP32, 1), (FP32, 3)):
+        q, s, z, w = int4_weights(3, n, k, group, scale_dtype, True, 1)
+        sbuf = torch.empty(s.numel() + skip, dtype=scale_dtype, device="cuda")
+        sv = sbuf[skip:].view(s.shape).copy_(s)
+        zbuf = torch.empty(z.numel() + 4, dtype=torch.uint8, device="cuda")
+        zv = zbuf[4:].view(z.shape).copy_(z)
+        x = padded(24, k, 2, 0)
+        out = torch.empty((24, n), dtype=FP32, device="cuda")
+        mf.moe_grouped_gemv_int4(x, q, sv, offsets_of(sizes), out, zeros=zv)
+        lo = 0
+        for e, m in enumerate(sizes):
+            r = x[lo:lo + m].double()
+            within(out[lo:lo + m], r @ w[e].t(), r.abs() @ w[e].abs().t(), k + 2 * k // group, FP32)
+            lo += m
+
+
+def test_int4_every_nibble_and_zero(cuda_lib):
+    """All 256 pairs of nibble and zero point, exactly (one value a row of x)."""
+    k, n = 256, 512
+    q = torch.arange(256, dtype=torch.int32)
+    nib = (q % 16).repeat(n, 1)                         # column c holds c % 16
+    packed = (nib[:, 0::2] | nib[:, 1::2] << 4).to(torch.uint8).view(1, n, k // 2).cuda()
+    zeros = (torch.arange(n * 8) // 8 % 16).to(torch.uint8).view(1, n, 8).cuda()
+    scales = torch.ones((1, n, 8), dtype=FP32, device="cuda")
+    x = torch.zeros((16, k), dtype=BF16, device="cuda")
+    x[torch.arange(16), torch.arange(16) + 48] = 1.0    # row r picks column 48 + r
+    out = torch.empty((16, n), dtype=FP32, device="cuda")
+    mf.moe_grouped_gemv_int4(x, packed, scales, None, out, zeros=zeros)
+    want = torch.arange(16).view(16, 1) - (torch.arange(n) % 16).view(1, n)
+    assert torch.equal(out.cpu(), want.float())
 
 
 def test_int4_many_experts(cuda_lib):
@@ -616,6 +733,89 @@ def test_bits_repeat_on_streams_and_in_graphs(cuda_lib, programmatic):
             assert torch.equal(outs[3], want[3] * -2)
     finally:
         mf.set_programmatic_launch(True)
+
+
+def test_decode_loop_in_a_graph(cuda_lib):
+    """Decoded tokens one after the other: every launch right behind a finalize that lets
+    its successor start early, with programmatic launch on and off."""
+    T, K, E, H = 2, 8, 16, 4096
+    q, s, z, _ = int4_weights(E, H, H, 128, BF16, True, 1)
+    w = weights(E, H, H, 2)
+    norm = torch.ones(H, dtype=BF16, device="cuda")
+    rw = torch.rand((T, K), generator=gen(3)).cuda()
+    ids = torch.stack([torch.randperm(E, generator=gen(t))[:K] for t in range(T)]).int().cuda()
+    start = randn((T, H), 4)
+
+    def steps():
+        h, kept = start, []
+        for i in range(4):
+            step_ids = ((ids + i) % E).contiguous()
+            off, idx, tok = mf.moe_expert_permutation(step_ids, E)
+            y = torch.empty((T * K, H), dtype=BF16, device="cuda")
+            if i % 2:
+                mf.moe_grouped_gemv_int4(h, q, s, off, y, zeros=z, row_index=tok)
+            else:
+                mf.moe_grouped_gemm(h, w, off, y, row_index=tok)
+            h = torch.empty((T, H), dtype=BF16, device="cuda")
+            mf.moe_finalize_rmsnorm(y, rw, idx, norm, h, eps=1e-6, gain_center=0.0,
+                                    weight_before_norm=False)
+            kept.append(h)
+        return kept
+
+    results = []
+    try:
+        for programmatic in (True, False):
+            mf.set_programmatic_launch(programmatic)
+            results.append([t.clone() for t in steps()])
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                outs = steps()
+            for _ in range(3):
+                g.replay()
+            torch.cuda.synchronize()
+            results.append(outs)
+    finally:
+        mf.set_programmatic_launch(True)
+    for other in results[1:]:
+        for a, b in zip(results[0], other):
+            assert torch.equal(a, b)
+    assert all(torch.isfinite(t).all() for t in results[0])
+
+
+def test_two_streams_at_once(cuda_lib):
+    """Large products on two streams at the same time give what each gives alone."""
+    jobs = []
+    for seed in (1, 2):
+        sizes = [700, 0, 300, 90 * seed]
+        x, w = padded(sum(sizes), 1032, seed, 0), weights(4, 1416, 1032, seed + 5)
+        q, s, z, _ = int4_weights(4, 1000, 1024, 64, BF16, True, seed)
+        jobs.append((x, w, offsets_of(sizes), q, s, z, padded(sum(sizes), 1024, seed + 9, 0)))
+
+    def run(job, outs=None):
+        x, w, off, q, s, z, x4 = job
+        outs = outs or (torch.empty((x.shape[0], 1416), dtype=BF16, device="cuda"),
+                        torch.empty((x.shape[0], 1000), dtype=FP32, device="cuda"),
+                        torch.empty(w.shape, dtype=FP32, device="cuda"))
+        mf.moe_grouped_gemm(x, w, off, outs[0])
+        mf.moe_grouped_gemv_int4(x4, q, s, off, outs[1], zeros=z)
+        mf.moe_grouped_gemm_wgrad(outs[0], x, off, outs[2])
+        return outs
+
+    alone = [run(j) for j in jobs]
+    torch.cuda.synchronize()
+    together = [tuple(torch.empty_like(t) for t in a) for a in alone]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for st, job, outs in zip(streams, jobs, together):
+            with torch.cuda.stream(st):
+                run(job, outs)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, together):
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)
 
 
 def test_stream_argument(cuda_lib):
