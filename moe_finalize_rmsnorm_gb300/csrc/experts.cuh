@@ -14,6 +14,28 @@ __device__ __forceinline__ void expert_rows(const int32_t *offsets, int e, int r
     hi = min(max(__ldg(offsets + e + 1), lo), rows);
 }
 
+// mbar_wait of common.cuh for waits that are long and many (a persistent kernel's
+// roles wait for each other all the time): each try may suspend the thread for up to
+// a millisecond, so that a waiting warp issues next to nothing.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    const auto attempt = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(1000000u)
+            : "memory");
+        return ok != 0;
+    };
+    if (attempt()) return true;
+    const uint64_t start = globaltimer_ns();
+    while (!attempt())
+        if (globaltimer_ns() - start > limit_ns) return false;
+    return true;
+}
+
 // One lane of the warp, the same one every time, known to the compiler as one:
 // the asynchronous copies and products take their operands from uniform
 // registers, and code that several lanes might enter is issued lane by lane.

@@ -304,7 +304,7 @@ struct Gemv {
             const int blocks = WHOLE ? 8 : min(kSpan, a.k - now.stage * kSpan) / 32;
             const uint32_t slot = it % kStages;
             cp_async_wait<kStages - 2>();
-            if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * slot, it / kStages & 1, limit))) {
+            if (!__all_sync(0xffffffffu, mbar_wait_long(full + 8 * slot, it / kStages & 1, limit))) {
                 limit = 0;
                 if (lane == 0) atomicOr(a.status, kStatusWaitTimeout);
             }
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     }
     if (limit == 0)  // copies may still be in flight: wait once more before the memory goes
         for (uint32_t s = 1; s <= kStages && s <= it; ++s)
-            (void)mbar_wait(k.full + 8 * ((it - s) % kStages), (it - s) / kStages & 1, a.timeout_ns);
+            (void)mbar_wait_long(k.full + 8 * ((it - s) % kStages), (it - s) / kStages & 1, a.timeout_ns);
     cp_async_wait<0>();
 }
 
