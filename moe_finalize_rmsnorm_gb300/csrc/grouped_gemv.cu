@@ -320,7 +320,9 @@ struct Gemv {
             const int next = now.item != d.item ? 0
                              : WHOLE            ? 8
                                                 : min(kSpan, a.k - now.stage * kSpan) / 32;
-#pragma unroll 1
+            // written out twice where the registers allow it (73 against 78 us, 8 tokens)
+            constexpr int kUnroll = TILES == 1 ? 2 : 1;
+#pragma unroll kUnroll
             for (int half = 0; half < 2; ++half) {
                 const int left = WHOLE ? 4 : blocks - 4 * half;  // blocks from here on
                 const int after = half ? next : blocks - 4;
@@ -358,6 +360,9 @@ struct Gemv {
                 const int x_next = half ? share * kSpan - 128 : 128;
                 const uint32_t wh = wd ^ half << 6;
                 float sum[2][NT][4];
+                uint32_t wn[4];  // the words of the next block
+#pragma unroll
+                for (int i = 0; i < 4; ++i) wn[i] = lds<uint32_t>(wh + 1024 * i);
                 // minus the zero, in 64ths (made as the nibbles are)
                 uint32_t zero[4] = {0xBE00BE00u, 0xBE00BE00u, 0xBE00BE00u, 0xBE00BE00u};
 #pragma unroll
@@ -381,7 +386,8 @@ struct Gemv {
                     uint32_t q[4][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t w = lds<uint32_t>((wh ^ b << 4) + 1024 * i);
+                        const uint32_t w = wn[i];
+                        if (b < 3) wn[i] = lds<uint32_t>((wh ^ (b + 1) << 4) + 1024 * i);
                         const uint32_t v = w >> 8;
                         q[i][0] = fma_bf16x2(w & 0x000F000Fu, 0x7F007F00u, zero[i]);
                         q[i][1] = fma_bf16x2(w & 0x00F000F0u, 0x7D007D00u, zero[i]);
