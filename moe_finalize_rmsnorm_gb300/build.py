@@ -22,7 +22,7 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libmoe_finalize.so")
 
 SOURCES = ["api.cu", "experts_api.cu", "tp_finalize.cu", "beam_finalize.cu", "permute.cu",
-           "grouped_gemm.cu", "grouped_gemv.cu"]
+           "grouped_gemm.cu", "grouped_gemv.cu", "grouped_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
               "--expt-relaxed-constexpr", f"-I{INCLUDE}"]

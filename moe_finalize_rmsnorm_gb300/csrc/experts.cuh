@@ -14,6 +14,55 @@ __device__ __forceinline__ void expert_rows(const int32_t *offsets, int e, int r
     hi = min(max(__ldg(offsets + e + 1), lo), rows);
 }
 
+// The experts' rows and the numbers of their passes (of up to `per_pass` rows):
+// lo[e] is the first row, lo[num_experts] the end; passes[e] counts the passes of the
+// experts before e.  Called by the whole CTA, of which `THREADS` threads take a run of
+// experts each; `scratch` holds an int per warp of theirs.  Returns the passes of all
+// experts; the tables are complete after the caller's next barrier.
+template <int THREADS>
+__device__ __forceinline__ int scan_experts(const int32_t *offsets, int num_experts, int rows,
+                                            int per_pass, int *lo, int *passes, int *scratch) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int per = (num_experts + THREADS - 1) / THREADS;
+    const int first = min(static_cast<int>(threadIdx.x) * per, num_experts);
+    const int last = min(first + per, num_experts);
+    int sum = 0;
+    for (int e = first; e < last; ++e) {
+        int l = 0, h = rows;  // without offsets one expert has every row
+        if (offsets) expert_rows(offsets, e, rows, l, h);
+        lo[e] = l;
+        if (e + 1 == num_experts) lo[e + 1] = h;
+        passes[e] = sum;
+        sum += (h - l + per_pass - 1) / per_pass;
+    }
+    int before = sum;
+    for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+    }
+    if (lane == 31 && warp < THREADS / 32) scratch[warp] = before;
+    before -= sum;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += scratch[w];
+        total += scratch[w];
+    }
+    for (int e = first; e < last; ++e) passes[e] += before;
+    if (threadIdx.x == 0) passes[num_experts] = total;
+    return total;
+}
+
+// The expert of a pass: the last whose passes start at or before it.  `step` is the
+// largest power of two up to the number of experts.
+__device__ __forceinline__ int expert_of_pass(const int *passes, int num_experts, int step,
+                                              int pass) {
+    int e = 0;
+    for (; step > 0; step /= 2)
+        if (e + step < num_experts && passes[e + step] <= pass) e += step;
+    return e;
+}
+
 // mbar_wait of common.cuh for waits that are long and many (a persistent kernel's
 // roles wait for each other all the time): each try may suspend the thread for up to
 // a millisecond, so that a waiting warp issues next to nothing.

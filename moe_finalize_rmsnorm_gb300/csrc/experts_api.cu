@@ -10,10 +10,12 @@ namespace mf {
 cudaError_t prepare_permute_kernels();
 cudaError_t prepare_grouped_gemm(int *pairs);
 cudaError_t prepare_grouped_gemv();
+cudaError_t prepare_grouped_rows();
 
 cudaError_t prepare_expert_kernels(int *pairs) {
     cudaError_t e = prepare_permute_kernels();
     if (e == cudaSuccess) e = prepare_grouped_gemv();
+    if (e == cudaSuccess) e = prepare_grouped_rows();
     return e == cudaSuccess ? prepare_grouped_gemm(pairs) : e;
 }
 }  // namespace mf

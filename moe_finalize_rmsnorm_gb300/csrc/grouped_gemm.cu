@@ -120,9 +120,7 @@ __device__ __forceinline__ Tile tile_of(const GroupedArgs &a, const Control &c, 
         r.sum0 = c.lo[r.expert];
     } else {
         const int u = t / mt;
-        int e = 0;  // the last expert whose tiles start at or before u
-        for (int step = 512; step > 0; step /= 2)
-            if (e + step < a.num_experts && c.tiles[e + step] <= u) e += step;
+        const int e = expert_of_pass(c.tiles, a.num_experts, kMaxExperts / 2, u);
         r.expert = e;
         const int rows = c.lo[e + 1] - c.lo[e];
         const int rt = c.tiles[e + 1] - c.tiles[e];
@@ -248,35 +246,8 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
     pdl_wait();
     if (warp == 2) tmem_alloc<CTAS>(smem_u32(&c.tmem), kTmemColumns);
 
-    // The experts' rows and their tiles' numbers (an exclusive scan, each thread
-    // a run of experts).
-    const int per = divide_up(a.num_experts, kScanThreads);
-    const int first = min(static_cast<int>(threadIdx.x) * per, a.num_experts);
-    const int last = min(first + per, a.num_experts);
-    int sum = 0;
-    for (int e = first; e < last; ++e) {
-        int lo, hi;
-        expert_rows(a.offsets, e, static_cast<int>(a.rows), lo, hi);
-        c.lo[e] = lo;
-        if (e + 1 == a.num_experts) c.lo[e + 1] = hi;
-        c.tiles[e] = sum;
-        sum += divide_up(hi - lo, kRowsMax);
-    }
-    int before = sum;
-    for (int o = 1; o < 32; o *= 2) {
-        const int v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
-    }
-    if (lane == 31 && warp < kScanThreads / 32) c.scan[warp] = before;
-    before -= sum;
-    __syncthreads();
-    int total = 0;
-    for (int w = 0; w < kScanThreads / 32; ++w) {
-        if (w < warp) before += c.scan[w];
-        total += c.scan[w];
-    }
-    for (int e = first; e < last; ++e) c.tiles[e] += before;
-    if (threadIdx.x == 0) c.tiles[a.num_experts] = total;
+    const int total = scan_experts<kScanThreads>(a.offsets, a.num_experts, static_cast<int>(a.rows),
+                                                 kRowsMax, c.lo, c.tiles, c.scan);
     tcgen05_fence_before();
     __syncthreads();
     if (PAIR) cluster_barrier();
@@ -726,6 +697,7 @@ cudaError_t prepare_grouped_gemm(int *pairs) {
 }
 
 cudaError_t launch_grouped_gemm(const GroupedArgs &a, cudaStream_t s) {
+    if (a.kind == kForward && few_rows(a.rows, a.num_experts)) return launch_grouped_rows(a, s);
     const bool narrow = (a.kind == kForward ? a.n : a.k) <= 128;
     if (a.out_fp32) return narrow ? launch_ctas<1, true>(a, s) : launch_ctas<2, true>(a, s);
     return narrow ? launch_ctas<1, false>(a, s) : launch_ctas<2, false>(a, s);

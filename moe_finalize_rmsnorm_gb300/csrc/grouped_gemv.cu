@@ -9,8 +9,8 @@
 // conversion.  Each group's FP32 sum is scaled once (and by 64 at the end).  Warps that share a column
 // block split the summed values between them and add up through shared memory, in
 // warp order.
-#include "experts.cuh"
 #include "experts.h"
+#include "few_rows.cuh"
 #include "tensor_map.h"
 
 namespace mf {
@@ -64,23 +64,6 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src, int by
                  : "memory");
 }
 
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// The same with nothing to add to.
-__device__ __forceinline__ void mma_16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                                uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-
 // a * b + c on two BF16, one rounding.
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
@@ -94,11 +77,6 @@ __device__ __forceinline__ void fma_f32x2(float &c0, float &c1, float a, float b
         "mov.b64 c, {%0, %1};\n\tfma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
         : "+f"(c0), "+f"(c1)
         : "f"(a), "f"(b0), "f"(b1));
-}
-
-template <typename T>
-__device__ __forceinline__ T lds(uint32_t addr) {
-    return *reinterpret_cast<const T *>(__cvta_shared_to_generic(addr));
 }
 
 template <int N>
@@ -118,13 +96,6 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&v)[N]) {
         v[3] = q.w;
     }
 }
-
-// Where a warp is in its sequence of (column block, stage) pairs.
-struct Cursor {
-    int item;
-    int stage;  // of the item's spans
-    int expert, n0, row0, rows;
-};
 
 // The same for the copies.
 struct Copies {
@@ -157,12 +128,8 @@ struct Gemv {
     float *sums;  // of the block's first warp
     const int barrier;
 
-    // The expert of a pass over the weights (they are counted over the experts).
     __device__ int expert_of(int pass) const {
-        int e = 0;
-        for (int s = search; s > 0; s /= 2)
-            if (e + s < a.num_experts && c.tiles[e + s] <= pass) e += s;
-        return e;
+        return expert_of_pass(c.tiles, a.num_experts, search, pass);
     }
 
     __device__ void locate(Cursor &p) const {
@@ -495,45 +462,14 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     fence_mbar_init();
     pdl_wait();
 
-    // The experts' rows and the numbers of their passes (exclusive scan).
-    const int per = (a.num_experts + kGemvThreads - 1) / kGemvThreads;
-    const int first = min(static_cast<int>(threadIdx.x) * per, a.num_experts);
-    const int last = min(first + per, a.num_experts);
-    int sum = 0;
-    for (int e = first; e < last; ++e) {
-        int lo = 0, hi = static_cast<int>(a.rows);
-        if (a.offsets) expert_rows(a.offsets, e, static_cast<int>(a.rows), lo, hi);
-        c.lo[e] = lo;
-        if (e + 1 == a.num_experts) c.lo[e + 1] = hi;
-        c.tiles[e] = sum;
-        sum += (hi - lo + 8 * TILES - 1) / (8 * TILES);
-    }
-    int before = sum;
-    for (int o = 1; o < 32; o *= 2) {
-        const int v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
-    }
-    if (lane == 31) c.scan[warp] = before;
-    before -= sum;
-    __syncthreads();
-    int total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += c.scan[w];
-        total += c.scan[w];
-    }
-    for (int e = first; e < last; ++e) c.tiles[e] += before;
-    if (threadIdx.x == 0) c.tiles[a.num_experts] = total;
+    const int total = scan_experts<kGemvThreads>(a.offsets, a.num_experts, static_cast<int>(a.rows),
+                                                 8 * TILES, c.lo, c.tiles, c.scan);
     __syncthreads();
 
     const int block = warp / share;
     const unsigned col_blocks = (a.n + kCols - 1) / kCols;
-    // Column blocks that lie together to one CTA's warps (they read the same rows of x),
-    // unless there are so few that this would leave CTAs without.
     const int at_once = kWarps / share, items = total * static_cast<int>(col_blocks);
-    const int item0 = block >= at_once ? items  // a warp that is left over
-                      : items >= 4 * static_cast<int>(gridDim.x) * at_once
-                          ? blockIdx.x * at_once + block
-                          : blockIdx.x + gridDim.x * block;
+    const int item0 = first_item(block, at_once, items);
     const Gemv<GROUP, TILES, WHOLE> k{a,
                         map,
                         c,
@@ -580,23 +516,9 @@ cudaError_t launch(const GemvArgs &a, cudaStream_t s) {
                     {row, static_cast<cuuint64_t>(a.n), static_cast<cuuint64_t>(a.num_experts)},
                     {row, row * a.n}, kSpan / 2, kCols))
         return cudaErrorInvalidValue;
-    // Warps to a column block: as many as make the longest warp's work shortest,
-    // counted in stages, a block's beginning and end as two (the experts' sizes are
-    // known on the device only: at most this many blocks).
     const int64_t blocks = (a.n + kCols - 1) / kCols *
                            (a.rows / (8 * TILES) + min(int64_t{a.num_experts}, a.rows));
-    const int spans = (a.k + kSpan - 1) / kSpan;
-    int share = 1;
-    int64_t best = INT64_MAX;
-    for (int w : {1, 2, 3, 4, 5, 8, 16}) {
-        if (w > spans) break;
-        const int64_t at_once = int64_t{a.num_sms} * (kWarps / w);
-        const int64_t cost = (blocks + at_once - 1) / at_once * ((spans + w - 1) / w + 2);
-        if (cost < best) {
-            best = cost;
-            share = w;
-        }
-    }
+    const int share = warps_of_block(blocks, (a.k + kSpan - 1) / kSpan, kWarps, a.num_sms);
     // work items are counted in 32 bits (a buffer of so many results does not fit)
     if (blocks > INT32_MAX - int64_t{a.num_sms} * kWarps) return cudaErrorInvalidValue;
     return launch_ex(grouped_gemv_int4_kernel<GROUP, TILES, WHOLE>,

@@ -285,6 +285,26 @@ def test_forward_wide(cuda_lib, sizes, n, k):
     check_forward(sizes, n, k, FP32, gather=True, seed=5)
 
 
+@pytest.mark.parametrize("sizes", [[64], [65], [60, 1, 2, 1], [16, 17, 0, 31], [0, 0, 64, 0],
+                                   [2] * 128, [256] + [0] * 127, [253] + [0] * 128, [1] * 64])
+@pytest.mark.parametrize("n,k", [(136, 200), (1000, 1416)])
+def test_forward_where_the_few_rows_kernel_ends(cuda_lib, sizes, n, k):
+    for extra in (0, 1):
+        check_forward(sizes, n, k, FP32, extra=extra)
+        check_forward(sizes, n, k, BF16, gather=True, pad=8, extra=extra, seed=3)
+
+
+def test_few_rows_with_long_sums(cuda_lib):
+    """As test_fp32_sums_over_long_dimensions, at the sizes of the other kernel."""
+    n, k = 264, 16384
+    w, x = weights(2, n, k, 1), padded(20, k, 2, 0)
+    out = torch.empty((20, n), dtype=FP32, device="cuda")
+    mf.moe_grouped_gemm(x, w, offsets_of([13, 7]), out)
+    for e, sl in ((0, slice(0, 13)), (1, slice(13, 20))):
+        within(out[sl], x[sl].double() @ w[e].double().t(),
+               x[sl].double().abs() @ w[e].double().abs().t(), 2 * (40 + k // 640 + 13), FP32)
+
+
 def test_forward_many_experts(cuda_lib):
     sizes = [(7 * e) % 5 if e % 3 else 0 for e in range(1024)]
     check_forward(sizes, 64, 64, BF16)
