@@ -125,7 +125,8 @@ __device__ __forceinline__ Tile tile_of(const GroupedArgs &a, const Control &c, 
         const int rows = c.lo[e + 1] - c.lo[e];
         const int rt = c.tiles[e + 1] - c.tiles[e];
         const int local = t - c.tiles[e] * mt;
-        const int each = round_up(divide_up(rows, rt), 16);
+        // of what the instruction takes: only the last tile is padded
+        const int each = round_up(divide_up(rows, rt), 16 * CTAS);
         const int first = local % rt * each;
         r.m0 = local / rt * M;
         r.row0 = c.lo[e] + first;

@@ -271,7 +271,8 @@ struct Gemv {
             const int blocks = WHOLE ? 8 : min(kSpan, a.k - now.stage * kSpan) / 32;
             const uint32_t slot = it % kStages;
             cp_async_wait<kStages - 2>();
-            if (!__all_sync(0xffffffffu, mbar_wait_long(full + 8 * slot, it / kStages & 1, limit))) {
+            if (limit == 0 ||
+                !__all_sync(0xffffffffu, mbar_wait_long(full + 8 * slot, it / kStages & 1, limit))) {
                 limit = 0;
                 if (lane == 0) atomicOr(a.status, kStatusWaitTimeout);
             }

@@ -123,7 +123,8 @@ struct Rows {
         int segment = 0;
         while (now.item == d.item) {
             const uint32_t slot = it % kStages;
-            if (!__all_sync(0xffffffffu, mbar_wait_long(full + 8 * slot, it / kStages & 1, limit))) {
+            if (limit == 0 ||
+                !__all_sync(0xffffffffu, mbar_wait_long(full + 8 * slot, it / kStages & 1, limit))) {
                 limit = 0;
                 if (lane == 0) atomicOr(a.status, kStatusWaitTimeout);
             }
