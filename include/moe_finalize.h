@@ -385,7 +385,7 @@ mf_status moe_grouped_gemm_wgrad(const void *grad_output, int64_t grad_output_st
 /*
  * moe_grouped_gemv_int4 -- moe_grouped_gemm with 4-bit weights, for decode (few
  * rows per expert; any number is allowed, and the weights are read again for
- * every 16 of an expert's rows):
+ * every 8 to 32 of an expert's rows):
  *
  *   w[e, n, c]   = (q[e, n, c] - zero[e, n, c / group_size]) * scale[e, n, c / group_size]
  *   output[r, n] = sum over c of w[e, n, c] * x[i(r), c]

@@ -1,7 +1,7 @@
 // Products of few rows per expert with 4-bit weights and group scales.
 //
-// Bound by the weights' bytes: each is read once for every 16 rows of its
-// expert.  A warp takes 32 columns n and up to 16 rows.  It streams 256 summed
+// Bound by the weights' bytes: each is read once for every 8, 16 or 32 rows of its
+// expert.  A warp takes 32 columns n and up to so many rows.  It streams 256 summed
 // values of its 32 columns a stage (128 bytes a column) through its own ring in
 // shared memory, one tensor-map copy a stage, turns the nibbles into (q - z) / 64 in
 // BF16 (exact), and multiplies with the rows in mma.m16n8k16, n along M, the rows
@@ -16,8 +16,8 @@
 namespace mf {
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kGemvThreads = 32 * kWarps;
+// Warps of a CTA: for passes of 32 rows 12, with the registers of 16.
+constexpr int warps_of(int tiles) { return tiles == 4 ? 12 : 16; }
 constexpr int kCols = 32;      // n of a warp
 constexpr int kSpan = 256;     // summed values of a stage: 128 bytes of a column
 constexpr int kStages = 2;
@@ -35,8 +35,8 @@ struct GroupData {
 };
 
 struct GemvControl {
-    uint64_t full[kWarps][kStages];
-    int scan[kWarps];
+    uint64_t full[16][kStages];
+    int scan[16];
     int tiles[kMaxExperts + 1];  // passes of the experts before this one
     int lo[kMaxExperts + 1];     // first row
 };
@@ -46,7 +46,7 @@ template <int GROUP, int TILES>
 struct GemvSmem {
     static constexpr int kSumBytes = kCols * 8 * TILES * 4;
     static constexpr int kBytes =
-        1024 + kWarps * (kStages * (kWeightBytes + GroupData<GROUP>::kBytes) + kSumBytes) +
+        1024 + warps_of(TILES) * (kStages * (kWeightBytes + GroupData<GROUP>::kBytes) + kSumBytes) +
         static_cast<int>(sizeof(GemvControl));
     static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
 };
@@ -449,9 +449,10 @@ struct Gemv {
 };
 
 template <int GROUP, int TILES, bool WHOLE>
-__global__ void __launch_bounds__(kGemvThreads, 1)
+__global__ void __launch_bounds__(32 * warps_of(TILES), 1)
     grouped_gemv_int4_kernel(const __grid_constant__ CUtensorMap map, const GemvArgs a,
                              const int share) {
+    constexpr int kWarps = warps_of(TILES), kGemvThreads = 32 * kWarps;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + (((smem_u32(raw) + 1023u) & ~1023u) - smem_u32(raw));
     uint8_t *group_data = smem + kWarps * kStages * kWeightBytes;
@@ -500,6 +501,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     while (now.item < k.items) {
         if (TILES == 1 || now.rows <= 8)
             k.template item<1>(now, ahead, it, limit);
+        else if (TILES <= 2 || now.rows <= 16)
+            k.template item<(TILES < 2 ? TILES : 2)>(now, ahead, it, limit);
         else
             k.template item<TILES>(now, ahead, it, limit);
     }
@@ -511,6 +514,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
 
 template <int GROUP, int TILES, bool WHOLE>
 cudaError_t launch(const GemvArgs &a, cudaStream_t s) {
+    constexpr int kWarps = warps_of(TILES);
     CUtensorMap map;
     const cuuint64_t row = static_cast<cuuint64_t>(a.k) / 2;
     if (!encode_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, 3,
@@ -524,17 +528,20 @@ cudaError_t launch(const GemvArgs &a, cudaStream_t s) {
     if (blocks > INT32_MAX - int64_t{a.num_sms} * kWarps) return cudaErrorInvalidValue;
     return launch_ex(grouped_gemv_int4_kernel<GROUP, TILES, WHOLE>,
                      dim3(static_cast<unsigned>(min(blocks, int64_t{a.num_sms}))),
-                     dim3(kGemvThreads), GemvSmem<GROUP, TILES>::kBytes, s, 1, a.programmatic, map, a, share);
+                     dim3(32 * kWarps), GemvSmem<GROUP, TILES>::kBytes, s, 1, a.programmatic, map, a, share);
 }
 
 template <int GROUP>
 cudaError_t launch_group(const GemvArgs &a, cudaStream_t s) {
-    // More than five rows an expert on average: passes of 16 rows.
-    const bool many = a.rows > 5 * int64_t{a.num_experts};
+    // Rows of a pass by the average of an expert: 16 from five rows on (8 rows 100 against
+    // 122 us for 32 a pass), 32 from 24 on (one matrix: 24 rows 52 us in passes of 16, 62 in
+    // one of 32; 32 rows 80 against 62).
     const bool whole = a.k % kSpan == 0 && reinterpret_cast<uintptr_t>(a.scales) % 16 == 0 &&
                        reinterpret_cast<uintptr_t>(a.zeros) % 8 == 0;
-    if (whole) return many ? launch<GROUP, 2, true>(a, s) : launch<GROUP, 1, true>(a, s);
-    return many ? launch<GROUP, 2, false>(a, s) : launch<GROUP, 1, false>(a, s);
+    const int64_t E = a.num_experts;
+    if (a.rows > 24 * E) return whole ? launch<GROUP, 4, true>(a, s) : launch<GROUP, 4, false>(a, s);
+    if (a.rows > 5 * E) return whole ? launch<GROUP, 2, true>(a, s) : launch<GROUP, 2, false>(a, s);
+    return whole ? launch<GROUP, 1, true>(a, s) : launch<GROUP, 1, false>(a, s);
 }
 
 template <int GROUP, int TILES>
@@ -550,13 +557,17 @@ cudaError_t prepare() {
 
 }  // namespace
 
+template <int GROUP>
+static cudaError_t prepare_group() {
+    cudaError_t e = prepare<GROUP, 1>();
+    if (e == cudaSuccess) e = prepare<GROUP, 2>();
+    return e == cudaSuccess ? prepare<GROUP, 4>() : e;
+}
+
 cudaError_t prepare_grouped_gemv() {
-    cudaError_t e = prepare<32, 1>();
-    if (e == cudaSuccess) e = prepare<32, 2>();
-    if (e == cudaSuccess) e = prepare<64, 1>();
-    if (e == cudaSuccess) e = prepare<64, 2>();
-    if (e == cudaSuccess) e = prepare<128, 1>();
-    return e == cudaSuccess ? prepare<128, 2>() : e;
+    cudaError_t e = prepare_group<32>();
+    if (e == cudaSuccess) e = prepare_group<64>();
+    return e == cudaSuccess ? prepare_group<128>() : e;
 }
 
 cudaError_t launch_grouped_gemv_int4(const GemvArgs &a, cudaStream_t s) {

@@ -514,7 +514,8 @@ def check_int4(sizes, n, k, group, dtype, *, scale_dtype=BF16, zeros=False, gath
 
 
 @pytest.mark.parametrize("group", [32, 64, 128])
-@pytest.mark.parametrize("sizes", [[1], [2, 0, 1, 1], [8, 7, 9, 0, 16, 17], [33, 1, 64, 65]])
+@pytest.mark.parametrize("sizes", [[1], [2, 0, 1, 1], [8, 7, 9, 0, 16, 17], [33, 1, 64, 65],
+                                   [5, 5], [6, 5], [100, 0, 0, 0, 1]])
 def test_int4(cuda_lib, sizes, group):
     for i, (n, k) in enumerate(((1, group), (7, 3 * group), (33, 8 * group), (100, 640),
                                 (256, 1152))):
@@ -523,7 +524,7 @@ def test_int4(cuda_lib, sizes, group):
         check_int4(sizes, n, k, group, BF16, zeros=True, gather=True, pad=8, seed=i + 20)
 
 
-@pytest.mark.parametrize("rows", [1, 3, 8, 9, 40])
+@pytest.mark.parametrize("rows", [1, 3, 8, 9, 24, 25, 40, 64, 65])
 @pytest.mark.parametrize("n,k,group", [(1, 32, 32), (1001, 4096, 128), (515, 7168, 64),
                                        (64, 16384, 32)])
 def test_int4_dense(cuda_lib, rows, n, k, group):
