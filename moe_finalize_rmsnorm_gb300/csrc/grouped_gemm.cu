@@ -9,8 +9,9 @@
 //   wgrad    D[k, n] = sum_r x[i(r), k] dy[r, n]
 //
 // so the ragged dimension of the first two, an expert's rows, is the one whose
-// tile may be any multiple of 16 up to 256: an expert of 40 rows costs 48, not
-// 128 or 256.  An expert's rows are split evenly over its tiles.  In wgrad the
+// tile may be any multiple of 32 up to 256 (16 for a single CTA): an expert of 40
+// rows costs 64, not 128 or 256.  An expert's rows are split evenly over its tiles.
+// In wgrad the
 // ragged dimension is the summed one; the step that holds an expert's last rows
 // reads them by number, and the rows behind them as zeros, so that a row of
 // another expert (or one that was never written) enters nothing.
@@ -285,8 +286,8 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
             const int col0 = d.m0 + rank * 128 + w * 32;
             const int cols = columns - col0;  // what exists of the warp's 32
             auto take = [&]() {  // wait for the next accumulator
-                ok = __all_sync(0xffffffffu, mbar_wait_long(acc_full + 8 * (acc_n & 1), acc_n >> 1 & 1,
-                                                       a.timeout_ns));
+                ok = __all_sync(0xffffffffu, mbar_wait_long(acc_full + 8 * (acc_n & 1),
+                                                            acc_n >> 1 & 1, a.timeout_ns));
                 tcgen05_fence_after();
                 return lanes + (acc_n & 1) * kRowsMax;
             };
@@ -462,8 +463,8 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
             // chosen by row_index, and the last rows of wgrad's dy.  One or two warps for
             // every stage: a warp issues one copy in some 80 cycles, and a stage takes 32 of
             // them in 512.  (A prefill of 32768 rows at 4096 x 4096: two warps for all stages
-            // 1321 us, one per stage 751; 16-byte cp.async by one warp per stage 997, as the
-            // proxy fence waits for the copies.)  The numbers go through shared memory, so
+            // 1321 us, one per stage 751, two, reading the numbers eight at a time, 703; 16-byte
+            // cp.async by one warp per stage 997, as the proxy fence waits for the copies.)  The numbers go through shared memory, so
             // that the elected lane reads them with uniform addresses.
             const int index = warp < 4 ? warp - 2 : warp - W::kFirstGather + 2;
             const uint32_t stage = index % kStages;

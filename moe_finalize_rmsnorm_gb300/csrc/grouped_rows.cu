@@ -8,6 +8,10 @@
 // shared memory and multiplies them with the rows in mma.m16n8k16, columns along M;
 // where there are few blocks, several warps split one block's summed values and add up
 // through shared memory, in warp order.
+//
+// Measured (GB300, device time): one token through eight 2048 x 4096 matrices 23.4 us
+// (5.7 TB/s; 27.0 by the tensor-core kernel), 1024 x 4096 13.7 (21.7), two rows 9 (21); from
+// 32 rows on 6.6-7.0 TB/s, the copy's.
 #include "experts.h"
 #include "few_rows.cuh"
 #include "tensor_map.h"

@@ -99,11 +99,11 @@ def moe_expert_permutation(expert_ids: torch.Tensor, num_experts: int, *, packed
     # memory allocated here belongs to the stream that writes it
     with nullcontext() if stream is None else torch.cuda.stream(stream):
         if expert_offsets is None:
-            expert_offsets = expert_ids.new_empty(max(num_experts, 0) + 1)
+            expert_offsets = torch.empty(max(num_experts, 0) + 1, dtype=torch.int32, device=dev)
         if expanded_idx is None:
-            expanded_idx = expert_ids.new_empty((T, K))
+            expanded_idx = torch.empty((T, K), dtype=torch.int32, device=dev)
         if row_tokens is None:
-            row_tokens = expert_ids.new_empty(T * K)
+            row_tokens = torch.empty(T * K, dtype=torch.int32, device=dev)
     st = _on_device(dev, lib().moe_expert_permutation, expert_ids.data_ptr(), int(bool(packed)),
                     T, K, num_experts, expert_offsets.data_ptr(), expanded_idx.data_ptr(),
                     row_tokens.data_ptr(), _stream_ptr(stream, dev))
