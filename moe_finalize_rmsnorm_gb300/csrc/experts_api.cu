@@ -112,7 +112,7 @@ mf_status moe_permuted_row_sum(const void *permuted, mf_dtype permuted_dtype, in
     if (!expanded_idx_to_permuted_idx || !output || (rows > 0 && !permuted)) return MF_ERR_NULL;
     if (!aligned(permuted, 16) || !aligned(expanded_idx_to_permuted_idx, 4) || !aligned(output, 16))
         return MF_ERR_ALIGN;
-    if ((num_tokens * (hidden / 8) + 255) / 256 > 0x7fffffffLL) return MF_ERR_SHAPE;
+    if ((num_tokens * (hidden / 8) + 127) / 128 > 0x7fffffffLL) return MF_ERR_SHAPE;
     const mf::DeviceInfo *d = nullptr;
     mf_status st = mf::device_info(&d);
     if (st != MF_OK) return st;

@@ -9,7 +9,8 @@ namespace {
 //
 // Latency bound: 12 bytes a slot move in under a microsecond even for 262144
 // slots, so what counts is the number of dependent steps.  Up to kOneCta slots one
-// CTA does everything (2.8 us for 256 slots).  Beyond, two launches: a cluster
+// CTA does everything (256 slots 2.6 us; 2400 slots 6.1 against 7.7 us for the two
+// launches, 4000 7.7 either way, 8000 12.1 against 7.7).  Beyond, two launches: a cluster
 // counts the slots chunk by chunk and turns the counts into each chunk's first row
 // per expert, and a CTA for every chunk places its slots.  The first rows need no
 // workspace: a chunk is at least as long as there are experts, so they lie in its
@@ -18,8 +19,8 @@ namespace {
 
 constexpr int kPermuteThreads = 1024;
 constexpr int kPermuteWarps = kPermuteThreads / 32;
-constexpr int kOneCta = 8192;
-constexpr int kChunk = 2048;      // slots of a chunk, at least (the last up to twice as many)
+constexpr int kOneCta = 4096;
+constexpr int kChunk = 1024;      // slots of a chunk, at least (the last up to twice as many)
 constexpr int kMaxChunks = 152;
 // CTAs of the cluster that counts: 8, from kManySlots on 16, the largest there is
 // (64000 slots 12.0 against 13.3 us, 262144 slots 13.8 against 11.7 us).
@@ -224,8 +225,10 @@ __global__ void __launch_bounds__(kPermuteThreads) permute_place_kernel(PermuteA
 
 // out[t, :] = sum_j rows[idx[t, j], :], FP32 in ascending j: bound by the rows'
 // bytes.  A thread takes 16 bytes of a row (32 of an FP32 row), and loads the rows
-// of kRowsAhead slots before it adds the first.
-constexpr int kRowsAhead = 8;
+// of kRowsAhead slots before it adds the first.  8000 x 8 rows of 7168: 149.4 us, 6.91
+// TB/s, the copy's rate (two ahead 153, eight 164; 256 threads a CTA 151).
+constexpr int kRowsAhead = 4;
+constexpr int kSumThreads = 128;
 
 // The load of common.cuh's ld_nc_na_16, or zeros (p is not read): no branch between
 // the loads of several rows.
@@ -262,10 +265,10 @@ struct Chunk8 {
 };
 
 template <bool IN_FP32, bool OUT_FP32>
-__global__ void __launch_bounds__(256) permuted_row_sum_kernel(RowSumArgs a) {
+__global__ void __launch_bounds__(kSumThreads) permuted_row_sum_kernel(RowSumArgs a) {
     pdl_wait();
     const int chunks = a.hidden / 8;
-    const int64_t i = blockIdx.x * int64_t{256} + threadIdx.x;
+    const int64_t i = blockIdx.x * int64_t{kSumThreads} + threadIdx.x;
     if (i >= a.num_tokens * chunks) return;
     const int64_t t = i / chunks;
     const int c = static_cast<int>(i - t * chunks) * 8;
@@ -335,7 +338,8 @@ cudaError_t launch_expert_permutation(const PermuteArgs &a, cudaStream_t s) {
 
 cudaError_t launch_permuted_row_sum(const RowSumArgs &a, cudaStream_t s) {
     const int64_t threads = a.num_tokens * (a.hidden / 8);
-    const dim3 grid(static_cast<unsigned>((threads + 255) / 256)), block(256);
+    const dim3 grid(static_cast<unsigned>((threads + kSumThreads - 1) / kSumThreads)),
+        block(kSumThreads);
     if (a.rows_fp32 && a.out_fp32)
         return launch_ex(permuted_row_sum_kernel<true, true>, grid, block, 0, s, 1,
                          a.programmatic, a);

@@ -120,7 +120,7 @@ def test_permutation_extremes(cuda_lib, T, K, E):
         assert torch.equal(tok.cpu(), tokens)
 
 
-@pytest.mark.parametrize("slots", [8191, 8192, 8193, 10239, 10240, 131071, 131072, 131073, 311296,
+@pytest.mark.parametrize("slots", [4095, 4096, 4097, 5120, 8191, 8192, 8193, 10239, 10240, 131071, 131072, 131073, 311296,
                                    400001])
 @pytest.mark.parametrize("E", [1, 7, 1024])
 def test_permutation_at_the_edges_of_its_launches(cuda_lib, slots, E):
