@@ -7,6 +7,8 @@ off by at most half a step of the output's type, 2^-8 (BF16) or 2^-24 (FP32) of
 the value.  Where the result must be exactly zero S is zero, so is the bound.
 """
 import itertools
+import os
+import random
 
 import pytest
 import torch
@@ -586,6 +588,51 @@ def test_int4_non_finite_rows(cuda_lib):
     want[1] = True
     want[3:, 3] = True
     assert torch.equal(bad, want)
+
+
+# ---------------------------------------------------------------------------
+# seeded random configurations
+
+def draw_sizes(rng):
+    E = rng.choice([1, 2, 3, 7, 16, 40, 130, 600])
+    kind = rng.choice(["even", "skewed", "sparse", "one"])
+    total = rng.choice([0, 1, 5, 64, 65, 200, 1000, 3000])
+    if kind == "one":
+        sizes = [0] * E
+        sizes[rng.randrange(E)] = total
+        return sizes
+    w = {"even": [1.0] * E, "skewed": [(1 + e) ** -1.5 for e in range(E)],
+         "sparse": [rng.random() < 0.2 for _ in range(E)]}[kind]
+    w = w if sum(w) else [1.0] * E
+    sizes = [0] * E
+    for _ in range(total):
+        sizes[rng.choices(range(E), w)[0]] += 1
+    return sizes
+
+
+@pytest.mark.parametrize("seed", range(int(os.environ.get("MF_FUZZ_SEEDS", "24"))))
+def test_random_grouped_products(cuda_lib, seed):
+    rng = random.Random(seed)
+    sizes = draw_sizes(rng)
+    widest = 2000 if len(sizes) < 100 else 300
+    n, k = (8 * rng.randint(1, widest // 8) for _ in range(2))
+    dtype = rng.choice([BF16, FP32])
+    pad, extra = rng.choice([0, 8, 40]), rng.choice([0, 1, 77])
+    which = rng.choice(["forward", "dgrad", "wgrad", "int4"])
+    gather = rng.random() < 0.5
+    if which == "forward":
+        check_forward(sizes, n, k, dtype, gather=gather, pad=pad, extra=extra, seed=seed)
+    elif which == "dgrad":
+        check_dgrad(sizes, n, k, dtype, pad=pad, extra=extra, seed=seed)
+    elif which == "wgrad":
+        check_wgrad(sizes, n, k, dtype, gather=gather, accumulate=rng.random() < 0.5, pad=pad,
+                    extra=extra, seed=seed)
+    else:
+        group = rng.choice([32, 64, 128])
+        k = group * rng.randint(1, max(1, widest // group))
+        check_int4(sizes, rng.randint(1, widest), k, group, dtype,
+                   scale_dtype=rng.choice([BF16, FP32]), zeros=rng.random() < 0.5, gather=gather,
+                   pad=pad, seed=seed)
 
 
 # ---------------------------------------------------------------------------
