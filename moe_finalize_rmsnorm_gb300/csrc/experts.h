@@ -18,6 +18,7 @@ struct PermuteArgs {
     int32_t *offsets;        // [E + 1]
     int32_t *slot_to_row;    // [slots], -1 for a slot without an expert
     int32_t *row_to_token;   // [slots], -1 behind the last row
+    bool wide_clusters;      // the device runs clusters of 16
     bool programmatic;
 };
 
@@ -100,8 +101,9 @@ struct GemvArgs {
 };
 
 // Per-device one-time set-up (kernel attributes); `pairs`: clusters of two CTAs
-// of the grouped product that the device runs at once.
-cudaError_t prepare_expert_kernels(int *pairs);
+// of the grouped product that the device runs at once; `wide_clusters`: whether it
+// runs clusters of 16.
+cudaError_t prepare_expert_kernels(int *pairs, bool *wide_clusters);
 
 cudaError_t launch_expert_permutation(const PermuteArgs &a, cudaStream_t s);
 cudaError_t launch_permuted_row_sum(const RowSumArgs &a, cudaStream_t s);

@@ -7,13 +7,13 @@
 #include "moe_finalize.h"
 
 namespace mf {
-cudaError_t prepare_permute_kernels();
+cudaError_t prepare_permute_kernels(bool *wide_clusters);
 cudaError_t prepare_grouped_gemm(int *pairs);
 cudaError_t prepare_grouped_gemv();
 cudaError_t prepare_grouped_rows();
 
-cudaError_t prepare_expert_kernels(int *pairs) {
-    cudaError_t e = prepare_permute_kernels();
+cudaError_t prepare_expert_kernels(int *pairs, bool *wide_clusters) {
+    cudaError_t e = prepare_permute_kernels(wide_clusters);
     if (e == cudaSuccess) e = prepare_grouped_gemv();
     if (e == cudaSuccess) e = prepare_grouped_rows();
     return e == cudaSuccess ? prepare_grouped_gemm(pairs) : e;
@@ -93,6 +93,7 @@ mf_status moe_expert_permutation(const int32_t *expert_ids, int packed, int64_t 
     a.offsets = expert_offsets;
     a.slot_to_row = expanded_idx_to_permuted_idx;
     a.row_to_token = permuted_row_to_token;
+    a.wide_clusters = d->wide_clusters;
     a.programmatic = mf::programmatic_launch();
     return from_launch(
         mf::launch_expert_permutation(a, reinterpret_cast<cudaStream_t>(stream)));

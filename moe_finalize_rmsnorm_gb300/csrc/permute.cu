@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kSumThreads) permuted_row_sum_kernel(RowSumArg
 
 }  // namespace
 
-cudaError_t prepare_permute_kernels() {
+cudaError_t prepare_permute_kernels(bool *wide_clusters) {
     const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
     const int bytes = kPermuteWarps * kMaxExperts * 4;
     cudaError_t e = cudaFuncSetAttribute(permute_one_cta_kernel, attr, bytes);
@@ -313,7 +313,25 @@ cudaError_t prepare_permute_kernels() {
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(permute_count_kernel, attr,
                                  (kMaxChunks + kCountCtas - 1) / kCountCtas * kMaxExperts * 4);
-    return e == cudaSuccess ? cudaFuncSetAttribute(permute_place_kernel, attr, bytes) : e;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(permute_place_kernel, attr, bytes);
+    if (e != cudaSuccess) return e;
+    // clusters of 16 are not portable: whether this device has room for one
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute wide = {};
+    wide.id = cudaLaunchAttributeClusterDimension;
+    wide.val.clusterDim.x = 2 * kCountCtas;
+    wide.val.clusterDim.y = wide.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2 * kCountCtas);
+    cfg.blockDim = dim3(kPermuteThreads);
+    cfg.dynamicSmemBytes = (kMaxChunks + kCountCtas - 1) / kCountCtas * kMaxExperts * 4;
+    cfg.attrs = &wide;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    *wide_clusters =
+        cudaOccupancyMaxActiveClusters(&clusters, permute_count_kernel, &cfg) == cudaSuccess &&
+        clusters > 0;
+    (void)cudaGetLastError();
+    return cudaSuccess;
 }
 
 cudaError_t launch_expert_permutation(const PermuteArgs &a, cudaStream_t s) {
@@ -326,7 +344,7 @@ cudaError_t launch_expert_permutation(const PermuteArgs &a, cudaStream_t s) {
                          warps);
     }
     const int chunks = static_cast<int>(min(a.slots / kChunk, int64_t{kMaxChunks}));
-    const int ctas = a.slots < kManySlots ? kCountCtas : 2 * kCountCtas;
+    const int ctas = a.slots < kManySlots || !a.wide_clusters ? kCountCtas : 2 * kCountCtas;
     cudaError_t e = launch_ex(permute_count_kernel, dim3(ctas), block,
                               sizeof(int32_t) * ((chunks + ctas - 1) / ctas) * a.num_experts, s,
                               ctas, a.programmatic, a, chunks, ctas);
