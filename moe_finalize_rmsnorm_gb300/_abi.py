@@ -78,6 +78,8 @@ class MoeFinalizeError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:   # loaded: no lock on the way to a call
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB):

@@ -9,6 +9,10 @@ import torch
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+# CUDA is initialised by then: the calls' tensors are on the device.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream_ptr(stream, device) -> int:
     if stream is not None:
         return stream.cuda_stream
@@ -19,7 +23,7 @@ def _stream_ptr(stream, device) -> int:
 
 def _on_device(dev: torch.device, fn, *args) -> int:
     """Call fn with dev as the current CUDA device (switching only if needed)."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
+    if dev.index is None or dev.index == _current_device():
         return fn(*args)
     with torch.cuda.device(dev):
         return fn(*args)

@@ -118,18 +118,23 @@ def moe_permuted_row_sum(permuted: torch.Tensor, expanded_idx: torch.Tensor, out
     [rows, >= hidden] (unit last-dim stride, row stride a multiple of 8);
     expanded_idx: int32 [num_tokens, top_k], entries outside the rows contribute
     zero; output: contiguous BF16 or FP32 [num_tokens, hidden].  Returns it."""
-    ld = _rows(permuted, "permuted", tuple(_VALUE_DTYPES))
-    _req(output.dim() == 2 and output.dtype in _VALUE_DTYPES and output.is_contiguous(),
-         "output must be a contiguous 2-D BF16 or FP32 tensor")
-    _req(expanded_idx.dim() == 2, "expanded_idx must be 2-D")
-    _index(expanded_idx, "expanded_idx", (output.shape[0], expanded_idx.shape[1]))
-    _req(permuted.shape[1] >= output.shape[1], "permuted has fewer columns than output")
+    ld = _rows(permuted, "permuted", _VALUE_DTYPES)
+    if output.dim() != 2 or output.dtype not in _VALUE_DTYPES or not output.is_contiguous():
+        raise ValueError("output must be a contiguous 2-D BF16 or FP32 tensor")
+    if expanded_idx.dim() != 2:
+        raise ValueError("expanded_idx must be 2-D")
+    T, hidden = output.shape
+    K = expanded_idx.shape[1]
+    _index(expanded_idx, "expanded_idx", (T, K))
+    rows, width = permuted.shape
+    if width < hidden:
+        raise ValueError("permuted has fewer columns than output")
     dev = output.device
     _same_device(dev, permuted, expanded_idx)
     st = _on_device(dev, lib().moe_permuted_row_sum, permuted.data_ptr(),
-                    _VALUE_DTYPES[permuted.dtype], permuted.shape[0], ld, expanded_idx.data_ptr(),
-                    output.data_ptr(), _VALUE_DTYPES[output.dtype], output.shape[0],
-                    output.shape[1], expanded_idx.shape[1], _stream_ptr(stream, dev))
+                    _VALUE_DTYPES[permuted.dtype], rows, ld, expanded_idx.data_ptr(),
+                    output.data_ptr(), _VALUE_DTYPES[output.dtype], T, hidden, K,
+                    _stream_ptr(stream, dev))
     check(st, "moe_permuted_row_sum")
     return output
 
