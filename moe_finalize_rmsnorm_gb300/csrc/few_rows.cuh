@@ -37,7 +37,9 @@ struct Cursor {
 
 // Host: warps to a column block, as many as make the longest warp's work shortest,
 // counted in stages, a block's beginning and end as two.  `blocks`: column blocks at most
-// (the experts' sizes are known on the device only), `spans`: stages of one.
+// (the experts' sizes are known on the device only), `spans`: stages of one.  Of 1, 2, 3, 4,
+// 5 and 8 warps forced it took the fastest in eight of eight shapes (4-bit, 8 x 4096 x 4096:
+// 21.9, 18.3, 21.3, 18.7, 22.6 and 21.1 us; 20003 x 7168: 37, 23.5, 20.9, 24.9, 23.2, 24.3).
 inline int warps_of_block(int64_t blocks, int spans, int warps, int num_sms) {
     int share = 1;
     int64_t best = INT64_MAX;

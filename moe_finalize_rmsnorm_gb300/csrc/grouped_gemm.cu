@@ -700,6 +700,9 @@ cudaError_t prepare_grouped_gemm(int *pairs) {
 
 cudaError_t launch_grouped_gemm(const GroupedArgs &a, cudaStream_t s) {
     if (a.kind == kForward && few_rows(a.rows, a.num_experts)) return launch_grouped_rows(a, s);
+    // Up to 128 columns single CTAs: half of a pair's tile would be empty (32768 rows of 4096
+    // values: 128 columns 58.7 against 61.1 us, 64 columns 55.9 against 60.1; at 256 columns
+    // 93 against 65).
     const bool narrow = (a.kind == kForward ? a.n : a.k) <= 128;
     if (a.out_fp32) return narrow ? launch_ctas<1, true>(a, s) : launch_ctas<2, true>(a, s);
     return narrow ? launch_ctas<1, false>(a, s) : launch_ctas<2, false>(a, s);
