@@ -51,8 +51,9 @@
  *     gave up waits once more (also bounded) for its copies in flight, but if
  *     that wait gives up too, a bulk copy may still land in shared memory that
  *     another CTA then uses.  Discard the results and the CUDA context.
- *   - The first call on a device sets kernel attributes; make it before any
- *     CUDA graph capture.  Captured calls replay with their arguments baked in.
+ *   - The first call on a device (of the permutation, of the grouped products
+ *     and of the 4-bit product, each its first) sets kernel attributes; make it
+ *     before any CUDA graph capture.  Captured calls replay with their arguments baked in.
  */
 #ifndef MOE_FINALIZE_H
 #define MOE_FINALIZE_H

@@ -8,7 +8,6 @@
 #include "moe_finalize.h"
 #include "common.cuh"
 #include "device_info.h"
-#include "experts.h"
 #include "kernels.h"
 
 namespace {
@@ -85,7 +84,6 @@ mf_status device_info(const DeviceInfo **out) {
                 cudaSuccess ||
             mf::prepare_tp_kernels(d.smem_optin, d.smem_per_sm) != cudaSuccess ||
             mf::prepare_beam_kernels(d.smem_per_sm) != cudaSuccess ||
-            mf::prepare_expert_kernels(&d.num_pairs, &d.wide_clusters) != cudaSuccess ||
             mf::tp_blocks_per_sm(&d.bulk_per_sm, &d.token_cta_per_sm) != cudaSuccess) {
             (void)cudaGetLastError();
             return MF_ERR_CUDA;

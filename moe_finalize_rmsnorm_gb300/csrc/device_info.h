@@ -14,8 +14,6 @@ struct DeviceInfo {
     int smem_per_sm = 0;
     int bulk_per_sm = 0;       // resident CTAs per SM of the staged hidden-4096 kernel
     int token_cta_per_sm = 0;  // and of the register kernel
-    int num_pairs = 0;         // resident pairs of SMs of the grouped products
-    bool wide_clusters = false;  // clusters of 16 CTAs run
     unsigned *status = nullptr;  // device address of the status word
 };
 

@@ -100,10 +100,13 @@ struct GemvArgs {
     bool programmatic;
 };
 
-// Per-device one-time set-up (kernel attributes); `pairs`: clusters of two CTAs
-// of the grouped product that the device runs at once; `wide_clusters`: whether it
-// runs clusters of 16.
-cudaError_t prepare_expert_kernels(int *pairs, bool *wide_clusters);
+// Per-device one-time set-up of each family (kernel attributes).  `wide_clusters`:
+// whether the device runs clusters of 16; `pairs`: clusters of two CTAs of the grouped
+// product that it runs at once.
+cudaError_t prepare_permute_kernels(bool *wide_clusters);
+cudaError_t prepare_grouped_gemm(int *pairs);
+cudaError_t prepare_grouped_rows();
+cudaError_t prepare_grouped_gemv();
 
 cudaError_t launch_expert_permutation(const PermuteArgs &a, cudaStream_t s);
 cudaError_t launch_permuted_row_sum(const RowSumArgs &a, cudaStream_t s);

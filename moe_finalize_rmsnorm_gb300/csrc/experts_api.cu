@@ -2,23 +2,11 @@
 // Declarations and the contract are in include/moe_finalize.h.
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "device_info.h"
 #include "experts.h"
 #include "moe_finalize.h"
-
-namespace mf {
-cudaError_t prepare_permute_kernels(bool *wide_clusters);
-cudaError_t prepare_grouped_gemm(int *pairs);
-cudaError_t prepare_grouped_gemv();
-cudaError_t prepare_grouped_rows();
-
-cudaError_t prepare_expert_kernels(int *pairs, bool *wide_clusters) {
-    cudaError_t e = prepare_permute_kernels(wide_clusters);
-    if (e == cudaSuccess) e = prepare_grouped_gemv();
-    if (e == cudaSuccess) e = prepare_grouped_rows();
-    return e == cudaSuccess ? prepare_grouped_gemm(pairs) : e;
-}
-}  // namespace mf
 
 namespace {
 
@@ -51,13 +39,55 @@ mf_status check_experts(int32_t num_experts, int32_t n, int32_t k) {
     return MF_OK;
 }
 
+// Each family's kernels are set up on its first call on a device, so that a call of
+// another operation pays nothing for them.
+enum Family { kPermutation = 1, kProducts = 2, kInt4 = 4 };
+
+struct ExpertDevice {
+    unsigned ready = 0;          // families
+    bool wide_clusters = false;  // clusters of 16 CTAs run
+    int num_pairs = 0;           // resident pairs of SMs of the grouped products
+};
+
+constexpr int kMaxDevices = 64;
+std::mutex g_expert_mutex;
+ExpertDevice g_expert_devices[kMaxDevices];
+
+mf_status expert_device(Family family, const mf::DeviceInfo **info, const ExpertDevice **out) {
+    const mf_status st = mf::device_info(info);
+    if (st != MF_OK) return st;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MF_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_expert_mutex);
+    ExpertDevice &d = g_expert_devices[dev];
+    if (!(d.ready & family)) {
+        cudaError_t e = cudaSuccess;
+        if (family == kPermutation) {
+            e = mf::prepare_permute_kernels(&d.wide_clusters);
+        } else if (family == kProducts) {
+            e = mf::prepare_grouped_gemm(&d.num_pairs);
+            if (e == cudaSuccess) e = mf::prepare_grouped_rows();
+        } else {
+            e = mf::prepare_grouped_gemv();
+        }
+        if (e != cudaSuccess) {
+            (void)cudaGetLastError();
+            return MF_ERR_CUDA;
+        }
+        d.ready |= family;
+    }
+    *out = &d;
+    return MF_OK;
+}
+
 // The facts every grouped launch needs.
 mf_status fill(mf::GroupedArgs &a) {
     const mf::DeviceInfo *d = nullptr;
-    mf_status st = mf::device_info(&d);
+    const ExpertDevice *x = nullptr;
+    mf_status st = expert_device(kProducts, &d, &x);
     if (st != MF_OK) return st;
     a.num_sms = d->num_sms;
-    a.num_pairs = d->num_pairs;
+    a.num_pairs = x->num_pairs;
     a.status = d->status;
     a.timeout_ns = mf::kWaitLimitNs;
     a.programmatic = mf::programmatic_launch();
@@ -82,7 +112,8 @@ mf_status moe_expert_permutation(const int32_t *expert_ids, int packed, int64_t 
         !aligned(expanded_idx_to_permuted_idx, 16) || !aligned(permuted_row_to_token, 16))
         return MF_ERR_ALIGN;
     const mf::DeviceInfo *d = nullptr;
-    mf_status st = mf::device_info(&d);
+    const ExpertDevice *x = nullptr;
+    mf_status st = expert_device(kPermutation, &d, &x);
     if (st != MF_OK) return st;
     mf::PermuteArgs a = {};
     a.ids = expert_ids;
@@ -93,7 +124,7 @@ mf_status moe_expert_permutation(const int32_t *expert_ids, int packed, int64_t 
     a.offsets = expert_offsets;
     a.slot_to_row = expanded_idx_to_permuted_idx;
     a.row_to_token = permuted_row_to_token;
-    a.wide_clusters = d->wide_clusters;
+    a.wide_clusters = x->wide_clusters;
     a.programmatic = mf::programmatic_launch();
     return from_launch(
         mf::launch_expert_permutation(a, reinterpret_cast<cudaStream_t>(stream)));
@@ -278,7 +309,8 @@ mf_status moe_grouped_gemv_int4(const void *x, int64_t x_rows, int64_t x_stride,
         !aligned(expert_offsets, 4) || !aligned(row_index, 4) || !aligned(zeros, 4))
         return MF_ERR_ALIGN;
     const mf::DeviceInfo *d = nullptr;
-    mf_status st = mf::device_info(&d);
+    const ExpertDevice *e = nullptr;
+    mf_status st = expert_device(kInt4, &d, &e);
     if (st != MF_OK) return st;
     mf::GemvArgs a = {};
     a.x = x;

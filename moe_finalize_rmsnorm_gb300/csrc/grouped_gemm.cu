@@ -668,17 +668,21 @@ bool encode_map(CUtensorMap *m, CUtensorMapDataType type, const void *p, int ran
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+cudaError_t find_encoder() {
+    if (g_encode) return cudaSuccess;
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    g_encode = reinterpret_cast<EncodeFn>(fn);
+    return cudaSuccess;
+}
+
 cudaError_t prepare_grouped_gemm(int *pairs) {
-    if (!g_encode) {
-        void *fn = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                                         cudaEnableDefault, &found);
-        if (e != cudaSuccess) return e;
-        if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-        g_encode = reinterpret_cast<EncodeFn>(fn);
-    }
-    cudaError_t e = prepare_ctas<1, false>();
+    cudaError_t e = find_encoder();
+    if (e == cudaSuccess) e = prepare_ctas<1, false>();
     if (e == cudaSuccess) e = prepare_ctas<1, true>();
     if (e == cudaSuccess) e = prepare_ctas<2, false>();
     if (e == cudaSuccess) e = prepare_ctas<2, true>();

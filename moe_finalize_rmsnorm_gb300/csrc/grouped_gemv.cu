@@ -572,7 +572,8 @@ static cudaError_t prepare_group() {
 }
 
 cudaError_t prepare_grouped_gemv() {
-    cudaError_t e = prepare_group<32>();
+    cudaError_t e = find_encoder();
+    if (e == cudaSuccess) e = prepare_group<32>();
     if (e == cudaSuccess) e = prepare_group<64>();
     return e == cudaSuccess ? prepare_group<128>() : e;
 }

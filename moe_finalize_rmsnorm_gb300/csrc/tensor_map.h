@@ -2,9 +2,13 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace mf {
+
+// Find the driver's encoder (once, before the first map; not thread-safe by itself).
+cudaError_t find_encoder();
 
 // Map of a row-major tensor of `rank` 2 or 3: sizes fastest first, byte strides of
 // the slower dimensions, boxes of `columns` (128 bytes, stored with the 128-byte
