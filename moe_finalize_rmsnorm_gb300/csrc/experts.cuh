@@ -85,6 +85,11 @@ __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, ui
     return true;
 }
 
+// Arrive on a barrier of this CTA.
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // One lane of the warp, the same one every time, known to the compiler as one:
 // the asynchronous copies and products take their operands from uniform
 // registers, and code that several lanes might enter is issued lane by lane.

@@ -76,7 +76,7 @@ struct Warps {
 // Shared memory behind the stages and the epilogue's blocks.
 struct Control {
     int4 list[256];              // rows by number, four a copy; a part for each gathering warp
-    uint64_t full[6], empty[6], acc_full[2], acc_empty[2];
+    uint64_t full[6], empty[6], tail[6], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int scan[kScanThreads / 32];
     int tiles[kMaxExperts + 1];  // row tiles of the experts before this one
@@ -230,13 +230,14 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
     Control &c = *reinterpret_cast<Control *>(blocks + 8 * kTurnBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
-    const uint32_t full = smem_u32(c.full), empty = smem_u32(c.empty);
+    const uint32_t full = smem_u32(c.full), empty = smem_u32(c.empty), tail = smem_u32(c.tail);
     const uint32_t acc_full = smem_u32(c.acc_full), acc_empty = smem_u32(c.acc_empty);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
+            mbar_init(tail + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
@@ -401,6 +402,8 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
                             for (int i = 0; i < half; i += 64)
                                 tma_2d<PAIR>(sb + i / 64 * 8192, &maps.b, b0 + i, r, bar);
                         }
+                        // the stage is free for warp 2's copies
+                        if (KIND == kWgrad && !GATHER && !whole) mbar_arrive(tail + 8 * stage);
                     }
                     __syncwarp();
                 }
@@ -537,30 +540,36 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
                 done += d.steps;
             }
         } else if (KIND == kWgrad && !GATHER && warp == 2) {
-            // The step that holds a sum's last rows, by number.
-            uint32_t it = 0;
-            for (int t = first_tile; t < tiles && ok; t += tile_step) {
+            // The step that holds a sum's last rows, by number.  Warp 0 says when its stage is
+            // free: `empty` moves on at every step, whether this warp has seen it or not, and
+            // a parity wait that is a phase late does not end.  A stage's `tail` cannot move
+            // on without this warp: its next phase needs the stage again, which needs this
+            // warp's copies.
+            uint32_t it = 0;       // steps up to this tile's end
+            uint32_t phases = 0;   // bit s: parity of stage s's next tail
+            for (int t = first_tile; t < tiles; t += tile_step) {
                 const Tile d = tile_of<KIND, CTAS>(a, c, t);
+                it += d.steps;
+                if (d.summed % kStep == 0) continue;
+                const uint32_t stage = (it - 1) % kStages;
+                ok = __all_sync(0xffffffffu, mbar_wait_long(tail + 8 * stage, phases >> stage & 1,
+                                                       a.timeout_ns));
+                if (!ok) break;
+                phases ^= 1u << stage;
                 const int half = d.n / CTAS;
                 const int m0 = d.m0 + rank * 128;
                 const int row_end = d.sum0 + d.summed;
-                for (int s = 0; s < d.steps; ++s, ++it) {
-                    const uint32_t stage = it % kStages;
-                    ok = __all_sync(0xffffffffu, mbar_wait_long(empty + 8 * stage, (it / kStages & 1) ^ 1,
-                                                           a.timeout_ns));
-                    if (!ok) break;
-                    const uint32_t bar = full_at + 8 * stage;
-                    const uint32_t sa = base + stage * S::kStageBytes, sb = sa + kABytes;
-                    const int r0 = d.sum0 + s * kStep;
-                    if ((s + 1) * kStep > d.summed && elect_one()) {
-                        for (int q = 0; q < kStep / 4; ++q)
-                            for (int h = 0; h < 2; ++h)
-                                tma_gather4<PAIR>(sa + h * 8192 + q * 512, &maps.a4, m0 + 64 * h,
-                                                  rows_until(r0 + 4 * q, row_end), bar);
-                        dy_tail<PAIR>(maps, sb, r0, row_end, d.row0 + rank * half, half, 0, 1, bar);
-                    }
-                    __syncwarp();
+                const uint32_t bar = full_at + 8 * stage;
+                const uint32_t sa = base + stage * S::kStageBytes, sb = sa + kABytes;
+                const int r0 = d.sum0 + (d.steps - 1) * kStep;
+                if (elect_one()) {
+                    for (int q = 0; q < kStep / 4; ++q)
+                        for (int h = 0; h < 2; ++h)
+                            tma_gather4<PAIR>(sa + h * 8192 + q * 512, &maps.a4, m0 + 64 * h,
+                                              rows_until(r0 + 4 * q, row_end), bar);
+                    dy_tail<PAIR>(maps, sb, r0, row_end, d.row0 + rank * half, half, 0, 1, bar);
                 }
+                __syncwarp();
             }
         }
         if (!ok && lane == 0) atomicOr(a.status, kStatusWaitTimeout);
