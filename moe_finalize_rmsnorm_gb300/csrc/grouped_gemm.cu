@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
             const int col0 = d.m0 + rank * 128 + w * 32;
             const int cols = columns - col0;  // what exists of the warp's 32
             auto take = [&]() {  // wait for the next accumulator
-                ok = __all_sync(0xffffffffu, mbar_wait_long(acc_full + 8 * (acc_n & 1),
+                ok = __all_sync(0xffffffffu, mbar_wait_long<PAIR>(acc_full + 8 * (acc_n & 1),
                                                             acc_n >> 1 & 1, a.timeout_ns));
                 tcgen05_fence_after();
                 return lanes + (acc_n & 1) * kRowsMax;
@@ -379,7 +379,8 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
                 for (int s = 0; s < d.steps; ++s, ++it) {
                     const uint32_t stage = it % kStages, phase = it / kStages & 1;
                     // all lanes give up together: the warp meets again below
-                    ok = __all_sync(0xffffffffu, mbar_wait_long(empty + 8 * stage, phase ^ 1, a.timeout_ns));
+                    ok = __all_sync(0xffffffffu, mbar_wait_long<PAIR>(empty + 8 * stage, phase ^ 1,
+                                                                     a.timeout_ns));
                     if (!ok) break;
                     const uint32_t bar = full_at + 8 * stage;
                     const uint32_t sa = base + stage * S::kStageBytes, sb = sa + kABytes;
@@ -413,12 +414,14 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
             if (ok)
                 for (uint32_t i = 0; i < kStages && i < it; ++i) {
                     const uint32_t p = it - 1 - i;
-                    ok = ok && mbar_wait_long(empty + 8 * (p % kStages), p / kStages & 1, a.timeout_ns);
+                    ok = ok && mbar_wait_long<PAIR>(empty + 8 * (p % kStages), p / kStages & 1,
+                                                    a.timeout_ns);
                 }
             if (!ok && rank == 0)  // the copies in flight, before the memory is given back
                 for (uint32_t i = 0; i < kStages && i < it; ++i) {
                     const uint32_t p = it - 1 - i;
-                    (void)mbar_wait_long(full + 8 * (p % kStages), p / kStages & 1, a.timeout_ns);
+                    (void)mbar_wait_long<PAIR>(full + 8 * (p % kStages), p / kStages & 1,
+                                               a.timeout_ns);
                 }
         } else if (warp == 1 && rank == 0) {
             // Products.
@@ -430,13 +433,14 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
                 for (int s = 0; s < d.steps; ++s, ++it) {
                     const int in_segment = FP32 ? s % kSegment : s;
                     if (in_segment == 0) {
-                        ok = __all_sync(0xffffffffu, mbar_wait_long(acc_empty + 8 * (acc_n & 1),
-                                                               (acc_n >> 1 & 1) ^ 1, a.timeout_ns));
+                        ok = __all_sync(0xffffffffu,
+                                        mbar_wait_long<PAIR>(acc_empty + 8 * (acc_n & 1),
+                                                             (acc_n >> 1 & 1) ^ 1, a.timeout_ns));
                         if (!ok) break;
                     }
                     const uint32_t stage = it % kStages;
-                    ok = __all_sync(0xffffffffu, mbar_wait_long(full + 8 * stage, it / kStages & 1,
-                                                           a.timeout_ns));
+                    ok = __all_sync(0xffffffffu, mbar_wait_long<PAIR>(full + 8 * stage,
+                                                                     it / kStages & 1, a.timeout_ns));
                     if (!ok) break;
                     tcgen05_fence_after();
                     const uint32_t sa = base + stage * S::kStageBytes, sb = sa + kABytes;
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
                             reinterpret_cast<int *>(list)[i] = x_row(d.sum0 + c0 + i);
                         __syncwarp();
                     }
-                    ok = __all_sync(0xffffffffu, mbar_wait_long(empty + 8 * stage,
+                    ok = __all_sync(0xffffffffu, mbar_wait_long<PAIR>(empty + 8 * stage,
                                                            (it / kStages & 1) ^ 1, a.timeout_ns));
                     if (!ok) break;
                     if (elect_one()) {

@@ -208,3 +208,14 @@ def test_the_kernel_has_the_rule_of_the_model():
     role = text[text.index("KIND == kWgrad && !GATHER && warp == 2"):]
     waits = re.findall(r"mbar_wait_long\((\w+) \+", role[:role.index("atomicOr")])
     assert waits == ["tail"]
+
+
+def test_signals_between_the_ctas_of_a_pair_have_cluster_scope():
+    """Every barrier but `tail` is signalled by the other CTA of a pair too."""
+    waits = re.findall(r"mbar_wait_long(<PAIR>)?\((\w+) \+", open(SOURCE).read())
+    assert {bar for _, bar in waits} == {"full", "empty", "tail", "acc_full", "acc_empty"}
+    assert all((scope == "<PAIR>") == (bar != "tail") for scope, bar in waits)
+    helpers = open(SOURCE.replace("grouped_gemm.cu", "experts.cuh")).read()
+    arrive = helpers[helpers.index("void mbar_arrive_cluster"):]
+    assert re.search(r"mbarrier\.arrive\.\w+\.(\w+)", arrive).group(1) == "cluster"
+    assert "try_wait.parity.acquire.cluster" in helpers
