@@ -312,8 +312,14 @@ mf_status moe_permuted_row_sum(const void *permuted, mf_dtype permuted_dtype, in
  *
  *   output[r, :] = weight[e] . x[i(r), :]     i(r) = row_index[r], or r
  *
- * with FP32 accumulation, rounded once.  Rows outside every expert are left as
- * they were.
+ * accumulated in FP32, rounded once.  Rows outside every expert are left as they
+ * were.  The tensor cores truncate their FP32 partial sums, towards zero.  For
+ * FP32 results, and for every sum of more than 32768 values, the sums leave the
+ * tensor cores every 640 values: C summed values are within
+ * (40 + C / 640) * 2^-22 of the sum of the terms' magnitudes, and a rounding
+ * (measured: 1e-6 at 4096 values of one sign, 5e-8 at 4096 of either sign).  For
+ * the other BF16 results they are within C / 16 * 2^-22 (measured: 1.1e-5 at 4096
+ * values of one sign, 1.6e-4 at 32768), beside the rounding's 2^-8 of the value.
  *
  *   x                device, BF16 [x_rows, x_stride], columns [0, k) used.
  *   row_index        device, int32 [rows], or NULL (row r reads row r of x and
@@ -374,8 +380,8 @@ mf_status moe_grouped_gemm_dgrad(const void *grad_output, int64_t grad_output_st
  *
  *   grad_weight      device, BF16 or FP32 [num_experts, n, k] contiguous,
  *                    16-byte aligned.
- *   The rest, and the errors, as for moe_grouped_gemm.  Zero rows: the zeros
- *   are written (nothing with `accumulate`).
+ *   The rest, and the errors, as for moe_grouped_gemm, the sums being over an
+ *   expert's rows.  Zero rows: the zeros are written (nothing with `accumulate`).
  */
 mf_status moe_grouped_gemm_wgrad(const void *grad_output, int64_t grad_output_stride, const void *x,
                                  int64_t x_rows, int64_t x_stride, const int32_t *row_index,

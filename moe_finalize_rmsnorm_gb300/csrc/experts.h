@@ -69,6 +69,7 @@ struct GroupedArgs {
     int out_fp32;
     int64_t out_ld;          // forward, dgrad
     int accumulate;          // wgrad: add to what out holds
+    int sum_from, sum_to;    // wgrad: experts with so many rows (set by the launch)
     int num_sms;
     int num_pairs;           // pairs of SMs that run at once
     unsigned *status;

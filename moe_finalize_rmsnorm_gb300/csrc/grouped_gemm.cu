@@ -46,11 +46,16 @@ constexpr int kTmemColumns = 512;           // two accumulators of 256
 constexpr int kTurnBytes = 2048;            // an epilogue warp's block to turn results in
 constexpr int kScanThreads = 256;           // threads that scan the experts
 
-// FP32 results: sums are moved out of TMEM and added up in registers every this
-// many steps.  The tensor cores truncate each partial sum, an error that grows with
-// the products added to one accumulator (some 1.8e-8 of the result per 16 summed
-// values); 640 summed values keep it under 1e-6.  BF16 results round off 2e-3.
+// Moved sums: moved out of TMEM and added up in registers every this many steps.  The
+// tensor cores truncate each partial sum, an error that grows with the products added to
+// one accumulator: every 16 summed values lose up to 9e-8 of it, towards zero (values of
+// one sign: 4096 of them 1.1e-5 of the sum, 32768 1.6e-4, 2^20 6.1e-3; of either sign the
+// losses cancel for the most part).  640 summed values keep it near 1e-6, the plain
+// additions' own error.  FP32 results are made so.
 constexpr int kSegment = 10;
+// BF16 results of more than this many summed values are, too.  Up to it one accumulator
+// takes the whole sum: 1.6e-4 beside the rounding's 2^-8.
+constexpr int kLongSum = 32768;
 
 template <int CTAS>
 struct Shape {
@@ -61,14 +66,15 @@ struct Shape {
 
 // Warps: 0 block copies, 1 products, from 4 on the epilogue, then those that gather
 // (with 2 and 3, which otherwise only copy the last rows of a sum).
-template <int CTAS, bool FP32, bool GATHER>
+// SUMS: the sums are moved (kSegment).
+template <int CTAS, bool SUMS, bool GATHER>
 struct Warps {
-    static constexpr int kEpilogue = FP32 ? 8 : 4;
+    static constexpr int kEpilogue = SUMS ? 8 : 4;
     static constexpr int kFirstGather = 4 + kEpilogue;
-    static constexpr int kShare = FP32 ? 1 : 2;  // gathering warps of a stage
-    // 512 threads with FP32 sums: whole warpgroups, as the register split needs
+    static constexpr int kShare = SUMS ? 1 : 2;  // gathering warps of a stage
+    // 512 threads with moved sums: whole warpgroups, as the register split needs
     static constexpr int kAll = !GATHER ? kFirstGather
-                                : FP32  ? 16
+                                : SUMS  ? 16
                                         : kFirstGather + kShare * Shape<CTAS>::kStages - 2;
     static constexpr int kThreads = 32 * kAll;
 };
@@ -79,7 +85,7 @@ struct Control {
     uint64_t full[6], empty[6], tail[6], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int scan[kScanThreads / 32];
-    int tiles[kMaxExperts + 1];  // row tiles of the experts before this one
+    int tiles[kMaxExperts + 1];  // row tiles of the experts before this one; wgrad: rows summed
     int lo[kMaxExperts + 1];     // first row; the next expert's is the end
 };
 
@@ -117,7 +123,7 @@ __device__ __forceinline__ Tile tile_of(const GroupedArgs &a, const Control &c, 
         r.m0 = local % mt * M;
         r.row0 = local / mt * kRowsMax;
         r.nrows = min(kRowsMax, a.n - r.row0);
-        r.summed = max(c.lo[r.expert + 1] - c.lo[r.expert], 0);
+        r.summed = c.tiles[r.expert];
         r.sum0 = c.lo[r.expert];
     } else {
         const int u = t / mt;
@@ -165,7 +171,7 @@ __device__ __forceinline__ void store16(const GroupedArgs &a, uint8_t *block, in
             }
             *o = x;
         }
-    } else {  // BF16 that is added to: the sum is rounded once
+    } else {  // BF16 of a long sum, or that is added to: rounded once
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = i * 8 + lane / 4, col = lane % 4 * 8;
@@ -173,7 +179,7 @@ __device__ __forceinline__ void store16(const GroupedArgs &a, uint8_t *block, in
             uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + out + r * ld +
                                                  col);
             float y[8];
-            unpack8(*o, y);
+            unpack8(a.accumulate ? *o : make_uint4(0, 0, 0, 0), y);
 #pragma unroll
             for (int u = 0; u < 8; ++u) y[u] += f[r * 32 + col + u];
             *o = pack8_rn(y);
@@ -217,11 +223,11 @@ __device__ __forceinline__ void dy_tail(const Maps &maps, uint32_t sb, int r0, i
                               rows_until(r0 + 4 * q, end), bar);
 }
 
-template <int KIND, int CTAS, bool GATHER, bool FP32>
-__global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
+template <int KIND, int CTAS, bool GATHER, bool SUMS>
+__global__ void __launch_bounds__(Warps<CTAS, SUMS, GATHER>::kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ Maps maps, const GroupedArgs a) {
     using S = Shape<CTAS>;
-    using W = Warps<CTAS, FP32, GATHER>;
+    using W = Warps<CTAS, SUMS, GATHER>;
     constexpr bool PAIR = CTAS == 2;
     constexpr int kStages = S::kStages;
     extern __shared__ uint8_t raw[];
@@ -251,6 +257,14 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
 
     const int total = scan_experts<kScanThreads>(a.offsets, a.num_experts, static_cast<int>(a.rows),
                                                  kRowsMax, c.lo, c.tiles, c.scan);
+    if (KIND == kWgrad) {  // by the thread that scanned the expert
+        const int per = divide_up(a.num_experts, kScanThreads);
+        const int first = min(static_cast<int>(threadIdx.x) * per, a.num_experts);
+        for (int e = first; e < min(first + per, a.num_experts); ++e) {
+            const int rows = max(c.lo[e + 1] - c.lo[e], 0);
+            c.tiles[e] = rows >= a.sum_from && rows <= a.sum_to ? rows : 0;
+        }
+    }
     tcgen05_fence_before();
     __syncthreads();
     if (PAIR) cluster_barrier();
@@ -259,12 +273,18 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
 
     const int columns = KIND == kForward ? a.n : a.k;
     const int mt = divide_up(columns, S::kM);
-    const int tiles = mt * (KIND == kWgrad ? a.num_experts * divide_up(a.n, kRowsMax) : total);
+    int tiles = mt * (KIND == kWgrad ? a.num_experts * divide_up(a.n, kRowsMax) : total);
+    if (KIND == kWgrad && SUMS && a.sum_from > 0) {  // seldom has any expert so many rows
+        bool any = false;
+        for (int e = threadIdx.x; e < a.num_experts; e += W::kThreads)
+            any |= c.tiles[e] > 0;
+        if (!__syncthreads_or(any)) tiles = 0;
+    }
     const int first_tile = blockIdx.x / CTAS, tile_step = gridDim.x / CTAS;
 
-    // Registers: the warps that hold FP32 sums take some of the others'
+    // Registers: the warps that hold the moved sums take some of the others'
     // (8 * 32 * 176 + 8 * 32 * 80 = the launch's 512 * 128).
-    constexpr bool kMoveRegisters = FP32 && GATHER;
+    constexpr bool kMoveRegisters = SUMS && GATHER;
     static_assert(!kMoveRegisters || W::kThreads == 512, "register split");
 
     if (warp >= 4 && warp < W::kFirstGather) {
@@ -281,7 +301,8 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
         for (int t = first_tile; t < tiles && ok; t += tile_step) {
             const Tile d = tile_of<KIND, CTAS>(a, c, t);
             const bool none = d.steps == 0;
-            if (none && a.accumulate) continue;
+            // nothing to add, or another launch's
+            if (none && (a.accumulate || c.lo[d.expert + 1] > c.lo[d.expert])) continue;
             const int64_t ld = KIND == kWgrad ? a.k : a.out_ld;
             const int64_t row0 = KIND == kWgrad ? int64_t{d.expert} * a.n + d.row0 : d.row0;
             const int col0 = d.m0 + rank * 128 + w * 32;
@@ -298,7 +319,7 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
                 if (lane == 0) mbar_arrive_cluster(done_at + 8 * (acc_n & 1));
                 ++acc_n;
             };
-            if constexpr (FP32) {
+            if constexpr (SUMS) {
                 constexpr int kChunks = kRowsMax / 32 / kGroups;
                 float sums[kChunks][32];
 #pragma unroll
@@ -431,7 +452,7 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
                 const Tile d = tile_of<KIND, CTAS>(a, c, t);
                 const uint32_t idesc = instr_desc(S::kM, d.n, A_MN, B_MN);
                 for (int s = 0; s < d.steps; ++s, ++it) {
-                    const int in_segment = FP32 ? s % kSegment : s;
+                    const int in_segment = SUMS ? s % kSegment : s;
                     if (in_segment == 0) {
                         ok = __all_sync(0xffffffffu,
                                         mbar_wait_long<PAIR>(acc_empty + 8 * (acc_n & 1),
@@ -450,7 +471,7 @@ __global__ void __launch_bounds__(Warps<CTAS, FP32, GATHER>::kThreads, 1)
                     const uint64_t da = smem_desc(sa, A_MN ? 8192 : 16, 1024);
                     const uint64_t db = smem_desc(sb, B_MN ? 8192 : 16, 1024);
                     const int parts = (min(kStep, d.summed - s * kStep) + 15) / 16;
-                    const bool end = s + 1 == d.steps || (FP32 && in_segment == kSegment - 1);
+                    const bool end = s + 1 == d.steps || (SUMS && in_segment == kSegment - 1);
                     if (elect_one()) {
 #pragma unroll
                         for (int p = 0; p < 4; ++p)
@@ -603,16 +624,16 @@ bool encode(CUtensorMap *m, const void *p, int rank, const cuuint64_t (&sizes)[3
         rows);
 }
 
-template <int KIND, int CTAS, bool GATHER, bool FP32>
+template <int KIND, int CTAS, bool GATHER, bool SUMS>
 cudaError_t launch(const Maps &maps, const GroupedArgs &a, int64_t tiles, cudaStream_t s) {
     const unsigned ctas =
         static_cast<unsigned>(CTAS * min(tiles, int64_t{CTAS == 2 ? a.num_pairs : a.num_sms}));
-    return launch_ex(grouped_gemm_kernel<KIND, CTAS, GATHER, FP32>, dim3(ctas),
-                     dim3(Warps<CTAS, FP32, GATHER>::kThreads), kSmemBytes, s, CTAS, a.programmatic, maps,
+    return launch_ex(grouped_gemm_kernel<KIND, CTAS, GATHER, SUMS>, dim3(ctas),
+                     dim3(Warps<CTAS, SUMS, GATHER>::kThreads), kSmemBytes, s, CTAS, a.programmatic, maps,
                      a);
 }
 
-template <int CTAS, bool FP32>
+template <int CTAS, bool SUMS>
 cudaError_t launch_ctas(const GroupedArgs &a, cudaStream_t s) {
     using u64 = cuuint64_t;
     constexpr int kM = 128 * CTAS;
@@ -643,28 +664,28 @@ cudaError_t launch_ctas(const GroupedArgs &a, cudaStream_t s) {
     if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
     switch (a.kind) {
         case kForward:
-            return a.row_index ? launch<kForward, CTAS, true, FP32>(m, a, tiles, s)
-                               : launch<kForward, CTAS, false, FP32>(m, a, tiles, s);
-        case kDgrad: return launch<kDgrad, CTAS, false, FP32>(m, a, tiles, s);
+            return a.row_index ? launch<kForward, CTAS, true, SUMS>(m, a, tiles, s)
+                               : launch<kForward, CTAS, false, SUMS>(m, a, tiles, s);
+        case kDgrad: return launch<kDgrad, CTAS, false, SUMS>(m, a, tiles, s);
         default:
-            return a.row_index ? launch<kWgrad, CTAS, true, FP32>(m, a, tiles, s)
-                               : launch<kWgrad, CTAS, false, FP32>(m, a, tiles, s);
+            return a.row_index ? launch<kWgrad, CTAS, true, SUMS>(m, a, tiles, s)
+                               : launch<kWgrad, CTAS, false, SUMS>(m, a, tiles, s);
     }
 }
 
-template <int CTAS, bool FP32>
+template <int CTAS, bool SUMS>
 cudaError_t prepare_ctas() {
     const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
     cudaError_t e =
-        cudaFuncSetAttribute(grouped_gemm_kernel<kForward, CTAS, false, FP32>, attr, kSmemBytes);
+        cudaFuncSetAttribute(grouped_gemm_kernel<kForward, CTAS, false, SUMS>, attr, kSmemBytes);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(grouped_gemm_kernel<kForward, CTAS, true, FP32>, attr, kSmemBytes);
+        e = cudaFuncSetAttribute(grouped_gemm_kernel<kForward, CTAS, true, SUMS>, attr, kSmemBytes);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(grouped_gemm_kernel<kDgrad, CTAS, false, FP32>, attr, kSmemBytes);
+        e = cudaFuncSetAttribute(grouped_gemm_kernel<kDgrad, CTAS, false, SUMS>, attr, kSmemBytes);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(grouped_gemm_kernel<kWgrad, CTAS, false, FP32>, attr, kSmemBytes);
+        e = cudaFuncSetAttribute(grouped_gemm_kernel<kWgrad, CTAS, false, SUMS>, attr, kSmemBytes);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(grouped_gemm_kernel<kWgrad, CTAS, true, FP32>, attr, kSmemBytes);
+        e = cudaFuncSetAttribute(grouped_gemm_kernel<kWgrad, CTAS, true, SUMS>, attr, kSmemBytes);
     return e;
 }
 
@@ -721,8 +742,26 @@ cudaError_t launch_grouped_gemm(const GroupedArgs &a, cudaStream_t s) {
     // values: 128 columns 58.7 against 61.1 us, 64 columns 55.9 against 60.1; at 256 columns
     // 93 against 65).
     const bool narrow = (a.kind == kForward ? a.n : a.k) <= 128;
-    if (a.out_fp32) return narrow ? launch_ctas<1, true>(a, s) : launch_ctas<2, true>(a, s);
-    return narrow ? launch_ctas<1, false>(a, s) : launch_ctas<2, false>(a, s);
+    const auto launch_sums = [&](const GroupedArgs &b) {
+        return narrow ? launch_ctas<1, true>(b, s) : launch_ctas<2, true>(b, s);
+    };
+    const auto launch_one = [&](const GroupedArgs &b) {
+        return narrow ? launch_ctas<1, false>(b, s) : launch_ctas<2, false>(b, s);
+    };
+    if (a.kind != kWgrad)
+        return a.out_fp32 || (a.kind == kForward ? a.k : a.n) > kLongSum ? launch_sums(a)
+                                                                         : launch_one(a);
+    // The weights' gradient sums an expert's rows, whose number is known on the device only:
+    // where there may be a long sum, a second launch takes those experts and the first leaves
+    // them out (1.2 us where there are none; that kernel for all of them would cost more:
+    // 16 experts of 2048 rows, 2048 x 4096: 333 us with FP32 results, 295 here).
+    GroupedArgs part = a;
+    part.sum_to = a.out_fp32 ? INT32_MAX : kLongSum;
+    cudaError_t e = a.out_fp32 ? launch_sums(part) : launch_one(part);
+    if (a.out_fp32 || a.rows <= kLongSum || e != cudaSuccess) return e;
+    part.sum_from = kLongSum + 1;
+    part.sum_to = INT32_MAX;
+    return launch_sums(part);
 }
 
 }  // namespace mf
