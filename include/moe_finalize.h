@@ -331,9 +331,10 @@ mf_status moe_permuted_row_sum(const void *permuted, mf_dtype permuted_dtype, in
  *                    weight_row_stride and weight_expert_stride in elements, an
  *                    expert's matrix not overlapping the next.
  *   expert_offsets   device, int32 [num_experts + 1], ascending, 4-byte aligned.
- *                    They are read on the device and brought into [0, rows]:
- *                    values that do not ascend give unspecified rows, and no
- *                    access outside the buffers.
+ *                    They are read on the device and brought into [0, rows].
+ *                    Where they do not ascend then, no row is written (the
+ *                    weights' gradient is unspecified), and nothing outside
+ *                    the buffers is touched.
  *   output           device, BF16 or FP32 [rows, output_stride].
  *   n, k             multiples of 8, 8 .. 2^20.   num_experts  1 .. 1024.
  *   All strides are multiples of 8 elements, at least the row's width; x,

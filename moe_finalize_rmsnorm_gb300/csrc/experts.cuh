@@ -5,20 +5,16 @@
 
 namespace mf {
 
-// Rows [lo, hi) of expert e.  The offsets are device data that the host cannot
-// check, so they are brought into [0, rows] and into order: offsets that do
-// not ascend give wrong rows, never an access outside the buffers.
-__device__ __forceinline__ void expert_rows(const int32_t *offsets, int e, int rows, int &lo,
-                                            int &hi) {
-    lo = min(max(__ldg(offsets + e), 0), rows);
-    hi = min(max(__ldg(offsets + e + 1), lo), rows);
-}
-
 // The experts' rows and the numbers of their passes (of up to `per_pass` rows):
 // lo[e] is the first row, lo[num_experts] the end; passes[e] counts the passes of the
 // experts before e.  Called by the whole CTA, of which `THREADS` threads take a run of
 // experts each; `scratch` holds an int per warp of theirs.  Returns the passes of all
 // experts; the tables are complete after the caller's next barrier.
+//
+// The offsets are device data that the host cannot check, so they are brought into
+// [0, rows], and offsets that do not ascend give no passes at all: experts that overlap
+// could have more of them than 32 bits count, and an item number that wraps around would
+// reach outside the buffers.
 template <int THREADS>
 __device__ __forceinline__ int scan_experts(const int32_t *offsets, int num_experts, int rows,
                                             int per_pass, int *lo, int *passes, int *scratch) {
@@ -27,13 +23,18 @@ __device__ __forceinline__ int scan_experts(const int32_t *offsets, int num_expe
     const int first = min(static_cast<int>(threadIdx.x) * per, num_experts);
     const int last = min(first + per, num_experts);
     int sum = 0;
+    bool ascend = true;
     for (int e = first; e < last; ++e) {
         int l = 0, h = rows;  // without offsets one expert has every row
-        if (offsets) expert_rows(offsets, e, rows, l, h);
+        if (offsets) {
+            l = min(max(__ldg(offsets + e), 0), rows);
+            h = min(max(__ldg(offsets + e + 1), 0), rows);
+        }
+        ascend = ascend && l <= h;
         lo[e] = l;
         if (e + 1 == num_experts) lo[e + 1] = h;
         passes[e] = sum;
-        sum += (h - l + per_pass - 1) / per_pass;
+        if (ascend) sum += (h - l + per_pass - 1) / per_pass;  // a run of up to `rows` rows
     }
     int before = sum;
     for (int o = 1; o < 32; o *= 2) {
@@ -42,7 +43,7 @@ __device__ __forceinline__ int scan_experts(const int32_t *offsets, int num_expe
     }
     if (lane == 31 && warp < THREADS / 32) scratch[warp] = before;
     before -= sum;
-    __syncthreads();
+    if (__syncthreads_or(!ascend)) return 0;
     int total = 0;
     for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) before += scratch[w];
