@@ -71,7 +71,8 @@ typedef enum mf_status {
     MF_OK = 0,
     MF_ERR_NULL = 1,             /* a required pointer is NULL */
     MF_ERR_SHAPE = 2,            /* sizes or strides break the tensor contract */
-    MF_ERR_ALIGN = 3,            /* a pointer breaks the 16-byte (or 4-byte) alignment rule */
+    MF_ERR_ALIGN = 3,            /* a pointer breaks the 16-byte (or 4-byte) alignment rule,
+                                  * or buffers overlap (where the call says so) */
     MF_ERR_DTYPE = 4,            /* unknown weight dtype */
     MF_ERR_UNSUPPORTED = 5,      /* hidden / top_k outside what the operation defines */
     MF_ERR_CUDA = 6,             /* CUDA runtime error (no device, launch failure, ...) */
@@ -274,7 +275,8 @@ mf_status beam_moe_finalize_norm_residual_norm(
  *
  * Zero tokens: expert_offsets is written (zeros), the other pointers are not
  * used.  Errors: MF_ERR_UNSUPPORTED, MF_ERR_SHAPE (num_tokens < 0 or
- * num_tokens * top_k above 2^31 - 1025), MF_ERR_NULL, MF_ERR_ALIGN, MF_ERR_CUDA.
+ * num_tokens * top_k above 2^31 - 1025), MF_ERR_NULL, MF_ERR_ALIGN (also where two
+ * of the four buffers overlap), MF_ERR_CUDA.
  */
 mf_status moe_expert_permutation(const int32_t *expert_ids, int packed, int64_t num_tokens,
                                  int32_t top_k, int32_t num_experts, int32_t *expert_offsets,

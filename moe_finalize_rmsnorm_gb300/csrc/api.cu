@@ -105,7 +105,7 @@ const char *mf_status_string(mf_status s) {
         case MF_OK: return "ok";
         case MF_ERR_NULL: return "a required pointer is NULL";
         case MF_ERR_SHAPE: return "sizes or strides break the tensor contract";
-        case MF_ERR_ALIGN: return "a pointer is not aligned as required";
+        case MF_ERR_ALIGN: return "a pointer is not aligned as required, or buffers overlap";
         case MF_ERR_DTYPE: return "unknown weight dtype";
         case MF_ERR_UNSUPPORTED: return "hidden or top_k outside what the operation defines";
         case MF_ERR_CUDA: return "CUDA runtime error";

@@ -32,6 +32,12 @@ bool weight_strides_ok(int64_t row_stride, int64_t expert_stride, int32_t num_ex
     return num_experts == 1 || expert_stride >= (n - 1) * row_stride + k;
 }
 
+// Whether two buffers share a byte.
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return p < q + static_cast<uintptr_t>(b_bytes) && q < p + static_cast<uintptr_t>(a_bytes);
+}
+
 mf_status check_experts(int32_t num_experts, int32_t n, int32_t k) {
     if (num_experts < 1 || num_experts > mf::kMaxExperts) return MF_ERR_UNSUPPORTED;
     if (n < 8 || n > kMaxWidth || n % 8 != 0 || k < 8 || k > kMaxWidth || k % 8 != 0)
@@ -111,6 +117,15 @@ mf_status moe_expert_permutation(const int32_t *expert_ids, int packed, int64_t 
     if (!aligned(expert_ids, 16) || !aligned(expert_offsets, 4) ||
         !aligned(expanded_idx_to_permuted_idx, 16) || !aligned(permuted_row_to_token, 16))
         return MF_ERR_ALIGN;
+    // A map written over ids that are still to be read would not count them as it places
+    // them: rows outside the buffers.
+    const void *buffers[4] = {expert_ids, expanded_idx_to_permuted_idx, permuted_row_to_token,
+                              expert_offsets};
+    const int64_t slots = 4 * num_tokens * top_k, bytes[4] = {slots, slots, slots,
+                                                              4 * (int64_t{num_experts} + 1)};
+    for (int i = 0; num_tokens > 0 && i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlap(buffers[i], bytes[i], buffers[j], bytes[j])) return MF_ERR_ALIGN;
     const mf::DeviceInfo *d = nullptr;
     const ExpertDevice *x = nullptr;
     mf_status st = expert_device(kPermutation, &d, &x);

@@ -82,7 +82,8 @@ def moe_expert_permutation(expert_ids: torch.Tensor, num_experts: int, *, packed
     expert_ids: contiguous int32 [num_tokens, top_k]; with ``packed`` they are
     routing words ``(expert_id << 16) | bf16 weight bits``.  A slot whose id is
     outside [0, num_experts) gets no row: its map entry is -1, and row_to_token
-    is -1 behind the last row.  The outputs are allocated unless given.
+    is -1 behind the last row.  The outputs are allocated unless given; they may
+    not overlap the ids or each other.
     """
     _req(expert_ids.dim() == 2 and expert_ids.dtype == torch.int32 and expert_ids.is_contiguous(),
          "expert_ids must be a contiguous 2-D int32 tensor")
