@@ -257,7 +257,7 @@ mf_status beam_moe_finalize_norm_residual_norm(
  * one expert keep their order), which gives the index map that
  * moe_finalize_rmsnorm reads and the row order of the grouped products.
  *
- *   expert_ids       device, int32 [num_tokens, top_k] contiguous, 16-byte
+ *   expert_ids       device, int32 [num_tokens, top_k] contiguous, 4-byte
  *                    aligned: expert ids, or with nonzero `packed` routing words
  *                    (expert_id << 16) | weight bits (MF_DTYPE_PACKED_TOPK; the
  *                    id is the high half, unsigned).  A slot whose id is outside
@@ -266,10 +266,11 @@ mf_status beam_moe_finalize_norm_residual_norm(
  *                    the rows of expert e are expert_offsets[e] up to
  *                    expert_offsets[e + 1].
  *   expanded_idx_to_permuted_idx
- *                    device, int32 [num_tokens, top_k], 16-byte aligned,
- *                    written: the row of each slot, -1 for a slot without one.
+ *                    device, int32 [num_tokens, top_k], 4-byte aligned,
+ *                    written: the row of each slot, -1 for a slot without one
+ *                    (moe_finalize_rmsnorm reads it 16-byte aligned).
  *   permuted_row_to_token
- *                    device, int32 [num_tokens * top_k], 16-byte aligned,
+ *                    device, int32 [num_tokens * top_k], 4-byte aligned,
  *                    written: the token of each row, -1 behind the last row.
  *   num_experts, top_k   1 .. 1024 and 1 .. 32.
  *

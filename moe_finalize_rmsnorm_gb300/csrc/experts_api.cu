@@ -114,8 +114,8 @@ mf_status moe_expert_permutation(const int32_t *expert_ids, int packed, int64_t 
     if (!expert_offsets ||
         (num_tokens > 0 && (!expert_ids || !expanded_idx_to_permuted_idx || !permuted_row_to_token)))
         return MF_ERR_NULL;
-    if (!aligned(expert_ids, 16) || !aligned(expert_offsets, 4) ||
-        !aligned(expanded_idx_to_permuted_idx, 16) || !aligned(permuted_row_to_token, 16))
+    if (!aligned(expert_ids, 4) || !aligned(expert_offsets, 4) ||
+        !aligned(expanded_idx_to_permuted_idx, 4) || !aligned(permuted_row_to_token, 4))
         return MF_ERR_ALIGN;
     // A map written over ids that are still to be read would not count them as it places
     // them: rows outside the buffers.

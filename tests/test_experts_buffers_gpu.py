@@ -32,3 +32,23 @@ def test_permutation_in_one_allocation(cuda_lib, T, K, E):
     with pytest.raises(mf.MoeFinalizeError):       # two outputs in one place
         mf.moe_expert_permutation(a, E, expanded_idx=idx, row_tokens=idx.view(-1))
     assert torch.equal(a.cpu(), ids)
+
+
+@pytest.mark.parametrize("T,K,E", [(9, 1, 5), (700, 5, 33), (4097, 1, 60), (8211, 3, 100),
+                                   (140001, 1, 256)])
+def test_permutation_of_slices(cuda_lib, T, K, E):
+    """A batch's ids from some token on, outputs at any word of a larger buffer."""
+    ids = ids_of(T + 3, K, E)
+    n = T * K
+    whole = ids.cuda()
+    for first in (1, 2, 3):
+        part = whole[first:first + T]
+        bufs = [torch.full((size + 8,), GUARD, dtype=torch.int32, device="cuda")
+                for size in (E + 1, n, n)]
+        off, idx, tok = (b[first:first + size] for b, size in zip(bufs, (E + 1, n, n)))
+        mf.moe_expert_permutation(part, E, expert_offsets=off, expanded_idx=idx.view(T, K),
+                                  row_tokens=tok)
+        want = permutation_ref(ids[first:first + T], E)
+        for b, out, ref in zip(bufs, (off, idx, tok), want):
+            assert torch.equal(out.cpu(), ref.flatten())
+            assert (b[:first] == GUARD).all() and (b[first + out.numel():] == GUARD).all()

@@ -30,3 +30,8 @@ def test_permutation_refuses_buffers_that_overlap(lib):
     for name, at in (("ids", IDS), ("idx", IDX), ("tok", TOK)):
         for shift in (0, size - 4, -4 * 16):
             assert permutation(lib, off=at + shift) == ALIGN, (name, shift)
+
+
+def test_permutation_refuses_what_is_no_word(lib):
+    for name, at in (("ids", IDS), ("idx", IDX), ("tok", TOK), ("off", OFF)):
+        assert permutation(lib, **{name: at + 2}) == ALIGN, name
