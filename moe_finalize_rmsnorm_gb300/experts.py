@@ -65,6 +65,13 @@ def _same_device(dev: torch.device, *tensors) -> None:
     raise ValueError("all tensors must be on the same CUDA device")
 
 
+def _int32(sizes: int) -> None:
+    """Sizes (or-ed together) that the C interface takes as 32-bit integers: a larger one
+    would lose its upper bits on the way."""
+    if sizes >> 31 not in (0, -1):
+        raise ValueError("a size does not fit into 32 bits")
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -90,6 +97,7 @@ def moe_expert_permutation(expert_ids: torch.Tensor, num_experts: int, *, packed
     dev = expert_ids.device
     T, K = expert_ids.shape
     num_experts = int(num_experts)
+    _int32(K | num_experts)
     _same_device(dev, expert_offsets, expanded_idx, row_tokens)
     if expert_offsets is not None:
         _index(expert_offsets, "expert_offsets", (num_experts + 1,))
@@ -126,6 +134,7 @@ def moe_permuted_row_sum(permuted: torch.Tensor, expanded_idx: torch.Tensor, out
         raise ValueError("expanded_idx must be 2-D")
     T, hidden = output.shape
     K = expanded_idx.shape[1]
+    _int32(hidden | K)
     _index(expanded_idx, "expanded_idx", (T, K))
     rows, width = permuted.shape
     if width < hidden:
@@ -146,6 +155,7 @@ def _weight(weight: torch.Tensor, offsets: torch.Tensor) -> tuple[int, int, int,
          (weight.stride(2) == 1 or weight.shape[2] <= 1),
          "weight must be a 3-D BF16 tensor with unit last-dim stride")
     E, n, k = weight.shape
+    _int32(E | n | k)
     _index(offsets, "expert_offsets", (E + 1,))
     row = weight.stride(1) if n > 1 else k
     return E, n, k, row, weight.stride(0) if E > 1 else n * row
@@ -221,6 +231,7 @@ def moe_grouped_gemm_wgrad(grad_output: torch.Tensor, x: torch.Tensor,
     _req(grad_weight.dim() == 3 and grad_weight.dtype in _VALUE_DTYPES and
          grad_weight.is_contiguous(), "grad_weight must be a contiguous 3-D BF16 or FP32 tensor")
     E, n, k = grad_weight.shape
+    _int32(E | n | k)
     _index(expert_offsets, "expert_offsets", (E + 1,))
     dy_ld = _rows(grad_output, "grad_output")
     x_ld = _rows(x, "x")
@@ -255,6 +266,7 @@ def moe_grouped_gemv_int4(x: torch.Tensor, weight: torch.Tensor, scales: torch.T
     _req(weight.dim() == 3 and weight.dtype == torch.uint8 and weight.is_contiguous(),
          "weight must be a contiguous 3-D uint8 tensor")
     E, n, k = weight.shape[0], weight.shape[1], 2 * weight.shape[2]
+    _int32(E | n | k)
     _req(scales.dim() == 3 and scales.dtype in _VALUE_DTYPES and scales.is_contiguous() and
          scales.shape[:2] == (E, n), "scales must be contiguous BF16 or FP32 [experts, n, groups]")
     groups = scales.shape[2]
