@@ -26,9 +26,6 @@ constexpr int kRowsPass = 16;  // rows of one pass over the weights
 constexpr int kSpan = 64;      // summed values of a stage
 constexpr int kStages = 4;
 constexpr int kStageBytes = kCols * kSpan * 2;
-// The tensor cores truncate their partial sums: every so many stages (640 summed
-// values) they are added up in FP32 and begin again, as in the tensor-core kernel.
-constexpr int kSegment = 10;
 
 struct RowsControl {
     float sums[kWarps][kRowsPass * kCols];
@@ -123,8 +120,10 @@ struct Rows {
         };
         load_x(0, now.stage);
         load_x(1, now.stage);
-        float acc[2][NT][4] = {}, sum[2][NT][4] = {};
-        int segment = 0;
+        // The tensor cores truncate their partial sums, so every stage's sum is begun anew
+        // and added up in FP32 (of 4096 values 1.2e-7 of the result; 5.9e-7 where ten
+        // stages made one sum, in the same time).
+        float acc[2][NT][4] = {};
         while (now.item == d.item) {
             const uint32_t slot = it % kStages;
             if (limit == 0 ||
@@ -136,6 +135,7 @@ struct Rows {
             const uint32_t w = ring + slot * kStageBytes + g * 128;
             advance(now);
             const int next = now.item == d.item ? now.stage : spans;  // behind the last: zeros
+            float sum[2][NT][4];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 // eight summed values of columns g + 8 i (the copy's swizzle keeps the
@@ -152,7 +152,10 @@ struct Rows {
                     const uint4 v = xv[b][i];
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        mma_16816(sum[m][i], a0[m], v.x, v.y);
+                        if (b == 0)
+                            mma_16816_first(sum[m][i], a0[m], v.x, v.y);
+                        else
+                            mma_16816(sum[m][i], a0[m], v.x, v.y);
                         mma_16816(sum[m][i], a1[m], v.z, v.w);
                     }
                 }
@@ -160,18 +163,12 @@ struct Rows {
             }
             __syncwarp();
             ++it;
-            if (++segment == kSegment || now.item != d.item) {
-                segment = 0;
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
+                for (int i = 0; i < NT; ++i)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            acc[m][i][j] += sum[m][i][j];
-                            sum[m][i][j] = 0.f;
-                        }
-            }
+                    for (int j = 0; j < 4; ++j) acc[m][i][j] += sum[m][i][j];
         }
         // acc[m][i][j]: n = 16 m + g + 8 (j / 2), row = 8 i + 2 t + j % 2
         float *mine = c.sums[warp];

@@ -88,3 +88,22 @@ def test_bf16_weight_gradients_of_long_sums(cuda_lib, many, gather):
         within(exact[e], ref[e], ref[e], moved_sums(m), FP32)
     if many > 32768:
         assert torch.equal(written[2], exact[2].to(BF16))
+
+
+@pytest.mark.parametrize("rows,experts,n,k", [(1, 1, 264, 7168), (8, 8, 512, 4096),
+                                              (64, 3, 136, 4104), (200, 100, 64, 1000),
+                                              (33, 2, 40, 40)])
+def test_few_rows_are_summed_in_short_pieces(cuda_lib, rows, experts, n, k):
+    """64 values at a time (four products of 16), each stage's sum and the up to twelve
+    warps' shares added in FP32."""
+    sizes = [rows // experts + (e < rows % experts) for e in range(experts)]
+    off = offsets_of(sizes)
+    x, w = positive((rows, k), 1), positive((experts, n, k), 2)
+    out = torch.empty((rows, n), dtype=FP32, device="cuda")
+    mf.moe_grouped_gemm(x, w, off, out)
+    ref = torch.cat([r @ m.t() for r, m in zip(x.double().split(sizes), w.double())])
+    stages = -(-k // 64)
+    within(out, ref, ref, 2 * 4 + (stages + 12) / 2, FP32)
+    # the truncation of a piece is at most 4 * 2^-22, on average half; what the sums of the
+    # stages round off cancels
+    assert (out.double() - ref).norm() < 5e-7 * ref.norm()
