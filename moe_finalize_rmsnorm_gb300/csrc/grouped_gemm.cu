@@ -10,8 +10,8 @@
 //
 // so the ragged dimension of the first two, an expert's rows, is the one whose
 // tile may be any multiple of 32 up to 256 (16 for a single CTA): an expert of 40
-// rows costs 64, not 128 or 256.  An expert's rows are split evenly over its tiles.
-// In wgrad the
+// rows costs 64, not 128 or 256.  An expert's rows are split into tiles of one such
+// multiple, the last with what is left (528 rows: 192, 192 and 144).  In wgrad the
 // ragged dimension is the summed one; the step that holds an expert's last rows
 // reads them by number, and the rows behind them as zeros, so that a row of
 // another expert (or one that was never written) enters nothing.
@@ -23,12 +23,16 @@
 // eight warps that move the other accumulator out, and six or twelve for rows that
 // are gathered.
 //
-// What bounds it (4096 x 4096, 16384 rows, GB300): up to some 200 rows an expert
-// the weights' bytes (64 experts: 330-354 us, 317 at the copy bandwidth), at 512
-// and more the tensor cores (1.8-1.87 PFLOP/s, as a plain library product).  In
-// between, 1.26-1.6 PFLOP/s at 288-384 rows, a tile of N rows brings (16 KB + 64 N)
-// into an SM for 2 N cycles of products: at N = 144 more than the 64 bytes a cycle
-// that it takes in.  Tiles of two blocks that share an operand needed fewer and
+// What bounds it (4096 x 4096, up to 16384 rows, GB300, short runs): up to some 200
+// rows an expert the weights' bytes (64 experts: 330-354 us, 317 at the copy
+// bandwidth).  Beyond, a step of a tile of N rows brings (16 KB + 64 N) into an SM, which
+// takes in 64 bytes a cycle, for 2 N cycles of products: the two are equal at N = 256
+// and the copies take longer below.  So 512 and 1024 rows (tiles of 256) run at 1.7-1.87
+// PFLOP/s, as a plain library product, 288 (160 and 128) at 1.25 and 528 (192, 192 and
+// 144) at 1.45-1.53, where the bytes allow 1.35 and 1.52.  The weights' gradient has
+// tiles of 256 always and is bound by its results' way out where few rows are summed:
+// 128 rows 0.47, 288 0.9, 512 1.24, 528 1.1-1.17, 1024 1.7-1.78 PFLOP/s.
+// Tiles of two blocks that share an operand needed fewer and
 // longer stages and both accumulators: 6 % faster at 288 rows, 4-30 % slower from
 // 512 rows on and for the weights' gradient; not kept.
 #include "experts.cuh"
@@ -50,8 +54,9 @@ constexpr int kScanThreads = 256;           // threads that scan the experts
 // tensor cores truncate each partial sum, an error that grows with the products added to
 // one accumulator: every 16 summed values lose up to 9e-8 of it, towards zero (values of
 // one sign: 4096 of them 1.1e-5 of the sum, 32768 1.6e-4, 2^20 6.1e-3; of either sign the
-// losses cancel for the most part).  640 summed values keep it near 1e-6, the plain
-// additions' own error.  FP32 results are made so.
+// losses cancel for the most part).  640 summed values keep it near 1e-6 for values of
+// one sign; of either sign FP32 results are off by 5.8e-7 of the result (320 values
+// 2.9e-7, as FP32 multiply-adds, in 1-3 % more time, the weights' gradient 5-8 %).
 constexpr int kSegment = 10;
 // BF16 results of more than this many summed values are, too.  Up to it one accumulator
 // takes the whole sum: 1.6e-4 beside the rounding's 2^-8.

@@ -13,8 +13,12 @@
 // Measured (GB300, device time): one token through eight 4096 x 4096 matrices, groups of
 // 128, 18.3 us (69 MB; 10.2 at the copy bandwidth, some 4 of start); eight tokens through
 // 41 of them 75 us (4.9 TB/s); 512 rows through 64 matrices of 4096 x 2048, groups of 32
-// with zeros, 99 us (3.2 TB/s).  What bounds it is the issue of instructions: 85 to 106 for
-// 1024 weights, of which 36 convert them.
+// with zeros, 100 us (3.2 TB/s).  What bounds it is the issue of instructions: 71 to 106 for
+// 1024 weights, of which 36 convert them.  Summed values that are no whole stages (k not a
+// multiple of 256) take the forms without WHOLE, which load scales word by word and, with
+// passes of 16 and 32 rows, keep up to 488 bytes a thread in local memory: k = 2880 152 us
+// where 2816 takes 109 (512 rows, 64 experts, groups of 32), 24 and 17 (64 rows, 8
+// experts), 15.7 and 14.0 (8 rows).
 #include "experts.h"
 #include "few_rows.cuh"
 #include "tensor_map.h"
@@ -540,8 +544,8 @@ cudaError_t launch(const GemvArgs &a, cudaStream_t s) {
 
 template <int GROUP>
 cudaError_t launch_group(const GemvArgs &a, cudaStream_t s) {
-    // Rows of a pass by the average of an expert: 16 from five rows on (8 rows 100 against
-    // 122 us for 32 a pass), 32 from 24 on (one matrix: 24 rows 52 us in passes of 16, 62 in
+    // Rows of a pass by the average of an expert: 16 above five rows (8 rows 100 against
+    // 122 us for 32 a pass), 32 above 24 (one matrix: 24 rows 52 us in passes of 16, 62 in
     // one of 32; 32 rows 80 against 62).
     const bool whole = a.k % kSpan == 0 && reinterpret_cast<uintptr_t>(a.scales) % 16 == 0 &&
                        reinterpret_cast<uintptr_t>(a.zeros) % 8 == 0;
