@@ -178,3 +178,35 @@ def test_4_bit_products(cuda_lib, rows, n, k, group):
         out = torch.empty((sum(sizes), n), dtype=dtype, device="cuda")
         mf.moe_grouped_gemv_int4(x, q, s, offsets_of(sizes), out, zeros=z)
         check(out, *split_product(x.double(), w.transpose(1, 2), sizes), int4(k, group), dtype)
+
+
+@pytest.mark.parametrize("programmatic", [True, False])
+def test_long_weight_gradients_in_a_graph(cuda_lib, programmatic):
+    """The two launches of a call with a long sum, captured behind the product that makes
+    their operand, added to and replayed: the bits of the eager calls."""
+    sizes, n, k = [33000, 0, 500], 136, 264
+    rows, off = sum(sizes), offsets_of(sizes)
+    w, x, dy = weights(3, n, k, 1), padded(rows, k, 2, 0), padded(rows, n, 3, 0)
+    start = randn((3, n, k), 4)
+
+    def step(grad, made):
+        mf.moe_grouped_gemm(x, w, off, made)
+        mf.moe_grouped_gemm_wgrad(made, x, off, grad, accumulate=True)
+        mf.moe_grouped_gemm_wgrad(dy, x, off, grad, accumulate=True)
+
+    mf.set_programmatic_launch(programmatic)
+    try:
+        want, made = start.clone(), torch.empty((rows, n), dtype=BF16, device="cuda")
+        step(want, made)
+        step(want, made)
+        got, made = start.clone(), torch.empty((rows, n), dtype=BF16, device="cuda")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(got, made)
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    finally:
+        mf.set_programmatic_launch(True)
