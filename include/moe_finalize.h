@@ -24,6 +24,8 @@
  *
  *   moe_expert_permutation -- the index map from routed expert ids, and
  *     moe_permuted_row_sum, the gradient of the gather that it defines.
+ *   moe_dispatch, moe_combine, moe_combine_backward -- the tokens' rows into
+ *     expert order and back, with the routing weights, and the gradients.
  *   moe_grouped_gemm, moe_grouped_gemm_dgrad, moe_grouped_gemm_wgrad -- matrix
  *     products over each expert's rows: forward and both gradients.
  *   moe_grouped_gemv_int4 -- the product with 4-bit weights, for few rows per
@@ -308,6 +310,96 @@ mf_status moe_permuted_row_sum(const void *permuted, mf_dtype permuted_dtype, in
                                int64_t row_stride, const int32_t *expanded_idx_to_permuted_idx,
                                void *output, mf_dtype output_dtype, int64_t num_tokens,
                                int32_t hidden, int32_t top_k, mf_stream_t stream);
+
+/*
+ * moe_dispatch -- the tokens' rows into expert order, weighted if weights are
+ * given:
+ *
+ *   output[i(t, j), :] = w(t, j) x[t, :]      i = expanded_idx_to_permuted_idx
+ *
+ * the product in FP32, rounded once.  A slot whose index is negative or not below
+ * `rows` moves nothing (its weight has no effect); rows that no slot names are left
+ * as they were.  No two slots may name one row (a map made by
+ * moe_expert_permutation names each once): of such a row the values are those of
+ * either slot.  Its gradients are moe_combine (of x) and moe_combine_backward
+ * with grad_output = x, permuted = the gradient of `output` and no grad_permuted
+ * (of the weights).
+ *
+ *   x                device, BF16 or FP32 [num_tokens, x_stride], columns
+ *                    [0, hidden) used.
+ *   expert_weights   device, BF16, FP32 or packed int32 routing words
+ *                    [num_tokens, top_k] contiguous, aligned to its elements; NULL:
+ *                    no weights (the rows are copied).
+ *   expanded_idx_to_permuted_idx
+ *                    device, int32 [num_tokens, top_k] contiguous, 4-byte aligned.
+ *   output           device, BF16 or FP32 [rows, output_stride], columns
+ *                    [0, hidden) written.
+ *   hidden           a multiple of 8, 8 .. 2^20.   top_k  1 .. 32.
+ *   Row strides are multiples of 8 elements, at least hidden; x and output 16-byte
+ *   aligned.  The output may not overlap an input (MF_ERR_ALIGN).
+ *
+ * Errors: MF_ERR_UNSUPPORTED, MF_ERR_SHAPE, MF_ERR_DTYPE, MF_ERR_NULL,
+ * MF_ERR_ALIGN, MF_ERR_CUDA.  Zero tokens or rows: MF_OK, nothing launched.
+ */
+mf_status moe_dispatch(const void *x, mf_dtype x_dtype, int64_t x_stride,
+                       const void *expert_weights, mf_dtype weights_dtype,
+                       const int32_t *expanded_idx_to_permuted_idx, void *output,
+                       mf_dtype output_dtype, int64_t rows, int64_t output_stride,
+                       int64_t num_tokens, int32_t hidden, int32_t top_k, mf_stream_t stream);
+
+/*
+ * moe_combine -- the experts' rows back to the tokens, weighted, without a norm:
+ *
+ *   output[t, :] = sum over j of w(t, j) permuted[i(t, j), :]
+ *
+ * one FP32 multiply-add per slot in ascending j, rounded once.  A slot whose index
+ * is negative or not below `rows` contributes zero; its weight has no effect.
+ *
+ *   permuted         device, BF16 or FP32 [rows, row_stride].  May be NULL only
+ *                    when rows == 0.
+ *   expert_weights   as for moe_dispatch, required.
+ *   output           device, BF16 or FP32 [num_tokens, output_stride].
+ *   The rest, and the errors, as for moe_dispatch; a row may be named by several
+ *   slots.  Zero tokens: MF_OK, nothing launched.
+ */
+mf_status moe_combine(const void *permuted, mf_dtype permuted_dtype, int64_t rows,
+                      int64_t row_stride, const void *expert_weights, mf_dtype weights_dtype,
+                      const int32_t *expanded_idx_to_permuted_idx, void *output,
+                      mf_dtype output_dtype, int64_t output_stride, int64_t num_tokens,
+                      int32_t hidden, int32_t top_k, mf_stream_t stream);
+
+/*
+ * moe_combine_backward -- the gradients of moe_combine, in one pass over the rows:
+ *
+ *   grad_permuted[i(t, j), :] = w(t, j) grad_output[t, :]
+ *   grad_weights[t, j]        = sum over columns of permuted[i(t, j), :] grad_output[t, :]
+ *
+ * products and sums in FP32, each result rounded once; the sums' order is fixed by
+ * the sizes.  A slot without a row has grad_weights 0; rows that no slot names are
+ * left as they were, and no two slots may name one row when grad_permuted is wanted
+ * (as for moe_dispatch).
+ *
+ *   grad_output      device, BF16 or FP32 [num_tokens, grad_output_stride].
+ *   permuted         device, BF16 or FP32 [rows, row_stride]: the rows that were
+ *                    combined.  Not read (and may be NULL) without grad_weights.
+ *   expert_weights   as for moe_dispatch.  Not read (and may be NULL) without
+ *                    grad_permuted.
+ *   grad_permuted    device, permuted's dtype [rows, grad_permuted_stride], or NULL:
+ *                    not wanted.
+ *   grad_weights     device, BF16 or FP32 [num_tokens, top_k] contiguous, aligned to
+ *                    its elements, or NULL: not wanted.
+ *   The rest, and the errors, as for moe_dispatch, and MF_ERR_INVALID (neither
+ *   gradient wanted).  Outputs may not overlap inputs or each other
+ *   (MF_ERR_ALIGN).  Zero tokens: MF_OK, nothing launched.
+ */
+mf_status moe_combine_backward(const void *grad_output, mf_dtype grad_output_dtype,
+                               int64_t grad_output_stride, const void *permuted,
+                               mf_dtype permuted_dtype, int64_t rows, int64_t row_stride,
+                               const void *expert_weights, mf_dtype weights_dtype,
+                               const int32_t *expanded_idx_to_permuted_idx, void *grad_permuted,
+                               int64_t grad_permuted_stride, void *grad_weights,
+                               mf_dtype grad_weights_dtype, int64_t num_tokens, int32_t hidden,
+                               int32_t top_k, mf_stream_t stream);
 
 /*
  * moe_grouped_gemm -- for each expert e and each of its rows r

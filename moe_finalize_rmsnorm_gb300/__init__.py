@@ -15,6 +15,8 @@ streams.  There is no CPU fallback: without the built library the calls raise.
 * ``moe_expert_permutation``, ``moe_permuted_row_sum``, ``moe_grouped_gemm`` with
   its gradients and ``moe_grouped_gemv_int4`` (``experts.py``) are the steps of an
   expert layer before the finalize.
+* ``moe_dispatch``, ``moe_combine`` and ``moe_combine_backward`` (``combine.py``) take the
+  tokens' rows into expert order and back, with the routing weights and their gradients.
 """
 from __future__ import annotations
 
@@ -24,12 +26,14 @@ import torch
 from ._abi import (MF_DTYPE_BF16, MF_DTYPE_FP32, MF_DTYPE_PACKED_TOPK, VARIANT_NAMES, VARIANTS, MoeFinalizeError,
                    check, lib)
 from ._binding import _on_device, _req, _stream_ptr
+from .combine import moe_combine, moe_combine_backward, moe_dispatch
 from .experts import (moe_expert_permutation, moe_grouped_gemm, moe_grouped_gemm_dgrad,
                       moe_grouped_gemm_wgrad, moe_grouped_gemv_int4, moe_permuted_row_sum)
 
 __all__ = [
     "moe_finalize_rmsnorm", "tp_moe_finalize_rmsnorm", "beam_moe_finalize",
     "beam_moe_finalize_norm_residual_norm", "moe_expert_permutation", "moe_permuted_row_sum",
+    "moe_dispatch", "moe_combine", "moe_combine_backward",
     "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad",
     "moe_grouped_gemv_int4", "MoeFinalizeError",
     "device_status", "selftest_wait_timeout", "select_finalize_variant", "select_beam_variant",

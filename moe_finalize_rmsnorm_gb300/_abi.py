@@ -35,6 +35,13 @@ SIGNATURES = {
     "moe_expert_permutation": (_int, [_vp, _int, _i64, _i32, _i32, _vp, _vp, _vp, _vp]),
     "moe_permuted_row_sum": (
         _int, [_vp, _int, _i64, _i64, _vp, _vp, _int, _i64, _i32, _i32, _vp]),
+    "moe_dispatch": (
+        _int, [_vp, _int, _i64, _vp, _int, _vp, _vp, _int, _i64, _i64, _i64, _i32, _i32, _vp]),
+    "moe_combine": (
+        _int, [_vp, _int, _i64, _i64, _vp, _int, _vp, _vp, _int, _i64, _i64, _i32, _i32, _vp]),
+    "moe_combine_backward": (
+        _int, [_vp, _int, _i64, _vp, _int, _i64, _i64, _vp, _int, _vp, _vp, _i64, _vp, _int, _i64,
+               _i32, _i32, _vp]),
     "moe_grouped_gemm": (
         _int, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _int, _i64, _i64, _i32, _i32, _i32,
                _vp]),

@@ -36,6 +36,31 @@ struct RowSumArgs {
     bool programmatic;
 };
 
+// The way into expert order and back.  `token_rows` has a row for each token, `rows` and
+// `out_rows` (of dispatch and of the gradient) a row for each slot; combine's `out_rows`
+// are the tokens'.
+struct CombineArgs {
+    const void *token_rows;  // dispatch x, backward dy: [T, token_ld]
+    int64_t token_ld;
+    int token_fp32;          // type of the tokens' rows, in or out
+    const void *rows;        // combine, backward: [num_rows, ld]
+    int64_t ld;
+    int64_t num_rows;
+    int rows_fp32;           // type of the slots' rows, in or out
+    void *out_rows;          // nullptr: no gradient of the rows
+    int64_t out_ld;
+    const void *weights;     // [T, K], by `weight_kind` (rows.cuh)
+    int weight_kind;
+    const int32_t *idx;      // [T, K]
+    void *grad_weights;      // [T, K], or nullptr
+    int grad_weights_fp32;
+    int64_t num_tokens;
+    int hidden;
+    int top_k;
+    int num_sms;
+    bool programmatic;
+};
+
 // Whether a forward product takes the kernel for few rows: up to 64 rows, or two an
 // expert (the experts' own are known on the device only; 256 at most, for a router that
 // sends them all to one).  At 2048 x 4096, few-rows against tensor-core kernel: 2 rows
@@ -111,6 +136,9 @@ cudaError_t prepare_grouped_gemv();
 
 cudaError_t launch_expert_permutation(const PermuteArgs &a, cudaStream_t s);
 cudaError_t launch_permuted_row_sum(const RowSumArgs &a, cudaStream_t s);
+cudaError_t launch_dispatch(const CombineArgs &a, cudaStream_t s);
+cudaError_t launch_combine(const CombineArgs &a, cudaStream_t s);
+cudaError_t launch_combine_backward(const CombineArgs &a, cudaStream_t s);
 cudaError_t launch_grouped_gemm(const GroupedArgs &a, cudaStream_t s);
 // The same for few rows (forward; launch_grouped_gemm chooses it).
 cudaError_t launch_grouped_rows(const GroupedArgs &a, cudaStream_t s);

@@ -4,6 +4,7 @@
 
 #include <mutex>
 
+#include "checks.h"
 #include "device_info.h"
 #include "experts.h"
 #include "moe_finalize.h"
@@ -11,18 +12,12 @@
 namespace {
 
 using mf::aligned;
-
-constexpr int64_t kMaxRows = 0x7fffffffLL - 1024;  // row numbers and tile ends stay in int32
-constexpr int32_t kMaxWidth = 1 << 20;             // columns of a matrix
-
-mf_status from_launch(cudaError_t e) { return e == cudaSuccess ? MF_OK : MF_ERR_CUDA; }
-
-bool value_dtype(mf_dtype d) { return d == MF_DTYPE_BF16 || d == MF_DTYPE_FP32; }
-
-// Row strides of the 16-byte kernels: at least the row, a multiple of 8 elements.
-bool row_stride_ok(int64_t stride, int64_t width) {
-    return stride >= width && stride % 8 == 0 && stride < (int64_t{1} << 36);
-}
+using mf::from_launch;
+using mf::kMaxRows;
+using mf::kMaxWidth;
+using mf::overlap;
+using mf::row_stride_ok;
+using mf::value_dtype;
 
 // Experts' matrices of rows * width elements: unit stride inside a row, no
 // expert inside another.
@@ -30,12 +25,6 @@ bool weight_strides_ok(int64_t row_stride, int64_t expert_stride, int32_t num_ex
                        int32_t k) {
     if (!row_stride_ok(row_stride, k) || !row_stride_ok(expert_stride, 0)) return false;
     return num_experts == 1 || expert_stride >= (n - 1) * row_stride + k;
-}
-
-// Whether two buffers share a byte.
-bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
-    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-    return p < q + static_cast<uintptr_t>(b_bytes) && q < p + static_cast<uintptr_t>(a_bytes);
 }
 
 mf_status check_experts(int32_t num_experts, int32_t n, int32_t k) {

@@ -1,6 +1,7 @@
 // Permutation by expert and the gradient of the gather it defines.
 #include "experts.cuh"
 #include "experts.h"
+#include "rows.cuh"
 
 namespace mf {
 namespace {
@@ -230,40 +231,6 @@ __global__ void __launch_bounds__(kPermuteThreads) permute_place_kernel(PermuteA
 constexpr int kRowsAhead = 4;
 constexpr int kSumThreads = 128;
 
-// The load of common.cuh's ld_nc_na_16, or zeros (p is not read): no branch between
-// the loads of several rows.
-__device__ __forceinline__ uint4 ld_nc_na_16_if(const void *p, bool read) {
-    uint4 r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-        : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
-        : "l"(p), "r"(uint32_t{read}));
-    return r;
-}
-
-template <bool FP32>
-struct Chunk8 {
-    uint4 v[FP32 ? 2 : 1];
-    __device__ void load(const void *rows, int64_t at, bool read) {
-        const uint8_t *p = static_cast<const uint8_t *>(rows) + at * (FP32 ? 4 : 2);
-        v[0] = ld_nc_na_16_if(p, read);
-        if (FP32) v[FP32 ? 1 : 0] = ld_nc_na_16_if(p + 16, read);
-    }
-    __device__ void get(float (&f)[8]) const {
-        if (FP32) {
-            const uint4 &a = v[0], &b = v[FP32 ? 1 : 0];
-            f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
-            f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
-            f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
-            f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
-        } else {
-            unpack8(v[0], f);
-        }
-    }
-};
-
 template <bool IN_FP32, bool OUT_FP32>
 __global__ void __launch_bounds__(kSumThreads) permuted_row_sum_kernel(RowSumArgs a) {
     pdl_wait();
@@ -289,16 +256,7 @@ __global__ void __launch_bounds__(kSumThreads) permuted_row_sum_kernel(RowSumArg
             for (int u = 0; u < 8; ++u) acc[u] += f[u];
         }
     }
-    const int64_t at = t * a.hidden + c;
-    if (OUT_FP32) {
-        float *o = static_cast<float *>(a.out) + at;
-        st_cs_16(o, make_uint4(__float_as_uint(acc[0]), __float_as_uint(acc[1]),
-                               __float_as_uint(acc[2]), __float_as_uint(acc[3])));
-        st_cs_16(o + 4, make_uint4(__float_as_uint(acc[4]), __float_as_uint(acc[5]),
-                                   __float_as_uint(acc[6]), __float_as_uint(acc[7])));
-    } else {
-        st_cs_16(static_cast<__nv_bfloat16 *>(a.out) + at, pack8_rn(acc));
-    }
+    store8<OUT_FP32>(a.out, t * a.hidden + c, acc);
 }
 
 }  // namespace
