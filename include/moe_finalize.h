@@ -30,6 +30,9 @@
  *     products over each expert's rows: forward and both gradients.
  *   moe_grouped_gemv_int4 -- the product with 4-bit weights, for few rows per
  *     expert.
+ *   moe_quantize_fp4, moe_dequantize_fp4, moe_grouped_gemm_fp4 -- rows to
+ *     microscaled 4-bit floating point and back, and the product of such rows
+ *     with such weights.
  *
  * Conventions for every entry point:
  *   - Pointers marked "device" are CUDA device (or managed) memory of the
@@ -54,7 +57,7 @@
  *     that wait gives up too, a bulk copy may still land in shared memory that
  *     another CTA then uses.  Discard the results and the CUDA context.
  *   - The first call on a device (of the permutation, of the grouped products
- *     and of the 4-bit product, each its first) sets kernel attributes; make it
+ *     and of either 4-bit product, each its first) sets kernel attributes; make it
  *     before any CUDA graph capture.  Captured calls replay with their arguments baked in.
  */
 #ifndef MOE_FINALIZE_H
@@ -93,6 +96,14 @@ typedef enum mf_dtype {
     MF_DTYPE_FP32 = 1,
     MF_DTYPE_PACKED_TOPK = 2
 } mf_dtype;
+
+/* Microscaled 4-bit floating point.  Values are E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and their negatives), column c in the low half of byte c / 2 for even c, in the
+ * high half for odd c; a block of columns shares a scale of one byte. */
+typedef enum mf_fp4_format {
+    MF_FP4_MX = 0,               /* blocks of 32, powers of two: E8M0, 2^(byte - 127), 255 NaN */
+    MF_FP4_NV = 1                /* blocks of 16, E4M3 (bit 7 is not used; 127 is NaN) */
+} mf_fp4_format;
 
 /* Kernel choice.  AUTO picks by size; the others force one kernel (for
  * validation and benchmarking, as the Beam wrappers' `strategy` argument
@@ -522,6 +533,89 @@ mf_status moe_grouped_gemv_int4(const void *x, int64_t x_rows, int64_t x_stride,
                                 int32_t group_size, const int32_t *expert_offsets, void *output,
                                 mf_dtype output_dtype, int64_t output_stride, int64_t rows,
                                 int32_t num_experts, int32_t n, int32_t k, mf_stream_t stream);
+
+/*
+ * moe_quantize_fp4 -- rows to 4-bit floating point.  For a block of v = factor * x
+ * (the product rounded to FP32; v = x without a factor) with largest magnitude m:
+ *
+ *   MX   s = 2^(floor(log2 m) - 2), at least 2^-127 (which zeros get, too)
+ *   NV   s = m / 6 rounded to E4M3, at most 448
+ *   q = the nearest E2M1 of v / s, ties to the even code, at most 6 in magnitude;
+ *       0 where s is 0
+ *
+ * decided as by the exact quotients.  A block in which some v is an infinity or a
+ * NaN gets a NaN as its scale and zeros as its values.
+ *
+ *   x                device, BF16 or FP32 [rows, x_stride], columns [0, k) used;
+ *                    x_stride a multiple of 8 elements.
+ *   factor           device, one FP32 value, or NULL.
+ *   quantized        device, [rows] rows of k / 2 bytes, quantized_stride apart.
+ *   scales           device, [rows] rows of k / 32 (MX) or k / 16 (NV) bytes,
+ *                    scales_stride apart.
+ *   k                a multiple of 32, 32 .. 2^20.
+ *   Byte strides are multiples of 16, at least the row's bytes; x, quantized and
+ *   scales 16-byte aligned.  Bytes behind a row's are neither read nor written.
+ *   Buffers may not overlap (MF_ERR_ALIGN).
+ *
+ * Errors: MF_ERR_INVALID (format), MF_ERR_UNSUPPORTED (k), MF_ERR_SHAPE,
+ * MF_ERR_DTYPE, MF_ERR_NULL, MF_ERR_ALIGN, MF_ERR_CUDA.  Zero rows: MF_OK.
+ */
+mf_status moe_quantize_fp4(const void *x, mf_dtype x_dtype, int64_t x_stride, const float *factor,
+                           uint8_t *quantized, int64_t quantized_stride, uint8_t *scales,
+                           int64_t scales_stride, mf_fp4_format format, int64_t rows, int32_t k,
+                           mf_stream_t stream);
+
+/*
+ * moe_dequantize_fp4 -- output[r, c] = value * scale in FP32 (exact within its
+ * range), rounded to BF16 where output is BF16 (exact within its range, too).
+ *
+ *   output           device, BF16 or FP32 [rows, output_stride], output_stride a
+ *                    multiple of 8 elements, 16-byte aligned.
+ *   The rest, and the errors, as for moe_quantize_fp4.
+ */
+mf_status moe_dequantize_fp4(const uint8_t *quantized, int64_t quantized_stride,
+                             const uint8_t *scales, int64_t scales_stride, mf_fp4_format format,
+                             void *output, mf_dtype output_dtype, int64_t output_stride,
+                             int64_t rows, int32_t k, mf_stream_t stream);
+
+/*
+ * moe_grouped_gemm_fp4 -- moe_grouped_gemm of 4-bit rows with 4-bit weights, both of
+ * one format: for each expert e and each of its rows r
+ *
+ *   output[r, :] = factor[e] * (weight[e] . x[i(r), :])     i(r) = row_index[r], or r
+ *
+ * accumulated in FP32, times the factor in FP32, rounded once.  Rows outside every
+ * expert are left as they were.
+ *
+ *   x, x_scales      device, x_rows rows of k / 2 bytes, and of k / 32 or k / 16
+ *                    scales.
+ *   row_index        as for moe_grouped_gemm (an entry outside [0, x_rows) selects
+ *                    a row of zeros).
+ *   weight, weight_scales
+ *                    device, num_experts matrices of n such rows; expert strides
+ *                    in bytes, an expert's matrix not overlapping the next.
+ *   factor           device, FP32 [num_experts], or NULL: 1.
+ *   expert_offsets   as for moe_grouped_gemm, or NULL when num_experts is 1:
+ *                    every row belongs to the one matrix.
+ *   output           device, BF16 or FP32 [rows, output_stride], output_stride a
+ *                    multiple of 8 elements, at least n.
+ *   n                a multiple of 8, 8 .. 2^20.   num_experts  1 .. 1024.
+ *   k                a multiple of 32, 32 .. 2^20.
+ *   Byte strides are multiples of 16, at least the row's bytes; x, weight, their
+ *   scales and output 16-byte aligned.  Bytes behind a row's are not read.
+ *
+ * Errors: those of moe_grouped_gemm, and MF_ERR_INVALID (format; no expert_offsets
+ * with more than one expert).  Zero rows: MF_OK, nothing launched.
+ */
+mf_status moe_grouped_gemm_fp4(const uint8_t *x, int64_t x_rows, int64_t x_stride,
+                               const uint8_t *x_scales, int64_t x_scales_stride,
+                               const int32_t *row_index, const uint8_t *weight,
+                               int64_t weight_row_stride, int64_t weight_expert_stride,
+                               const uint8_t *weight_scales, int64_t weight_scales_row_stride,
+                               int64_t weight_scales_expert_stride, mf_fp4_format format,
+                               const float *factor, const int32_t *expert_offsets, void *output,
+                               mf_dtype output_dtype, int64_t output_stride, int64_t rows,
+                               int32_t num_experts, int32_t n, int32_t k, mf_stream_t stream);
 
 /* The kernel AUTO would run for moe_finalize_rmsnorm with these sizes on the
  * calling thread's current device (MF_VARIANT_AUTO if none would run: no

@@ -17,6 +17,8 @@ streams.  There is no CPU fallback: without the built library the calls raise.
   expert layer before the finalize.
 * ``moe_dispatch``, ``moe_combine`` and ``moe_combine_backward`` (``combine.py``) take the
   tokens' rows into expert order and back, with the routing weights and their gradients.
+* ``moe_quantize_fp4``, ``moe_dequantize_fp4`` and ``moe_grouped_gemm_fp4`` (``fp4.py``) are
+  microscaled 4-bit floating point: rows to 4 bits and back, and the experts' product.
 """
 from __future__ import annotations
 
@@ -29,13 +31,15 @@ from ._binding import _on_device, _req, _stream_ptr
 from .combine import moe_combine, moe_combine_backward, moe_dispatch
 from .experts import (moe_expert_permutation, moe_grouped_gemm, moe_grouped_gemm_dgrad,
                       moe_grouped_gemm_wgrad, moe_grouped_gemv_int4, moe_permuted_row_sum)
+from .fp4 import moe_dequantize_fp4, moe_fp4_empty, moe_grouped_gemm_fp4, moe_quantize_fp4
 
 __all__ = [
     "moe_finalize_rmsnorm", "tp_moe_finalize_rmsnorm", "beam_moe_finalize",
     "beam_moe_finalize_norm_residual_norm", "moe_expert_permutation", "moe_permuted_row_sum",
     "moe_dispatch", "moe_combine", "moe_combine_backward",
     "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad",
-    "moe_grouped_gemv_int4", "MoeFinalizeError",
+    "moe_grouped_gemv_int4", "moe_fp4_empty", "moe_quantize_fp4", "moe_dequantize_fp4",
+    "moe_grouped_gemm_fp4", "MoeFinalizeError",
     "device_status", "selftest_wait_timeout", "select_finalize_variant", "select_beam_variant",
     "finalize_kernel_name", "beam_kernel_name", "finalize_data_movement",
     "version", "set_programmatic_launch", "programmatic_launch", "HIDDEN", "TOP_K",

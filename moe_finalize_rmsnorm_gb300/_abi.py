@@ -16,6 +16,7 @@ STATUS_NAMES = {
     5: "MF_ERR_UNSUPPORTED", 6: "MF_ERR_CUDA", 7: "MF_ERR_DEVICE_TIMEOUT", 8: "MF_ERR_INVALID",
 }
 MF_DTYPE_BF16, MF_DTYPE_FP32, MF_DTYPE_PACKED_TOPK = 0, 1, 2
+MF_FP4_MX, MF_FP4_NV = 0, 1
 VARIANTS = {"auto": 0, "token_cta": 1, "bulk": 2, "cluster": 3}
 VARIANT_NAMES = {v: k for k, v in VARIANTS.items()}
 
@@ -52,6 +53,13 @@ SIGNATURES = {
     "moe_grouped_gemv_int4": (
         _int, [_vp, _i64, _i64, _vp, _vp, _vp, _int, _vp, _i32, _vp, _vp, _int, _i64, _i64, _i32,
                _i32, _i32, _vp]),
+    "moe_quantize_fp4": (
+        _int, [_vp, _int, _i64, _vp, _vp, _i64, _vp, _i64, _int, _i64, _i32, _vp]),
+    "moe_dequantize_fp4": (
+        _int, [_vp, _i64, _vp, _i64, _int, _vp, _int, _i64, _i64, _i32, _vp]),
+    "moe_grouped_gemm_fp4": (
+        _int, [_vp, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _int, _vp, _vp,
+               _vp, _int, _i64, _i64, _i32, _i32, _i32, _vp]),
     "mf_finalize_data_movement": (_int, [_vp, _i64, _i64, _vp, _int, _vp, _vp, _i64, _vp]),
     "mf_select_finalize_variant": (_int, [_i64, _i32, _i32]),
     "mf_select_beam_variant": (_int, [_i64, _i32, _i32]),
