@@ -1,0 +1,720 @@
+// The 4-bit floating point product grouped by expert on the tensor cores
+// (tcgen05, block-scaled):
+//
+//   D[n, r] = sum over blocks b of sw[n, b] sx[r, b] sum_(k in b) qw[n, k] qx[i(r), k]
+//
+// computed transposed, as the BF16 products are: a tile's M is 256 output columns over a
+// pair of SMs, each holding half of either operand, and its N an expert's rows, any
+// multiple of 32 up to 192.  A persistent pair per two SMs walks the tiles: a warp
+// copies blocks (TMA, 128-byte swizzle, 256 summed values a step), a warp issues the
+// products into one of two accumulators in TMEM, four or eight warps move the other
+// accumulator out, and where rows are gathered, further warps copy them by number.
+//
+// The scales lie in rows beside the values' rows, and the products read them from TMEM:
+// lane l, column c the four bytes of row 32 c + l, the same in each quarter of the lanes.
+// Four warps, one to a quarter, bring 64 bytes a row into shared memory (cp.async, one
+// such group ahead), and write a step's scales into TMEM, two or three steps ahead of the
+// products.  The 128 columns behind the accumulators hold them: that is why a tile ends
+// at 192 rows.
+#include "experts.cuh"
+#include "experts.h"
+#include "fp4.cuh"
+#include "tensor_map.h"
+
+namespace mf {
+namespace {
+
+constexpr int kRowsMax = 192;             // N of a tile
+constexpr int kStep = 256;                // summed values per stage: 128 bytes
+constexpr int kStepBytes = kStep / 2;
+constexpr int kABytes = 128 * kStepBytes;  // A of one CTA and stage
+constexpr int kStageBytes = kABytes + kRowsMax / 2 * kStepBytes;
+constexpr int kStages = 5;
+constexpr int kTmemColumns = 512;         // two accumulators of 192, and the scales
+constexpr int kScaleColumn = 2 * kRowsMax;
+constexpr int kTurnBytes = 2048;          // an epilogue warp's block to turn results in
+constexpr int kScanThreads = 256;         // threads that scan the experts
+constexpr int kScaleRows = 128 + kRowsMax;      // rows whose scales a CTA holds
+constexpr int kGroupBytes = kScaleRows * 64;    // 64 bytes of scales a row
+constexpr int kScaleThreads = 128;
+
+// FP32 results, and BF16 results of more than kLongSum summed values: the sums leave the
+// tensor cores every this many steps and are added up in registers, as the tensor cores
+// truncate each partial sum.
+constexpr int kSegment = 10;
+constexpr int kLongSum = 131072;
+
+template <int FORMAT>
+struct Scales {
+    static constexpr int kBytes = FORMAT == kMx ? 8 : 16;     // of a row and step
+    static constexpr int kSteps = 64 / kBytes;                // steps of a group
+    static constexpr int kWords = kBytes / 4;
+    static constexpr int kColumns = 12 * kWords;              // of TMEM, of a step
+    static constexpr int kBuffers = FORMAT == kMx ? 4 : 2;    // steps held in TMEM
+    static_assert(kScaleColumn + kBuffers * kColumns <= kTmemColumns, "TMEM");
+    static_assert(kBuffers < kStages, "a stage's barrier tells when its scales may go");
+};
+
+// Warps: 0 block copies, 1 products, from 4 on the epilogue, then four for the scales,
+// then those that gather (with 2 and 3).
+template <bool SUMS, bool GATHER>
+struct Warps {
+    static constexpr int kEpilogue = SUMS ? 8 : 4;
+    static constexpr int kScale = 4 + kEpilogue;
+    static constexpr int kFirstGather = kScale + 4;
+    static constexpr int kShare = SUMS ? 1 : 2;  // gathering warps of a stage
+    static constexpr int kAll =
+        GATHER ? (SUMS ? 20 : kFirstGather + kShare * kStages - 2) : kFirstGather;
+    static constexpr int kThreads = 32 * kAll;
+};
+
+struct Control {
+    int4 list[kStages * 2][24];  // rows by number, four a copy; a part for each gathering warp
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], scale_full[4];
+    uint32_t tmem;
+    int scan[kScanThreads / 32];
+    int tiles[kMaxExperts + 1];  // row tiles of the experts before this one
+    int lo[kMaxExperts + 1];     // first row; the next expert's is the end
+};
+
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 2 * kGroupBytes + 8 * kTurnBytes +
+                           static_cast<int>(sizeof(Control));
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+
+struct Maps {
+    CUtensorMap a, b;  // whole blocks
+    CUtensorMap b4;    // rows by number
+};
+
+struct Tile {
+    int expert;
+    int m0;     // first output column
+    int row0;   // first output row
+    int nrows;  // output rows
+    int n;      // nrows rounded up to what the instruction takes
+};
+
+__device__ __forceinline__ int round_up(int v, int to) { return (v + to - 1) / to * to; }
+__device__ __forceinline__ int divide_up(int v, int by) { return (v + by - 1) / by; }
+
+__device__ __forceinline__ Tile tile_of(const Fp4GemmArgs &a, const Control &c, int t) {
+    const int mt = divide_up(a.n, 256);
+    const int e = expert_of_pass(c.tiles, a.num_experts, kMaxExperts / 2, t / mt);
+    const int rows = c.lo[e + 1] - c.lo[e], rt = c.tiles[e + 1] - c.tiles[e];
+    const int local = t - c.tiles[e] * mt;
+    const int each = round_up(divide_up(rows, rt), 32);  // only the last tile is padded
+    const int first = local % rt * each;
+    Tile r;
+    r.expert = e;
+    r.m0 = local / rt * 256;
+    r.row0 = c.lo[e] + first;
+    r.nrows = min(each, rows - first);
+    r.n = round_up(r.nrows, 32);
+    return r;
+}
+
+// Instruction descriptor: E2M1 operands along K, FP32 accumulators, M 256; `id`: the first
+// byte of a scale's word.
+template <int FORMAT>
+__device__ __forceinline__ uint32_t fp4_desc(int n, uint32_t id) {
+    return (id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (uint32_t{FORMAT == kMx} << 23) | (16u << 24) | (id << 29);
+}
+
+template <int FORMAT>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t scale_a, uint32_t scale_b, bool accumulate) {
+    if constexpr (FORMAT == kMx)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+            "[%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"(uint32_t{accumulate})
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+            "[%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"(uint32_t{accumulate})
+            : "memory");
+}
+
+// 8 or 16 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::
+                     "r"(addr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+                 "r"(v[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15])
+        : "memory");
+}
+
+// This CTA's scales are written: an arrival on the first CTA's barrier.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t remote_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
+                 : "memory");
+}
+
+// 32 output columns (one per lane) by 16 output rows to rows of `out`, turned in the
+// warp's block of shared memory; `cols` and `rows` what exists of the block.
+template <typename V>
+__device__ __forceinline__ void store16(const Fp4GemmArgs &a, uint8_t *block, int64_t out, int cols,
+                                        int rows, const V &value) {
+    const int lane = threadIdx.x % 32;
+    float *f = reinterpret_cast<float *>(block);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) f[j * 32 + lane] = value(j);
+    __syncwarp();
+    if (a.out_fp32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 4 + lane / 8, col = lane % 8 * 4;
+            if (r < rows && col < cols)
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + out + r * a.out_ld + col) =
+                    *reinterpret_cast<float4 *>(f + r * 32 + col);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = i * 8 + lane / 4, col = lane % 4 * 8;
+            if (r >= rows || col >= cols) continue;
+            float y[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) y[u] = f[r * 32 + col + u];
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + out + r * a.out_ld +
+                                       col) = pack8_rn(y);
+        }
+    }
+}
+
+// The same of 32 rows in BF16.
+__device__ __forceinline__ void store32_bf16(const Fp4GemmArgs &a, uint8_t *block, int64_t out,
+                                             int cols, int rows, float factor,
+                                             const uint32_t (&v)[32]) {
+    const int lane = threadIdx.x % 32;
+    __nv_bfloat16 *h = reinterpret_cast<__nv_bfloat16 *>(block);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        h[j * 32 + lane] = __float2bfloat16_rn(__uint_as_float(v[j]) * factor);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + lane / 4, col = lane % 4 * 8;
+        if (r < rows && col < cols)
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + out + r * a.out_ld +
+                                       col) = *reinterpret_cast<uint4 *>(h + r * 32 + col);
+    }
+}
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *p, int valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(valid)
+                 : "memory");
+}
+
+__device__ __forceinline__ void scale_warps_meet() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kScaleThreads) : "memory");
+}
+
+template <int FORMAT, bool GATHER, bool SUMS>
+__global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
+    fp4_gemm_kernel(const __grid_constant__ Maps maps, const Fp4GemmArgs a) {
+    using W = Warps<SUMS, GATHER>;
+    using Sc = Scales<FORMAT>;
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t groups = base + kStages * kStageBytes;
+    uint8_t *blocks = raw + (base - smem_u32(raw)) + kStages * kStageBytes + 2 * kGroupBytes;
+    Control &c = *reinterpret_cast<Control *>(blocks + 8 * kTurnBytes);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    const uint32_t full = smem_u32(c.full), empty = smem_u32(c.empty);
+    const uint32_t acc_full = smem_u32(c.acc_full), acc_empty = smem_u32(c.acc_empty);
+    const uint32_t scale_full = smem_u32(c.scale_full);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_empty + 8 * i, W::kEpilogue * 2);
+        }
+        for (int i = 0; i < Sc::kBuffers; ++i) mbar_init(scale_full + 8 * i, 4 * 2);
+        fence_mbar_init();
+    }
+    // After the wait, not before: a kernel that this one waits for may want TMEM.
+    pdl_wait();
+    if (warp == 2) tmem_alloc<2>(smem_u32(&c.tmem), kTmemColumns);
+    const int total = scan_experts<kScanThreads>(a.offsets, a.num_experts, static_cast<int>(a.rows),
+                                                 kRowsMax, c.lo, c.tiles, c.scan);
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_barrier();
+    tcgen05_fence_after();
+    const uint32_t tmem = c.tmem;
+
+    const int steps = divide_up(a.k, kStep);
+    const int tiles = divide_up(a.n, 256) * total;
+    const int first_tile = blockIdx.x / 2, tile_step = gridDim.x / 2;
+
+    // Registers: the warps that hold the moved sums take some of the others'
+    // (8 * 32 * 144 + 12 * 32 * 64 = the launch's 640 * 96).
+    constexpr bool kMoveRegisters = SUMS && GATHER;
+    static_assert(!kMoveRegisters || W::kThreads == 640, "register split");
+
+    bool ok = true;
+    if (warp >= 4 && warp < W::kScale) {
+        if constexpr (kMoveRegisters) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+        // Results: lane = output column, TMEM column = output row; four warps (one
+        // per 32 lanes) to all TMEM columns, or eight to every other 32.
+        const int w = warp % 4, group = (warp - 4) / 4;
+        constexpr int kGroups = W::kEpilogue / 4;
+        uint8_t *block = blocks + (warp - 4) * kTurnBytes;
+        const uint32_t done_at = map_to_cta(acc_empty, 0);
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
+        uint32_t acc_n = 0;  // accumulators taken so far
+        for (int t = first_tile; t < tiles && ok; t += tile_step) {
+            const Tile d = tile_of(a, c, t);
+            const int col0 = d.m0 + rank * 128 + w * 32;
+            const int cols = a.n - col0;  // what exists of the warp's 32
+            const float factor = a.factor ? __ldg(a.factor + d.expert) : 1.f;
+            auto take = [&]() {  // wait for the next accumulator
+                ok = __all_sync(0xffffffffu, mbar_wait_long<true>(acc_full + 8 * (acc_n & 1),
+                                                            acc_n >> 1 & 1, a.timeout_ns));
+                tcgen05_fence_after();
+                return lanes + (acc_n & 1) * kRowsMax;
+            };
+            auto give_back = [&]() {
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(done_at + 8 * (acc_n & 1));
+                ++acc_n;
+            };
+            if constexpr (SUMS) {
+                constexpr int kChunks = kRowsMax / 32 / kGroups;
+                float sums[kChunks][32];
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sums[i][j] = 0.f;
+                for (int s = 0; s < steps; s += kSegment) {
+                    const uint32_t from = take();
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        const int r = (kGroups * i + group) * 32;
+                        if (r < d.nrows) {
+#pragma unroll
+                            for (int part = 0; part < 2; ++part) {
+                                uint32_t v[16];
+                                tmem_ld16(from + r + part * 16, v);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    sums[i][16 * part + j] += __uint_as_float(v[j]);
+                            }
+                        }
+                    }
+                    give_back();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    const int r = (kGroups * i + group) * 32;
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+                        if (r + 16 * part < d.nrows)
+                            store16(a, block, int64_t{d.row0 + r + 16 * part} * a.out_ld + col0, cols,
+                                    d.nrows - r - 16 * part,
+                                    [&](int j) { return sums[i][16 * part + j] * factor; });
+                }
+            } else {
+                const uint32_t from = take();
+                if (!ok) break;
+                for (int r = 0; r < d.nrows; r += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(from + r, v);
+                    store32_bf16(a, block, int64_t{d.row0 + r} * a.out_ld + col0, cols, d.nrows - r,
+                                 factor, v);
+                }
+                give_back();
+            }
+        }
+    } else {
+        if constexpr (kMoveRegisters) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        const uint32_t full_at = map_to_cta(full, 0);
+        if (warp == 0) {
+            // Copies of whole blocks, and each stage's byte count.
+            uint32_t it = 0;
+            for (int t = first_tile; t < tiles && ok; t += tile_step) {
+                const Tile d = tile_of(a, c, t);
+                const int half = d.n / 2;  // B rows of this CTA
+                const int b0 = d.row0 + rank * half, m0 = d.m0 + rank * 128;
+                const uint32_t bytes = kABytes + round_up(half, GATHER ? 4 : 32) * kStepBytes;
+                for (int s = 0; s < steps; ++s, ++it) {
+                    const uint32_t stage = it % kStages, phase = it / kStages & 1;
+                    // all lanes give up together: the warp meets again below
+                    ok = __all_sync(0xffffffffu, mbar_wait_long<true>(empty + 8 * stage, phase ^ 1,
+                                                                     a.timeout_ns));
+                    if (!ok) break;
+                    const uint32_t bar = full_at + 8 * stage;
+                    const uint32_t sa = base + stage * kStageBytes, sb = sa + kABytes;
+                    if (elect_one()) {
+                        if (rank == 0) mbar_arrive_expect_tx(full + 8 * stage, 2 * bytes);
+                        tma_3d<true>(sa, &maps.a, s * kStepBytes, m0, d.expert, bar);
+                        if (!GATHER)
+                            for (int i = 0; i < half; i += 32)
+                                tma_2d<true>(sb + i * kStepBytes, &maps.b, s * kStepBytes, b0 + i,
+                                             bar);
+                    }
+                    __syncwarp();
+                }
+            }
+            // The products have read every stage (and the other CTA's completions have
+            // arrived here) before this CTA may leave.
+            if (ok)
+                for (uint32_t i = 0; i < kStages && i < it; ++i) {
+                    const uint32_t p = it - 1 - i;
+                    ok = ok && mbar_wait_long<true>(empty + 8 * (p % kStages), p / kStages & 1,
+                                                    a.timeout_ns);
+                }
+            if (!ok && rank == 0)  // the copies in flight, before the memory is given back
+                for (uint32_t i = 0; i < kStages && i < it; ++i) {
+                    const uint32_t p = it - 1 - i;
+                    (void)mbar_wait_long<true>(full + 8 * (p % kStages), p / kStages & 1,
+                                               a.timeout_ns);
+                }
+        } else if (warp == 1 && rank == 0) {
+            // Products.
+            uint32_t it = 0, acc_n = 0;
+            for (int t = first_tile; t < tiles && ok; t += tile_step) {
+                const Tile d = tile_of(a, c, t);
+                const uint32_t idesc = fp4_desc<FORMAT>(d.n, 0);
+                const uint32_t second = fp4_desc<FORMAT>(d.n, 2);  // the word's other two scales
+                for (int s = 0; s < steps; ++s, ++it) {
+                    const int in_segment = SUMS ? s % kSegment : s;
+                    if (in_segment == 0) {
+                        ok = __all_sync(0xffffffffu,
+                                        mbar_wait_long<true>(acc_empty + 8 * (acc_n & 1),
+                                                             (acc_n >> 1 & 1) ^ 1, a.timeout_ns));
+                        if (!ok) break;
+                    }
+                    const uint32_t stage = it % kStages, buffer = it % Sc::kBuffers;
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait_long<true>(scale_full + 8 * buffer,
+                                                         it / Sc::kBuffers & 1, a.timeout_ns) &&
+                                        mbar_wait_long<true>(full + 8 * stage, it / kStages & 1,
+                                                             a.timeout_ns));
+                    if (!ok) break;
+                    tcgen05_fence_after();
+                    const uint32_t sa = base + stage * kStageBytes, sb = sa + kABytes;
+                    const uint32_t dst = tmem + (acc_n & 1) * kRowsMax;
+                    const uint32_t scales = tmem + kScaleColumn + buffer * Sc::kColumns;
+                    const uint64_t da = smem_desc(sa, 16, 1024), db = smem_desc(sb, 16, 1024);
+                    const int parts = (min(kStep, a.k - s * kStep) + 63) / 64;
+                    const bool end = s + 1 == steps || (SUMS && in_segment == kSegment - 1);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            // 64 summed values: 32 bytes of a row, a word of its scales or half
+                            const int word = FORMAT == kMx ? p / 2 : p;
+                            if (p < parts)
+                                mma_fp4<FORMAT>(dst, da + p * 2, db + p * 2,
+                                                FORMAT == kMx && p % 2 ? second : idesc,
+                                                scales + 4 * word,
+                                                scales + 4 * Sc::kWords + 8 * word,
+                                                in_segment + p > 0);
+                        }
+                        mma_commit<2>(empty + 8 * stage);
+                        if (end) mma_commit<2>(acc_full + 8 * (acc_n & 1));
+                    }
+                    __syncwarp();
+                    if (end) ++acc_n;
+                }
+            }
+        } else if (warp >= W::kScale && warp < W::kFirstGather) {
+            // Scales.  Thread i of 128 copies 16 bytes of every 32nd row, rows 0 .. 127 the
+            // columns', 128 .. 319 the tile's rows; a warp reads them all and writes its
+            // quarter of the lanes.  A warp that gave up goes on meeting the others.
+            const int member = threadIdx.x - 32 * W::kScale;
+            const int row_bytes = a.k / (FORMAT == kMx ? 32 : 16);
+            const uint32_t scale_full_at = map_to_cta(scale_full, 0);
+            const uint32_t lanes = tmem + kScaleColumn +
+                                   (static_cast<uint32_t>(warp % 4 * 32) << 16);
+            const int tile_groups = divide_up(steps, Sc::kSteps);
+            int next_t = first_tile, next_g = 0;  // the group to copy next
+            Tile next = {};
+            int x_rows[kRowsMax / 32];            // of this thread, -1: none (zeros)
+            auto copy_group = [&](uint32_t buffer) {
+                if (next_t < tiles) {
+                    if (next_g == 0) {
+                        next = tile_of(a, c, next_t);
+#pragma unroll
+                        for (int u = 0; u < kRowsMax / 32; ++u) {
+                            const int i = 32 * u + member / 4;
+                            int row = -1;
+                            if (i < next.nrows) {
+                                row = next.row0 + i;
+                                if (GATHER) row = __ldg(a.row_index + row);
+                                if (row >= a.x_rows) row = -1;
+                            }
+                            x_rows[u] = row;
+                        }
+                    }
+                    const int chunk = member % 4, from = next_g * 64 + chunk * 16;
+                    const int valid = min(max(row_bytes - from, 0), 16);
+                    const uint32_t to = groups + buffer * kGroupBytes + member / 4 * 64 +
+                                        ((chunk ^ (member / 8 % 4)) << 4);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int n = next.m0 + static_cast<int>(rank) * 128 + 32 * u + member / 4;
+                        const bool read = valid > 0 && n < a.n;
+                        cp_async_16(to + u * 32 * 64,
+                                    read ? a.w_scales + next.expert * a.ws_expert + n * a.ws_ld + from
+                                         : a.w_scales,
+                                    read ? valid : 0);
+                    }
+#pragma unroll
+                    for (int u = 0; u < kRowsMax / 32; ++u) {
+                        const bool read = valid > 0 && x_rows[u] >= 0;
+                        cp_async_16(to + (128 + u * 32) * 64,
+                                    read ? a.x_scales + x_rows[u] * a.xs_ld + from : a.x_scales,
+                                    read ? valid : 0);
+                    }
+                    if (++next_g == tile_groups) {
+                        next_g = 0;
+                        next_t += tile_step;
+                    }
+                }
+                cp_async_commit();
+            };
+            copy_group(0);
+            uint32_t it = 0, g_it = 0;
+            for (int t = first_tile; t < tiles; t += tile_step) {
+                for (int g = 0; g < tile_groups; ++g, ++g_it) {
+                    cp_async_wait<0>();
+                    scale_warps_meet();  // the group is there, and the one before is read
+                    copy_group((g_it + 1) & 1);
+                    const uint32_t from = groups + (g_it & 1) * kGroupBytes + lane * 64;
+                    const int end = min(Sc::kSteps, steps - g * Sc::kSteps);
+                    for (int s = 0; s < end; ++s, ++it) {
+                        if (!ok) continue;
+                        // row 32 i + lane, this step's bytes (rows two apart lie in other banks)
+                        uint32_t v[10][Sc::kWords];
+                        const int at = s * Sc::kBytes;
+                        const uint32_t p = from + (((at / 16) ^ (lane / 2 % 4)) << 4) + at % 16;
+#pragma unroll
+                        for (int i = 0; i < 10; ++i) {
+                            if constexpr (FORMAT == kMx) {
+                                const uint2 q = *reinterpret_cast<const uint2 *>(
+                                    __cvta_shared_to_generic(p + i * 2048));
+                                v[i][0] = q.x;
+                                v[i][1] = q.y;
+                            } else {
+                                const uint4 q = lds_16(p + i * 2048);
+                                v[i][0] = q.x;
+                                v[i][1] = q.y;
+                                v[i][Sc::kWords - 2] = q.z;
+                                v[i][Sc::kWords - 1] = q.w;
+                            }
+                        }
+                        // the products of the step that had the place before are done
+                        if (it >= Sc::kBuffers) {
+                            const uint32_t before = it - Sc::kBuffers;
+                            ok = __all_sync(0xffffffffu,
+                                            mbar_wait_long<true>(empty + 8 * (before % kStages),
+                                                                 before / kStages & 1,
+                                                                 a.timeout_ns));
+                            if (!ok) continue;
+                        }
+                        tcgen05_fence_after();
+                        const uint32_t to = lanes + it % Sc::kBuffers * Sc::kColumns;
+                        if constexpr (FORMAT == kMx) {
+                            const uint32_t wv[8] = {v[0][0], v[1][0], v[2][0], v[3][0],
+                                                    v[0][1], v[1][1], v[2][1], v[3][1]};
+                            tmem_st8(to, wv);
+                            const uint32_t xv[16] = {v[4][0], v[5][0], v[6][0], v[7][0],
+                                                     v[8][0], v[9][0], 0,       0,
+                                                     v[4][1], v[5][1], v[6][1], v[7][1],
+                                                     v[8][1], v[9][1], 0,       0};
+                            tmem_st16(to + 8, xv);
+                        } else {
+                            constexpr int kLast = Sc::kWords - 1;
+                            const uint32_t wv[16] = {
+                                v[0][0],         v[1][0],         v[2][0],         v[3][0],
+                                v[0][1],         v[1][1],         v[2][1],         v[3][1],
+                                v[0][kLast - 1], v[1][kLast - 1], v[2][kLast - 1], v[3][kLast - 1],
+                                v[0][kLast],     v[1][kLast],     v[2][kLast],     v[3][kLast]};
+                            tmem_st16(to, wv);
+                            const uint32_t x0[16] = {v[4][0], v[5][0], v[6][0], v[7][0],
+                                                     v[8][0], v[9][0], 0,       0,
+                                                     v[4][1], v[5][1], v[6][1], v[7][1],
+                                                     v[8][1], v[9][1], 0,       0};
+                            tmem_st16(to + 16, x0);
+                            const uint32_t x1[16] = {
+                                v[4][kLast - 1], v[5][kLast - 1], v[6][kLast - 1], v[7][kLast - 1],
+                                v[8][kLast - 1], v[9][kLast - 1], 0,               0,
+                                v[4][kLast],     v[5][kLast],     v[6][kLast],     v[7][kLast],
+                                v[8][kLast],     v[9][kLast],     0,               0};
+                            tmem_st16(to + 32, x1);
+                        }
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                        tcgen05_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_release_cluster(scale_full_at + 8 * (it % Sc::kBuffers));
+                    }
+                }
+            }
+            cp_async_wait<0>();
+        } else if (GATHER && (warp == 2 || warp == 3 || warp >= W::kFirstGather)) {
+            // Rows by number, four a copy (-1, no such row, arrives as zeros), by one or two
+            // warps for every stage.  The numbers go through shared memory, so that the elected
+            // lane reads them with uniform addresses.
+            const int index = warp < 4 ? warp - 2 : warp - W::kFirstGather + 2;
+            const uint32_t stage = index % kStages;
+            const int sub = index / kStages;
+            const uint32_t bar = full_at + 8 * stage;
+            const uint32_t sb = base + stage * kStageBytes + kABytes;
+            uint32_t it = sub < W::kShare ? stage : ~0u;  // this warp's next step, over the tiles
+            int4 *list = c.list[sub < W::kShare ? index : 0];
+            uint32_t done = 0;                            // steps of the tiles before
+            for (int t = first_tile; t < tiles && ok && it != ~0u; t += tile_step) {
+                const Tile d = tile_of(a, c, t);
+                const int half = d.n / 2, b0 = d.row0 + rank * half;
+                const int row_end = d.row0 + d.nrows;
+                const int quads = (half / 4 - sub + W::kShare - 1) / W::kShare;
+                auto x_row = [&](int i) {
+                    const int v = i < row_end ? __ldg(a.row_index + i) : -1;
+                    return v >= 0 && v < a.x_rows ? v : -1;
+                };
+                if (it < done + steps) {
+                    // every kShare-th four rows of the CTA's half (24 fours at most)
+                    for (int q = lane; q < quads; q += 32) {
+                        const int i = b0 + 4 * (W::kShare * q + sub);
+                        list[q] = make_int4(x_row(i), x_row(i + 1), x_row(i + 2), x_row(i + 3));
+                    }
+                    __syncwarp();
+                }
+                for (; it < done + steps; it += kStages) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_long<true>(empty + 8 * stage,
+                                                           (it / kStages & 1) ^ 1, a.timeout_ns));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const int x = static_cast<int>(it - done) * kStepBytes;
+                        // eight at a time: the numbers are read before the first copy
+                        constexpr int kBatch = 8;
+                        for (int q0 = 0; q0 < quads; q0 += kBatch) {
+                            int4 rows[kBatch];
+#pragma unroll
+                            for (int q = 0; q < kBatch; ++q)
+                                if (q0 + q < quads) rows[q] = list[q0 + q];
+#pragma unroll
+                            for (int q = 0; q < kBatch; ++q)
+                                if (q0 + q < quads)
+                                    tma_gather4<true>(sb + (W::kShare * (q0 + q) + sub) * 512,
+                                                      &maps.b4, x, rows[q], bar);
+                        }
+                    }
+                    __syncwarp();
+                }
+                done += steps;
+            }
+        }
+    }
+    if (!ok && lane == 0) atomicOr(a.status, kStatusWaitTimeout);
+    __syncwarp();
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_barrier();
+    if (warp == 2) {
+        tcgen05_fence_after();
+        tmem_dealloc<2>(tmem, kTmemColumns);
+    }
+}
+
+template <int FORMAT, bool GATHER, bool SUMS>
+cudaError_t launch(const Maps &maps, const Fp4GemmArgs &a, int64_t tiles, cudaStream_t s) {
+    const unsigned ctas = static_cast<unsigned>(2 * min(tiles, int64_t{a.num_pairs}));
+    return launch_ex(fp4_gemm_kernel<FORMAT, GATHER, SUMS>, dim3(ctas),
+                     dim3(Warps<SUMS, GATHER>::kThreads), kSmemBytes, s, 2, a.programmatic, maps, a);
+}
+
+template <int FORMAT, bool GATHER, bool SUMS>
+cudaError_t prepare() {
+    return cudaFuncSetAttribute(fp4_gemm_kernel<FORMAT, GATHER, SUMS>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+}
+
+}  // namespace
+
+cudaError_t prepare_fp4_gemm(int *pairs) {
+    cudaError_t e = find_encoder();
+    if (e == cudaSuccess) e = prepare<kMx, false, false>();
+    if (e == cudaSuccess) e = prepare<kMx, false, true>();
+    if (e == cudaSuccess) e = prepare<kMx, true, false>();
+    if (e == cudaSuccess) e = prepare<kMx, true, true>();
+    if (e == cudaSuccess) e = prepare<kNv, false, false>();
+    if (e == cudaSuccess) e = prepare<kNv, false, true>();
+    if (e == cudaSuccess) e = prepare<kNv, true, false>();
+    if (e == cudaSuccess) e = prepare<kNv, true, true>();
+    if (e != cudaSuccess) return e;
+    // pairs of SMs that run at once: a persistent grid of more would leave some
+    // pairs' tiles for a second wave
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(Warps<true, true>::kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(pairs, fp4_gemm_kernel<kNv, true, true>, &cfg);
+}
+
+cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, cudaStream_t s) {
+    if (few_rows(a.rows, a.num_experts)) return launch_fp4_rows(a, s);
+    using u64 = cuuint64_t;
+    const u64 bytes = a.k / 2, n = a.n, E = a.num_experts, xr = a.x_rows;
+    Maps m = {};
+    const auto type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const u64 w_ld = a.w_ld, w_expert = a.w_expert, x_ld = a.x_ld;
+    if (!encode_map(&m.a, type, a.w, 3, {bytes, n, E}, {w_ld, w_expert}, kStepBytes, 128) ||
+        !encode_map(&m.b, type, a.x, 2, {bytes, xr, 1}, {x_ld, 0}, kStepBytes, 32) ||
+        !encode_map(&m.b4, type, a.x, 2, {bytes, xr, 1}, {x_ld, 0}, kStepBytes, 1))
+        return cudaErrorInvalidValue;
+    // at most this many tiles: the experts' sizes are known on the device only
+    const int64_t tiles = (n + 255) / 256 *
+                          (a.rows / kRowsMax + min(int64_t{a.num_experts}, a.rows));
+    // tiles are counted in 32 bits (results of so many do not fit into memory)
+    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+    const bool sums = a.out_fp32 || a.k > kLongSum, gather = a.row_index != nullptr;
+    if (a.format == kMx) {
+        if (sums)
+            return gather ? launch<kMx, true, true>(m, a, tiles, s)
+                          : launch<kMx, false, true>(m, a, tiles, s);
+        return gather ? launch<kMx, true, false>(m, a, tiles, s)
+                      : launch<kMx, false, false>(m, a, tiles, s);
+    }
+    if (sums)
+        return gather ? launch<kNv, true, true>(m, a, tiles, s)
+                      : launch<kNv, false, true>(m, a, tiles, s);
+    return gather ? launch<kNv, true, false>(m, a, tiles, s)
+                  : launch<kNv, false, false>(m, a, tiles, s);
+}
+
+}  // namespace mf

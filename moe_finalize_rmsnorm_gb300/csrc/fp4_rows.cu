@@ -432,7 +432,4 @@ cudaError_t launch_fp4_rows(const Fp4GemmArgs &a, cudaStream_t s) {
     return few ? launch<kNv, 1>(a, s) : launch<kNv, 2>(a, s);
 }
 
-cudaError_t prepare_fp4_gemm(int *) { return cudaSuccess; }
-cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, cudaStream_t s) { return launch_fp4_rows(a, s); }
-
 }  // namespace mf
