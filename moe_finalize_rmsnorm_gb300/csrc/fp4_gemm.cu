@@ -159,12 +159,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]
         : "memory");
 }
 
-// This CTA's scales are written: an arrival on the first CTA's barrier.
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t remote_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
-                 : "memory");
-}
-
 // 32 output columns (one per lane) by 16 output rows to rows of `out`, turned in the
 // warp's block of shared memory; `cols` and `rows` what exists of the block.
 template <typename V>
@@ -573,8 +567,10 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                         tcgen05_fence_before();
                         __syncwarp();
+                        // relaxed: the fences order it (a release at cluster scope took 0.9
+                        // us a step)
                         if (lane == 0)
-                            mbar_arrive_release_cluster(scale_full_at + 8 * (it % Sc::kBuffers));
+                            mbar_arrive_cluster(scale_full_at + 8 * (it % Sc::kBuffers));
                     }
                 }
             }
