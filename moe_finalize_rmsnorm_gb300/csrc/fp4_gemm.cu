@@ -11,11 +11,11 @@
 // accumulator out, and where rows are gathered, further warps copy them by number.
 //
 // The scales lie in rows beside the values' rows, and the products read them from TMEM:
-// lane l, column c the four bytes of row 32 c + l, the same in each quarter of the lanes.
-// Four warps, one to a quarter, bring 64 bytes a row into shared memory (cp.async, one
-// such group ahead), and write a step's scales into TMEM, two or three steps ahead of the
-// products.  The 128 columns behind the accumulators hold them: that is why a tile ends
-// at 192 rows.
+// lane l, column c the four bytes of row 32 c + l.  Four warps bring 64 bytes a row into
+// shared memory (cp.async, one such group ahead), turn them into blocks of 32 lanes by 16
+// bytes that lie beside the stage's operands, and the warp that issues the products copies
+// a step's blocks into TMEM before it (tcgen05.cp, which runs in order with them).  The 128
+// columns behind the accumulators hold them: that is why a tile ends at 192 rows.
 #include "experts.cuh"
 #include "experts.h"
 #include "fp4.cuh"
@@ -30,9 +30,9 @@ constexpr int kStepBytes = kStep / 2;
 constexpr int kABytes = 128 * kStepBytes;  // A of one CTA and stage
 constexpr int kStageBytes = kABytes + kRowsMax / 2 * kStepBytes;
 constexpr int kStages = 5;
+constexpr int kBlockBytes = 512;          // of scales: 32 lanes by 16 bytes, four TMEM columns
 constexpr int kTmemColumns = 512;         // two accumulators of 192, and the scales
 constexpr int kScaleColumn = 2 * kRowsMax;
-constexpr int kTurnBytes = 2048;          // an epilogue warp's block to turn results in
 constexpr int kScanThreads = 256;         // threads that scan the experts
 constexpr int kScaleRows = 128 + kRowsMax;      // rows whose scales a CTA holds
 constexpr int kGroupBytes = kScaleRows * 64;    // 64 bytes of scales a row
@@ -49,10 +49,12 @@ struct Scales {
     static constexpr int kBytes = FORMAT == kMx ? 8 : 16;     // of a row and step
     static constexpr int kSteps = 64 / kBytes;                // steps of a group
     static constexpr int kWords = kBytes / 4;
+    static constexpr int kStageBytes = 3 * kWords * kBlockBytes;  // the columns', the rows'
     static constexpr int kColumns = 12 * kWords;              // of TMEM, of a step
     static constexpr int kBuffers = FORMAT == kMx ? 4 : 2;    // steps held in TMEM
     static_assert(kScaleColumn + kBuffers * kColumns <= kTmemColumns, "TMEM");
-    static_assert(kBuffers < kStages, "a stage's barrier tells when its scales may go");
+    static constexpr int kRounds = kSteps / 4;                // of a group, a warp a step
+    static_assert(4 <= kStages, "what the waits of the scales' warps rest on");
 };
 
 // Warps: 0 block copies, 1 products, from 4 on the epilogue, then four for the scales,
@@ -70,16 +72,17 @@ struct Warps {
 
 struct Control {
     int4 list[kStages * 2][24];  // rows by number, four a copy; a part for each gathering warp
-    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], scale_full[4];
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], scale_full[kStages];
     uint32_t tmem;
     int scan[kScanThreads / 32];
     int tiles[kMaxExperts + 1];  // row tiles of the experts before this one
     int lo[kMaxExperts + 1];     // first row; the next expert's is the end
 };
 
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 2 * kGroupBytes + 8 * kTurnBytes +
-                           static_cast<int>(sizeof(Control));
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+template <int FORMAT>
+constexpr int kSmemBytes = 1024 + kStages * (kStageBytes + Scales<FORMAT>::kStageBytes) +
+                           2 * kGroupBytes + static_cast<int>(sizeof(Control));
+static_assert(kSmemBytes<kNv> <= 227 * 1024, "shared memory of one CTA");
 
 struct Maps {
     CUtensorMap a, b;  // whole blocks
@@ -140,80 +143,40 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
             : "memory");
 }
 
-// 8 or 16 columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::
-                     "r"(addr),
-                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-                 "r"(v[7])
+// A block of scales from shared memory to four TMEM columns, the same in each quarter of the
+// lanes, in both CTAs; in order with the products.
+__device__ __forceinline__ void scales_to_tmem(uint32_t addr, uint32_t block) {
+    // groups of eight lanes' 16 bytes lie 128 bytes apart, no swizzle
+    const uint64_t desc = uint64_t{(block & 0x3FFFFu) >> 4} | (uint64_t{128 >> 4} << 16) |
+                          (uint64_t{128 >> 4} << 32) | (uint64_t{1} << 46);
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(addr), "l"(desc)
                  : "memory");
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-        "r"(v[15])
-        : "memory");
-}
-
-// 32 output columns (one per lane) by 16 output rows to rows of `out`, turned in the
-// warp's block of shared memory; `cols` and `rows` what exists of the block.
-template <typename V>
-__device__ __forceinline__ void store16(const Fp4GemmArgs &a, uint8_t *block, int64_t out, int cols,
-                                        int rows, const V &value) {
-    const int lane = threadIdx.x % 32;
-    float *f = reinterpret_cast<float *>(block);
-    __syncwarp();
+// 32 output columns (one per lane) by `N` output rows: a row's 64 or 128 bytes are one
+// store of the warp.
+template <int N, typename V>
+__device__ __forceinline__ void store_rows(const Fp4GemmArgs &a, int64_t out, bool col, int rows,
+                                           const V &value) {
+    out += threadIdx.x % 32;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) f[j * 32 + lane] = value(j);
-    __syncwarp();
-    if (a.out_fp32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 4 + lane / 8, col = lane % 8 * 4;
-            if (r < rows && col < cols)
-                *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + out + r * a.out_ld + col) =
-                    *reinterpret_cast<float4 *>(f + r * 32 + col);
+    for (int j = 0; j < N; ++j, out += a.out_ld)
+        if (col && j < rows) {
+            if (a.out_fp32)
+                static_cast<float *>(a.out)[out] = value(j);
+            else
+                static_cast<__nv_bfloat16 *>(a.out)[out] = __float2bfloat16_rn(value(j));
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = i * 8 + lane / 4, col = lane % 4 * 8;
-            if (r >= rows || col >= cols) continue;
-            float y[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) y[u] = f[r * 32 + col + u];
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + out + r * a.out_ld +
-                                       col) = pack8_rn(y);
-        }
-    }
-}
-
-// The same of 32 rows in BF16.
-__device__ __forceinline__ void store32_bf16(const Fp4GemmArgs &a, uint8_t *block, int64_t out,
-                                             int cols, int rows, float factor,
-                                             const uint32_t (&v)[32]) {
-    const int lane = threadIdx.x % 32;
-    __nv_bfloat16 *h = reinterpret_cast<__nv_bfloat16 *>(block);
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-        h[j * 32 + lane] = __float2bfloat16_rn(__uint_as_float(v[j]) * factor);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + lane / 4, col = lane % 4 * 8;
-        if (r < rows && col < cols)
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + out + r * a.out_ld +
-                                       col) = *reinterpret_cast<uint4 *>(h + r * 32 + col);
-    }
 }
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *p, int valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(valid)
+                 : "memory");
+}
+
+__device__ __forceinline__ void sts_16(uint32_t addr, const uint4 &v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
                  : "memory");
 }
 
@@ -228,9 +191,9 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
     using Sc = Scales<FORMAT>;
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-    const uint32_t groups = base + kStages * kStageBytes;
-    uint8_t *blocks = raw + (base - smem_u32(raw)) + kStages * kStageBytes + 2 * kGroupBytes;
-    Control &c = *reinterpret_cast<Control *>(blocks + 8 * kTurnBytes);
+    const uint32_t scale_blocks = base + kStages * kStageBytes;
+    const uint32_t groups = scale_blocks + kStages * Sc::kStageBytes;
+    Control &c = *reinterpret_cast<Control *>(raw + (groups + 2 * kGroupBytes - smem_u32(raw)));
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
     const uint32_t full = smem_u32(c.full), empty = smem_u32(c.empty);
@@ -241,12 +204,12 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
+            mbar_init(scale_full + 8 * i, 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
             mbar_init(acc_empty + 8 * i, W::kEpilogue * 2);
         }
-        for (int i = 0; i < Sc::kBuffers; ++i) mbar_init(scale_full + 8 * i, 4 * 2);
         fence_mbar_init();
     }
     // After the wait, not before: a kernel that this one waits for may want TMEM.
@@ -276,14 +239,13 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
         // per 32 lanes) to all TMEM columns, or eight to every other 32.
         const int w = warp % 4, group = (warp - 4) / 4;
         constexpr int kGroups = W::kEpilogue / 4;
-        uint8_t *block = blocks + (warp - 4) * kTurnBytes;
         const uint32_t done_at = map_to_cta(acc_empty, 0);
         const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
         uint32_t acc_n = 0;  // accumulators taken so far
         for (int t = first_tile; t < tiles && ok; t += tile_step) {
             const Tile d = tile_of(a, c, t);
             const int col0 = d.m0 + rank * 128 + w * 32;
-            const int cols = a.n - col0;  // what exists of the warp's 32
+            const bool col = lane < a.n - col0;
             const float factor = a.factor ? __ldg(a.factor + d.expert) : 1.f;
             auto take = [&]() {  // wait for the next accumulator
                 ok = __all_sync(0xffffffffu, mbar_wait_long<true>(acc_full + 8 * (acc_n & 1),
@@ -330,9 +292,9 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
                         if (r + 16 * part < d.nrows)
-                            store16(a, block, int64_t{d.row0 + r + 16 * part} * a.out_ld + col0, cols,
-                                    d.nrows - r - 16 * part,
-                                    [&](int j) { return sums[i][16 * part + j] * factor; });
+                            store_rows<16>(a, int64_t{d.row0 + r + 16 * part} * a.out_ld + col0, col,
+                                           d.nrows - r - 16 * part,
+                                           [&](int j) { return sums[i][16 * part + j] * factor; });
                 }
             } else {
                 const uint32_t from = take();
@@ -340,8 +302,8 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                 for (int r = 0; r < d.nrows; r += 32) {
                     uint32_t v[32];
                     tmem_ld32(from + r, v);
-                    store32_bf16(a, block, int64_t{d.row0 + r} * a.out_ld + col0, cols, d.nrows - r,
-                                 factor, v);
+                    store_rows<32>(a, int64_t{d.row0 + r} * a.out_ld + col0, col, d.nrows - r,
+                                   [&](int j) { return __uint_as_float(v[j]) * factor; });
                 }
                 give_back();
             }
@@ -407,8 +369,8 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                     }
                     const uint32_t stage = it % kStages, buffer = it % Sc::kBuffers;
                     ok = __all_sync(0xffffffffu,
-                                    mbar_wait_long<true>(scale_full + 8 * buffer,
-                                                         it / Sc::kBuffers & 1, a.timeout_ns) &&
+                                    mbar_wait_long<true>(scale_full + 8 * stage, it / kStages & 1,
+                                                         a.timeout_ns) &&
                                         mbar_wait_long<true>(full + 8 * stage, it / kStages & 1,
                                                              a.timeout_ns));
                     if (!ok) break;
@@ -419,7 +381,12 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                     const uint64_t da = smem_desc(sa, 16, 1024), db = smem_desc(sb, 16, 1024);
                     const int parts = (min(kStep, a.k - s * kStep) + 63) / 64;
                     const bool end = s + 1 == steps || (SUMS && in_segment == kSegment - 1);
+                    const uint32_t blocks = scale_blocks + stage * Sc::kStageBytes;
                     if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < 3 * Sc::kWords; ++i)
+                            if (i < Sc::kWords || (i - Sc::kWords) % 2 == 0 || d.n > 128)
+                                scales_to_tmem(scales + 4 * i, blocks + i * kBlockBytes);
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
                             // 64 summed values: 32 bytes of a row, a word of its scales or half
@@ -440,13 +407,12 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             }
         } else if (warp >= W::kScale && warp < W::kFirstGather) {
             // Scales.  Thread i of 128 copies 16 bytes of every 32nd row, rows 0 .. 127 the
-            // columns', 128 .. 319 the tile's rows; a warp reads them all and writes its
-            // quarter of the lanes.  A warp that gave up goes on meeting the others.
+            // columns', 128 .. 319 the tile's rows; then in rounds of four steps each warp turns
+            // one step's.  A warp that gave up goes on meeting the others.
             const int member = threadIdx.x - 32 * W::kScale;
             const int row_bytes = a.k / (FORMAT == kMx ? 32 : 16);
             const uint32_t scale_full_at = map_to_cta(scale_full, 0);
-            const uint32_t lanes = tmem + kScaleColumn +
-                                   (static_cast<uint32_t>(warp % 4 * 32) << 16);
+            const int w = warp % 4;
             const int tile_groups = divide_up(steps, Sc::kSteps);
             int next_t = first_tile, next_g = 0;  // the group to copy next
             Tile next = {};
@@ -495,27 +461,28 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                 cp_async_commit();
             };
             copy_group(0);
-            uint32_t it = 0, g_it = 0;
+            uint32_t done = 0, g_it = 0;  // steps of the tiles before; groups
             for (int t = first_tile; t < tiles; t += tile_step) {
                 for (int g = 0; g < tile_groups; ++g, ++g_it) {
                     cp_async_wait<0>();
                     scale_warps_meet();  // the group is there, and the one before is read
                     copy_group((g_it + 1) & 1);
                     const uint32_t from = groups + (g_it & 1) * kGroupBytes + lane * 64;
-                    const int end = min(Sc::kSteps, steps - g * Sc::kSteps);
-                    for (int s = 0; s < end; ++s, ++it) {
-                        if (!ok) continue;
-                        // row 32 i + lane, this step's bytes (rows two apart lie in other banks)
-                        uint32_t v[10][Sc::kWords];
-                        const int at = s * Sc::kBytes;
+                    for (int round = 0; round < Sc::kRounds; ++round) {
+                        if (round > 0) scale_warps_meet();
+                        const int in_group = 4 * round + w, s = g * Sc::kSteps + in_group;
+                        if (s >= steps || !ok) continue;
+                        // row 32 i + lane (rows two apart lie in other banks)
+                        const int at = in_group * Sc::kBytes;
                         const uint32_t p = from + (((at / 16) ^ (lane / 2 % 4)) << 4) + at % 16;
+                        uint32_t v[12][Sc::kWords] = {};  // (the last 64 rows do not exist)
 #pragma unroll
                         for (int i = 0; i < 10; ++i) {
                             if constexpr (FORMAT == kMx) {
-                                const uint2 q = *reinterpret_cast<const uint2 *>(
-                                    __cvta_shared_to_generic(p + i * 2048));
-                                v[i][0] = q.x;
-                                v[i][1] = q.y;
+                                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                             : "=r"(v[i][0]), "=r"(v[i][1])
+                                             : "r"(p + i * 2048)
+                                             : "memory");
                             } else {
                                 const uint4 q = lds_16(p + i * 2048);
                                 v[i][0] = q.x;
@@ -524,55 +491,32 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                                 v[i][Sc::kWords - 1] = q.w;
                             }
                         }
-                        // the products of the step that had the place before are done
-                        if (it >= Sc::kBuffers) {
-                            const uint32_t before = it - Sc::kBuffers;
-                            ok = __all_sync(0xffffffffu,
-                                            mbar_wait_long<true>(empty + 8 * (before % kStages),
-                                                                 before / kStages & 1,
-                                                                 a.timeout_ns));
-                            if (!ok) continue;
-                        }
-                        tcgen05_fence_after();
-                        const uint32_t to = lanes + it % Sc::kBuffers * Sc::kColumns;
-                        if constexpr (FORMAT == kMx) {
-                            const uint32_t wv[8] = {v[0][0], v[1][0], v[2][0], v[3][0],
-                                                    v[0][1], v[1][1], v[2][1], v[3][1]};
-                            tmem_st8(to, wv);
-                            const uint32_t xv[16] = {v[4][0], v[5][0], v[6][0], v[7][0],
-                                                     v[8][0], v[9][0], 0,       0,
-                                                     v[4][1], v[5][1], v[6][1], v[7][1],
-                                                     v[8][1], v[9][1], 0,       0};
-                            tmem_st16(to + 8, xv);
-                        } else {
-                            constexpr int kLast = Sc::kWords - 1;
-                            const uint32_t wv[16] = {
-                                v[0][0],         v[1][0],         v[2][0],         v[3][0],
-                                v[0][1],         v[1][1],         v[2][1],         v[3][1],
-                                v[0][kLast - 1], v[1][kLast - 1], v[2][kLast - 1], v[3][kLast - 1],
-                                v[0][kLast],     v[1][kLast],     v[2][kLast],     v[3][kLast]};
-                            tmem_st16(to, wv);
-                            const uint32_t x0[16] = {v[4][0], v[5][0], v[6][0], v[7][0],
-                                                     v[8][0], v[9][0], 0,       0,
-                                                     v[4][1], v[5][1], v[6][1], v[7][1],
-                                                     v[8][1], v[9][1], 0,       0};
-                            tmem_st16(to + 16, x0);
-                            const uint32_t x1[16] = {
-                                v[4][kLast - 1], v[5][kLast - 1], v[6][kLast - 1], v[7][kLast - 1],
-                                v[8][kLast - 1], v[9][kLast - 1], 0,               0,
-                                v[4][kLast],     v[5][kLast],     v[6][kLast],     v[7][kLast],
-                                v[8][kLast],     v[9][kLast],     0,               0};
-                            tmem_st16(to + 32, x1);
-                        }
-                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                        tcgen05_fence_before();
+                        // The stage's last use is done.  Every step before this round is written,
+                        // so the products are done kStages before those, of this step's stage the
+                        // use before the last too; a parity would not tell it from the last.
+                        const uint32_t it = done + s, stage = it % kStages;
+                        ok = __all_sync(0xffffffffu, mbar_wait_long<true>(empty + 8 * stage,
+                                                            (it / kStages & 1) ^ 1, a.timeout_ns));
+                        if (!ok) continue;
+                        const uint32_t to = scale_blocks + stage * Sc::kStageBytes + lane * 16;
+#pragma unroll
+                        for (int j = 0; j < Sc::kWords; ++j)
+#pragma unroll
+                            for (int b = 0; b < 3; ++b) {
+                                const int block = b == 0 ? j : Sc::kWords + 2 * j + b - 1;
+                                sts_16(to + block * kBlockBytes,
+                                       make_uint4(v[4 * b][j], v[4 * b + 1][j], v[4 * b + 2][j],
+                                                  v[4 * b + 3][j]));
+                            }
+                        // The copies to TMEM read this SM's shared memory through the
+                        // asynchronous proxy, issued behind the arrival; so the arrival may
+                        // be relaxed (a release at cluster scope takes 0.9 us).
+                        fence_proxy_async_smem();
                         __syncwarp();
-                        // relaxed: the fences order it (a release at cluster scope took 0.9
-                        // us a step)
-                        if (lane == 0)
-                            mbar_arrive_cluster(scale_full_at + 8 * (it % Sc::kBuffers));
+                        if (lane == 0) mbar_arrive_cluster(scale_full_at + 8 * stage);
                     }
                 }
+                done += steps;
             }
             cp_async_wait<0>();
         } else if (GATHER && (warp == 2 || warp == 3 || warp >= W::kFirstGather)) {
@@ -645,13 +589,13 @@ template <int FORMAT, bool GATHER, bool SUMS>
 cudaError_t launch(const Maps &maps, const Fp4GemmArgs &a, int64_t tiles, cudaStream_t s) {
     const unsigned ctas = static_cast<unsigned>(2 * min(tiles, int64_t{a.num_pairs}));
     return launch_ex(fp4_gemm_kernel<FORMAT, GATHER, SUMS>, dim3(ctas),
-                     dim3(Warps<SUMS, GATHER>::kThreads), kSmemBytes, s, 2, a.programmatic, maps, a);
+                     dim3(Warps<SUMS, GATHER>::kThreads), kSmemBytes<FORMAT>, s, 2, a.programmatic, maps, a);
 }
 
 template <int FORMAT, bool GATHER, bool SUMS>
 cudaError_t prepare() {
     return cudaFuncSetAttribute(fp4_gemm_kernel<FORMAT, GATHER, SUMS>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<FORMAT>);
 }
 
 }  // namespace
@@ -676,7 +620,7 @@ cudaError_t prepare_fp4_gemm(int *pairs) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(Warps<true, true>::kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = kSmemBytes<kNv>;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaOccupancyMaxActiveClusters(pairs, fp4_gemm_kernel<kNv, true, true>, &cfg);
