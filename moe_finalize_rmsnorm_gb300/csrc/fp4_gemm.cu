@@ -100,21 +100,46 @@ struct Tile {
 __device__ __forceinline__ int round_up(int v, int to) { return (v + to - 1) / to * to; }
 __device__ __forceinline__ int divide_up(int v, int by) { return (v + by - 1) / by; }
 
-__device__ __forceinline__ Tile tile_of(const Fp4GemmArgs &a, const Control &c, int t) {
-    const int mt = divide_up(a.n, 256);
-    const int e = expert_of_pass(c.tiles, a.num_experts, kMaxExperts / 2, t / mt);
-    const int rows = c.lo[e + 1] - c.lo[e], rt = c.tiles[e + 1] - c.tiles[e];
-    const int local = t - c.tiles[e] * mt;
-    const int each = round_up(divide_up(rows, rt), 32);  // only the last tile is padded
-    const int first = local % rt * each;
-    Tile r;
-    r.expert = e;
-    r.m0 = local / rt * 256;
-    r.row0 = c.lo[e] + first;
-    r.nrows = min(each, rows - first);
-    r.n = round_up(r.nrows, 32);
-    return r;
-}
+// A pair's tiles in order: every `step`-th one.  An expert's column blocks lie behind each
+// other, the row tiles of a block together.
+struct Walk {
+    const Fp4GemmArgs &a;
+    const Control &c;
+    int left;     // tiles from this one on, of all pairs'
+    int step;
+    int expert;
+    int local;    // the tile's number in its expert, or behind its end
+
+    __device__ Walk(const Fp4GemmArgs &args, const Control &control, int tiles)
+        : a(args), c(control), left(tiles - static_cast<int>(blockIdx.x / 2)),
+          step(gridDim.x / 2), expert(0), local(blockIdx.x / 2) {}
+
+    __device__ bool more() const { return left > 0; }
+
+    // This tile, and on to the next (more() holds).
+    __device__ Tile take() {
+        const int mt = divide_up(a.n, 256);
+        int rt;
+        while (true) {  // ends: the tile numbers of all experts cover this one
+            rt = c.tiles[expert + 1] - c.tiles[expert];
+            if (local < rt * mt) break;
+            local -= rt * mt;
+            ++expert;
+        }
+        const int rows = c.lo[expert + 1] - c.lo[expert];
+        const int each = round_up(divide_up(rows, rt), 32);  // only the last tile is padded
+        const int block = local / rt, first = (local - block * rt) * each;
+        Tile r;
+        r.expert = expert;
+        r.m0 = block * 256;
+        r.row0 = c.lo[expert] + first;
+        r.nrows = min(each, rows - first);
+        r.n = round_up(r.nrows, 32);
+        left -= step;
+        local += step;
+        return r;
+    }
+};
 
 // Instruction descriptor: E2M1 operands along K, FP32 accumulators, M 256; `id`: the first
 // byte of a scale's word.
@@ -225,7 +250,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
 
     const int steps = divide_up(a.k, kStep);
     const int tiles = divide_up(a.n, 256) * total;
-    const int first_tile = blockIdx.x / 2, tile_step = gridDim.x / 2;
+    Walk walk(a, c, tiles);
 
     // Registers: the warps that hold the moved sums take some of the others'
     // (8 * 32 * 144 + 12 * 32 * 64 = the launch's 640 * 96).
@@ -242,8 +267,8 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
         const uint32_t done_at = map_to_cta(acc_empty, 0);
         const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
         uint32_t acc_n = 0;  // accumulators taken so far
-        for (int t = first_tile; t < tiles && ok; t += tile_step) {
-            const Tile d = tile_of(a, c, t);
+        while (ok && walk.more()) {
+            const Tile d = walk.take();
             const int col0 = d.m0 + rank * 128 + w * 32;
             const bool col = lane < a.n - col0;
             const float factor = a.factor ? __ldg(a.factor + d.expert) : 1.f;
@@ -314,8 +339,8 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
         if (warp == 0) {
             // Copies of whole blocks, and each stage's byte count.
             uint32_t it = 0;
-            for (int t = first_tile; t < tiles && ok; t += tile_step) {
-                const Tile d = tile_of(a, c, t);
+            while (ok && walk.more()) {
+                const Tile d = walk.take();
                 const int half = d.n / 2;  // B rows of this CTA
                 const int b0 = d.row0 + rank * half, m0 = d.m0 + rank * 128;
                 const uint32_t bytes = kABytes + round_up(half, GATHER ? 4 : 32) * kStepBytes;
@@ -355,10 +380,11 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
         } else if (warp == 1 && rank == 0) {
             // Products.
             uint32_t it = 0, acc_n = 0;
-            for (int t = first_tile; t < tiles && ok; t += tile_step) {
-                const Tile d = tile_of(a, c, t);
-                const uint32_t idesc = fp4_desc<FORMAT>(d.n, 0);
-                const uint32_t second = fp4_desc<FORMAT>(d.n, 2);  // the word's other two scales
+            int next_n = walk.more() ? walk.take().n : 0;
+            while (ok && next_n > 0) {
+                const int n = next_n;
+                const uint32_t idesc = fp4_desc<FORMAT>(n, 0);
+                const uint32_t second = fp4_desc<FORMAT>(n, 2);  // the word's other two scales
                 for (int s = 0; s < steps; ++s, ++it) {
                     const int in_segment = SUMS ? s % kSegment : s;
                     if (in_segment == 0) {
@@ -385,7 +411,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (int i = 0; i < 3 * Sc::kWords; ++i)
-                            if (i < Sc::kWords || (i - Sc::kWords) % 2 == 0 || d.n > 128)
+                            if (i < Sc::kWords || (i - Sc::kWords) % 2 == 0 || n > 128)
                                 scales_to_tmem(scales + 4 * i, blocks + i * kBlockBytes);
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
@@ -403,6 +429,8 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                     }
                     __syncwarp();
                     if (end) ++acc_n;
+                    // the next tile is found while this one's products run
+                    if (s == 0) next_n = walk.more() ? walk.take().n : 0;
                 }
             }
         } else if (warp >= W::kScale && warp < W::kFirstGather) {
@@ -414,83 +442,99 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             const uint32_t scale_full_at = map_to_cta(scale_full, 0);
             const int w = warp % 4;
             const int tile_groups = divide_up(steps, Sc::kSteps);
-            int next_t = first_tile, next_g = 0;  // the group to copy next
-            Tile next = {};
-            int x_rows[kRowsMax / 32];            // of this thread, -1: none (zeros)
+            // rows lie multiples of 16 bytes apart
+            const uint32_t w_ld = static_cast<uint32_t>(a.ws_ld / 16);
+            const uint32_t x_ld = static_cast<uint32_t>(a.xs_ld / 16);
+            Walk ahead = walk;          // the tile to copy next
+            int next_g = 0;             // its group
+            bool left = ahead.more();
+            const uint8_t *w_from = nullptr;  // this thread's first row of the columns
+            int w_rows = 0;                   // rows 32 u of the tile's columns that exist
+            int x_rows[kRowsMax / 32];        // of this thread, -1: none (zeros)
+            const int chunk = member % 4;
             auto copy_group = [&](uint32_t buffer) {
-                if (next_t < tiles) {
+                if (left) {
                     if (next_g == 0) {
-                        next = tile_of(a, c, next_t);
+                        const Tile d = ahead.take();
+                        const int n = d.m0 + static_cast<int>(rank) * 128 + member / 4;
+                        w_from = a.w_scales + d.expert * a.ws_expert + n * a.ws_ld;
+                        w_rows = (a.n - n + 31) / 32;
 #pragma unroll
                         for (int u = 0; u < kRowsMax / 32; ++u) {
                             const int i = 32 * u + member / 4;
                             int row = -1;
-                            if (i < next.nrows) {
-                                row = next.row0 + i;
+                            if (i < d.nrows) {
+                                row = d.row0 + i;
                                 if (GATHER) row = __ldg(a.row_index + row);
                                 if (row >= a.x_rows) row = -1;
                             }
                             x_rows[u] = row;
                         }
                     }
-                    const int chunk = member % 4, from = next_g * 64 + chunk * 16;
+                    const int from = next_g * 64 + chunk * 16;
                     const int valid = min(max(row_bytes - from, 0), 16);
                     const uint32_t to = groups + buffer * kGroupBytes + member / 4 * 64 +
                                         ((chunk ^ (member / 8 % 4)) << 4);
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        const int n = next.m0 + static_cast<int>(rank) * 128 + 32 * u + member / 4;
-                        const bool read = valid > 0 && n < a.n;
+                        const bool read = valid > 0 && u < w_rows;
                         cp_async_16(to + u * 32 * 64,
-                                    read ? a.w_scales + next.expert * a.ws_expert + n * a.ws_ld + from
+                                    read ? w_from + (static_cast<uint64_t>(w_ld) * (32 * u) << 4) + from
                                          : a.w_scales,
                                     read ? valid : 0);
                     }
 #pragma unroll
                     for (int u = 0; u < kRowsMax / 32; ++u) {
                         const bool read = valid > 0 && x_rows[u] >= 0;
+                        const uint32_t row = read ? x_rows[u] : 0;
                         cp_async_16(to + (128 + u * 32) * 64,
-                                    read ? a.x_scales + x_rows[u] * a.xs_ld + from : a.x_scales,
+                                    a.x_scales + (static_cast<uint64_t>(row) * x_ld << 4) +
+                                        (read ? from : 0),
                                     read ? valid : 0);
                     }
                     if (++next_g == tile_groups) {
                         next_g = 0;
-                        next_t += tile_step;
+                        left = ahead.more();
                     }
                 }
                 cp_async_commit();
             };
+            uint32_t v[12][Sc::kWords] = {};  // of this warp's step (the last 64 rows do not exist)
+            auto read = [&](uint32_t g_it, int in_group) {
+                // row 32 i + lane (rows two apart lie in other banks)
+                const int at = in_group * Sc::kBytes;
+                const uint32_t p = groups + (g_it & 1) * kGroupBytes + lane * 64 +
+                                   (((at / 16) ^ (lane / 2 % 4)) << 4) + at % 16;
+#pragma unroll
+                for (int i = 0; i < 10; ++i) {
+                    if constexpr (FORMAT == kMx) {
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                     : "=r"(v[i][0]), "=r"(v[i][1])
+                                     : "r"(p + i * 2048)
+                                     : "memory");
+                    } else {
+                        const uint4 q = lds_16(p + i * 2048);
+                        v[i][0] = q.x;
+                        v[i][1] = q.y;
+                        v[i][Sc::kWords - 2] = q.z;
+                        v[i][Sc::kWords - 1] = q.w;
+                    }
+                }
+            };
             copy_group(0);
             uint32_t done = 0, g_it = 0;  // steps of the tiles before; groups
-            for (int t = first_tile; t < tiles; t += tile_step) {
+            for (; walk.left > 0; walk.left -= walk.step, done += steps) {
                 for (int g = 0; g < tile_groups; ++g, ++g_it) {
-                    cp_async_wait<0>();
-                    scale_warps_meet();  // the group is there, and the one before is read
-                    copy_group((g_it + 1) & 1);
-                    const uint32_t from = groups + (g_it & 1) * kGroupBytes + lane * 64;
+#pragma unroll 1
                     for (int round = 0; round < Sc::kRounds; ++round) {
-                        if (round > 0) scale_warps_meet();
+                        if (round == 0) cp_async_wait<0>();
+                        // The steps before are written, and a group is there, the one before
+                        // read; its place is filled anew once this round's bytes are on the way.
+                        scale_warps_meet();
                         const int in_group = 4 * round + w, s = g * Sc::kSteps + in_group;
+                        read(g_it, in_group);
+                        if (round == 0) copy_group((g_it + 1) & 1);
                         if (s >= steps || !ok) continue;
-                        // row 32 i + lane (rows two apart lie in other banks)
-                        const int at = in_group * Sc::kBytes;
-                        const uint32_t p = from + (((at / 16) ^ (lane / 2 % 4)) << 4) + at % 16;
-                        uint32_t v[12][Sc::kWords] = {};  // (the last 64 rows do not exist)
-#pragma unroll
-                        for (int i = 0; i < 10; ++i) {
-                            if constexpr (FORMAT == kMx) {
-                                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                             : "=r"(v[i][0]), "=r"(v[i][1])
-                                             : "r"(p + i * 2048)
-                                             : "memory");
-                            } else {
-                                const uint4 q = lds_16(p + i * 2048);
-                                v[i][0] = q.x;
-                                v[i][1] = q.y;
-                                v[i][Sc::kWords - 2] = q.z;
-                                v[i][Sc::kWords - 1] = q.w;
-                            }
-                        }
                         // The stage's last use is done.  Every step before this round is written,
                         // so the products are done kStages before those, of this step's stage the
                         // use before the last too; a parity would not tell it from the last.
@@ -516,7 +560,6 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                         if (lane == 0) mbar_arrive_cluster(scale_full_at + 8 * stage);
                     }
                 }
-                done += steps;
             }
             cp_async_wait<0>();
         } else if (GATHER && (warp == 2 || warp == 3 || warp >= W::kFirstGather)) {
@@ -531,8 +574,8 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             uint32_t it = sub < W::kShare ? stage : ~0u;  // this warp's next step, over the tiles
             int4 *list = c.list[sub < W::kShare ? index : 0];
             uint32_t done = 0;                            // steps of the tiles before
-            for (int t = first_tile; t < tiles && ok && it != ~0u; t += tile_step) {
-                const Tile d = tile_of(a, c, t);
+            while (ok && it != ~0u && walk.more()) {
+                const Tile d = walk.take();
                 const int half = d.n / 2, b0 = d.row0 + rank * half;
                 const int row_end = d.row0 + d.nrows;
                 const int quads = (half / 4 - sub + W::kShare - 1) / W::kShare;
