@@ -72,7 +72,7 @@ struct Warps {
 
 struct Control {
     int4 list[kStages * 2][24];  // rows by number, four a copy; a part for each gathering warp
-    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], scale_full[kStages];
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int scan[kScanThreads / 32];
     int tiles[kMaxExperts + 1];  // row tiles of the experts before this one
@@ -168,14 +168,33 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
             : "memory");
 }
 
-// A block of scales from shared memory to four TMEM columns, the same in each quarter of the
-// lanes, in both CTAs; in order with the products.
-__device__ __forceinline__ void scales_to_tmem(uint32_t addr, uint32_t block) {
-    // groups of eight lanes' 16 bytes lie 128 bytes apart, no swizzle
-    const uint64_t desc = uint64_t{(block & 0x3FFFFu) >> 4} | (uint64_t{128 >> 4} << 16) |
-                          (uint64_t{128 >> 4} << 32) | (uint64_t{1} << 46);
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(addr), "l"(desc)
+// Descriptor of a block of scales: groups of eight lanes' 16 bytes lie 128 bytes apart, no
+// swizzle.
+__device__ __forceinline__ uint64_t block_desc(uint32_t block) {
+    return uint64_t{(block & 0x3FFFFu) >> 4} | (uint64_t{128 >> 4} << 16) |
+           (uint64_t{128 >> 4} << 32) | (uint64_t{1} << 46);
+}
+
+// Such a block to four TMEM columns, the same in each quarter of the lanes, in both CTAs;
+// in order with the products.
+__device__ __forceinline__ void scales_to_tmem(uint32_t addr, uint64_t block) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(addr), "l"(block)
                  : "memory");
+}
+
+// A whole warp's wait on a barrier that either CTA of the pair arrives on: all lanes go on,
+// or all give up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    uint32_t there;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(there)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (__all_sync(0xffffffffu, there)) return true;
+    return __all_sync(0xffffffffu, mbar_wait_long<true>(bar, parity, limit_ns));
 }
 
 // 32 output columns (one per lane) by `N` output rows: a row's 64 or 128 bytes are one
@@ -223,13 +242,11 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
     const uint32_t rank = cluster_ctarank();
     const uint32_t full = smem_u32(c.full), empty = smem_u32(c.empty);
     const uint32_t acc_full = smem_u32(c.acc_full), acc_empty = smem_u32(c.acc_empty);
-    const uint32_t scale_full = smem_u32(c.scale_full);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + 8 * i, 1);
+            mbar_init(full + 8 * i, 1 + 2);  // the copies, and either CTA's scales
             mbar_init(empty + 8 * i, 1);
-            mbar_init(scale_full + 8 * i, 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
@@ -273,8 +290,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             const bool col = lane < a.n - col0;
             const float factor = a.factor ? __ldg(a.factor + d.expert) : 1.f;
             auto take = [&]() {  // wait for the next accumulator
-                ok = __all_sync(0xffffffffu, mbar_wait_long<true>(acc_full + 8 * (acc_n & 1),
-                                                            acc_n >> 1 & 1, a.timeout_ns));
+                ok = warp_wait(acc_full + 8 * (acc_n & 1), acc_n >> 1 & 1, a.timeout_ns);
                 tcgen05_fence_after();
                 return lanes + (acc_n & 1) * kRowsMax;
             };
@@ -338,29 +354,33 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
         const uint32_t full_at = map_to_cta(full, 0);
         if (warp == 0) {
             // Copies of whole blocks, and each stage's byte count.
-            uint32_t it = 0;
+            uint32_t it = 0, stage = 0, phase = 1;
             while (ok && walk.more()) {
                 const Tile d = walk.take();
                 const int half = d.n / 2;  // B rows of this CTA
                 const int b0 = d.row0 + rank * half, m0 = d.m0 + rank * 128;
                 const uint32_t bytes = kABytes + round_up(half, GATHER ? 4 : 32) * kStepBytes;
                 for (int s = 0; s < steps; ++s, ++it) {
-                    const uint32_t stage = it % kStages, phase = it / kStages & 1;
                     // all lanes give up together: the warp meets again below
-                    ok = __all_sync(0xffffffffu, mbar_wait_long<true>(empty + 8 * stage, phase ^ 1,
-                                                                     a.timeout_ns));
+                    ok = warp_wait(empty + 8 * stage, phase, a.timeout_ns);
                     if (!ok) break;
-                    const uint32_t bar = full_at + 8 * stage;
-                    const uint32_t sa = base + stage * kStageBytes, sb = sa + kABytes;
                     if (elect_one()) {
+                        const uint32_t bar = full_at + 8 * stage;
+                        const uint32_t sa = base + stage * kStageBytes, sb = sa + kABytes;
                         if (rank == 0) mbar_arrive_expect_tx(full + 8 * stage, 2 * bytes);
                         tma_3d<true>(sa, &maps.a, s * kStepBytes, m0, d.expert, bar);
                         if (!GATHER)
-                            for (int i = 0; i < half; i += 32)
-                                tma_2d<true>(sb + i * kStepBytes, &maps.b, s * kStepBytes, b0 + i,
-                                             bar);
+#pragma unroll
+                            for (int i = 0; i < kRowsMax / 2; i += 32)
+                                if (i < half)
+                                    tma_2d<true>(sb + i * kStepBytes, &maps.b, s * kStepBytes,
+                                                 b0 + i, bar);
                     }
                     __syncwarp();
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             // The products have read every stage (and the other CTA's completions have
@@ -378,41 +398,41 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                                                a.timeout_ns);
                 }
         } else if (warp == 1 && rank == 0) {
-            // Products.
-            uint32_t it = 0, acc_n = 0;
+            // Products.  A step takes the tensor cores some 400 cycles, and this warp has to
+            // issue its 10 to 16 instructions in less: one barrier a step, places and parities
+            // kept by counting.
+            uint32_t stage = 0, phase = 0, buffer = 0, acc_n = 0;
+            const uint64_t operands = smem_desc(base, 16, 1024);
+            const uint64_t blocks = block_desc(scale_blocks);
+            const int last_parts = (a.k - (steps - 1) * kStep + 63) / 64;
             int next_n = walk.more() ? walk.take().n : 0;
             while (ok && next_n > 0) {
                 const int n = next_n;
                 const uint32_t idesc = fp4_desc<FORMAT>(n, 0);
                 const uint32_t second = fp4_desc<FORMAT>(n, 2);  // the word's other two scales
-                for (int s = 0; s < steps; ++s, ++it) {
-                    const int in_segment = SUMS ? s % kSegment : s;
+                int in_segment = 0;
+                for (int s = 0; s < steps; ++s) {
                     if (in_segment == 0) {
-                        ok = __all_sync(0xffffffffu,
-                                        mbar_wait_long<true>(acc_empty + 8 * (acc_n & 1),
-                                                             (acc_n >> 1 & 1) ^ 1, a.timeout_ns));
+                        ok = warp_wait(acc_empty + 8 * (acc_n & 1), (acc_n >> 1 & 1) ^ 1,
+                                       a.timeout_ns);
                         if (!ok) break;
                     }
-                    const uint32_t stage = it % kStages, buffer = it % Sc::kBuffers;
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait_long<true>(scale_full + 8 * stage, it / kStages & 1,
-                                                         a.timeout_ns) &&
-                                        mbar_wait_long<true>(full + 8 * stage, it / kStages & 1,
-                                                             a.timeout_ns));
+                    ok = warp_wait(full + 8 * stage, phase, a.timeout_ns);
                     if (!ok) break;
                     tcgen05_fence_after();
-                    const uint32_t sa = base + stage * kStageBytes, sb = sa + kABytes;
-                    const uint32_t dst = tmem + (acc_n & 1) * kRowsMax;
-                    const uint32_t scales = tmem + kScaleColumn + buffer * Sc::kColumns;
-                    const uint64_t da = smem_desc(sa, 16, 1024), db = smem_desc(sb, 16, 1024);
-                    const int parts = (min(kStep, a.k - s * kStep) + 63) / 64;
-                    const bool end = s + 1 == steps || (SUMS && in_segment == kSegment - 1);
-                    const uint32_t blocks = scale_blocks + stage * Sc::kStageBytes;
+                    const bool last = s + 1 == steps;
+                    const bool end = last || (SUMS && in_segment == kSegment - 1);
                     if (elect_one()) {
+                        const uint64_t da = operands + stage * (kStageBytes / 16);
+                        const uint64_t db = da + kABytes / 16;
+                        const uint64_t sc = blocks + stage * (Sc::kStageBytes / 16);
+                        const uint32_t dst = tmem + (acc_n & 1) * kRowsMax;
+                        const uint32_t scales = tmem + kScaleColumn + buffer * Sc::kColumns;
+                        const int parts = last ? last_parts : 4;
 #pragma unroll
                         for (int i = 0; i < 3 * Sc::kWords; ++i)
                             if (i < Sc::kWords || (i - Sc::kWords) % 2 == 0 || n > 128)
-                                scales_to_tmem(scales + 4 * i, blocks + i * kBlockBytes);
+                                scales_to_tmem(scales + 4 * i, sc + i * (kBlockBytes / 16));
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
                             // 64 summed values: 32 bytes of a row, a word of its scales or half
@@ -422,13 +442,19 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                                                 FORMAT == kMx && p % 2 ? second : idesc,
                                                 scales + 4 * word,
                                                 scales + 4 * Sc::kWords + 8 * word,
-                                                in_segment + p > 0);
+                                                p > 0 || in_segment > 0);
                         }
                         mma_commit<2>(empty + 8 * stage);
                         if (end) mma_commit<2>(acc_full + 8 * (acc_n & 1));
                     }
                     __syncwarp();
-                    if (end) ++acc_n;
+                    in_segment = end ? 0 : in_segment + 1;
+                    acc_n += end;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    buffer = (buffer + 1) % Sc::kBuffers;
                     // the next tile is found while this one's products run
                     if (s == 0) next_n = walk.more() ? walk.take().n : 0;
                 }
@@ -439,7 +465,6 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             // one step's.  A warp that gave up goes on meeting the others.
             const int member = threadIdx.x - 32 * W::kScale;
             const int row_bytes = a.k / (FORMAT == kMx ? 32 : 16);
-            const uint32_t scale_full_at = map_to_cta(scale_full, 0);
             const int w = warp % 4;
             const int tile_groups = divide_up(steps, Sc::kSteps);
             // rows lie multiples of 16 bytes apart
@@ -539,8 +564,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                         // so the products are done kStages before those, of this step's stage the
                         // use before the last too; a parity would not tell it from the last.
                         const uint32_t it = done + s, stage = it % kStages;
-                        ok = __all_sync(0xffffffffu, mbar_wait_long<true>(empty + 8 * stage,
-                                                            (it / kStages & 1) ^ 1, a.timeout_ns));
+                        ok = warp_wait(empty + 8 * stage, (it / kStages & 1) ^ 1, a.timeout_ns);
                         if (!ok) continue;
                         const uint32_t to = scale_blocks + stage * Sc::kStageBytes + lane * 16;
 #pragma unroll
@@ -557,7 +581,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                         // be relaxed (a release at cluster scope takes 0.9 us).
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(scale_full_at + 8 * stage);
+                        if (lane == 0) mbar_arrive_cluster(full_at + 8 * stage);
                     }
                 }
             }
@@ -592,8 +616,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                     __syncwarp();
                 }
                 for (; it < done + steps; it += kStages) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_long<true>(empty + 8 * stage,
-                                                           (it / kStages & 1) ^ 1, a.timeout_ns));
+                    ok = warp_wait(empty + 8 * stage, (it / kStages & 1) ^ 1, a.timeout_ns);
                     if (!ok) break;
                     if (elect_one()) {
                         const int x = static_cast<int>(it - done) * kStepBytes;
