@@ -34,6 +34,7 @@ constexpr int kBlockBytes = 512;          // of scales: 32 lanes by 16 bytes, fo
 constexpr int kTmemColumns = 512;         // two accumulators of 192, and the scales
 constexpr int kScaleColumn = 2 * kRowsMax;
 constexpr int kScanThreads = 256;         // threads that scan the experts
+constexpr int kListed = 128;              // tiles of a pair that are found at the start
 constexpr int kScaleRows = 128 + kRowsMax;      // rows whose scales a CTA holds
 constexpr int kGroupBytes = kScaleRows * 64;    // 64 bytes of scales a row
 constexpr int kScaleThreads = 128;
@@ -73,6 +74,7 @@ struct Warps {
 struct Control {
     int4 list[kStages * 2][24];  // rows by number, four a copy; a part for each gathering warp
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    int4 listed[kListed];        // this pair's first tiles: expert, column, row, rows
     uint32_t tmem;
     int scan[kScanThreads / 32];
     int tiles[kMaxExperts + 1];  // row tiles of the experts before this one
@@ -100,44 +102,38 @@ struct Tile {
 __device__ __forceinline__ int round_up(int v, int to) { return (v + to - 1) / to * to; }
 __device__ __forceinline__ int divide_up(int v, int by) { return (v + by - 1) / by; }
 
-// A pair's tiles in order: every `step`-th one.  An expert's column blocks lie behind each
-// other, the row tiles of a block together.
+// Tile number t: an expert's column blocks lie behind each other, the row tiles of a block
+// together.
+__device__ __forceinline__ int4 locate_tile(const Fp4GemmArgs &a, const Control &c, int t) {
+    const int mt = divide_up(a.n, 256);
+    const int e = expert_of_pass(c.tiles, a.num_experts, 1 << (31 - __clz(a.num_experts)), t / mt);
+    const int rows = c.lo[e + 1] - c.lo[e], rt = c.tiles[e + 1] - c.tiles[e];
+    const int local = t - c.tiles[e] * mt;
+    const int each = round_up(divide_up(rows, rt), 32);  // only the last tile is padded
+    const int block = local / rt, first = (local - block * rt) * each;
+    return make_int4(e, block * 256, c.lo[e] + first, min(each, rows - first));
+}
+
+// A pair's tiles in order: every `step`-th one.  The first kListed are found by all threads
+// together at the start (a warp that finds one alone takes 0.3 - 0.5 us, once a tile for
+// either of the copies and the products: 12 of 75 us at 12 tiles a pair).
 struct Walk {
     const Fp4GemmArgs &a;
     const Control &c;
-    int left;     // tiles from this one on, of all pairs'
-    int step;
-    int expert;
-    int local;    // the tile's number in its expert, or behind its end
+    const int first, step, count;
+    int i;
 
     __device__ Walk(const Fp4GemmArgs &args, const Control &control, int tiles)
-        : a(args), c(control), left(tiles - static_cast<int>(blockIdx.x / 2)),
-          step(gridDim.x / 2), expert(0), local(blockIdx.x / 2) {}
+        : a(args), c(control), first(blockIdx.x / 2), step(gridDim.x / 2),
+          count((tiles - first + step - 1) / step), i(0) {}
 
-    __device__ bool more() const { return left > 0; }
+    __device__ bool more() const { return i < count; }
 
     // This tile, and on to the next (more() holds).
     __device__ Tile take() {
-        const int mt = divide_up(a.n, 256);
-        int rt;
-        while (true) {  // ends: the tile numbers of all experts cover this one
-            rt = c.tiles[expert + 1] - c.tiles[expert];
-            if (local < rt * mt) break;
-            local -= rt * mt;
-            ++expert;
-        }
-        const int rows = c.lo[expert + 1] - c.lo[expert];
-        const int each = round_up(divide_up(rows, rt), 32);  // only the last tile is padded
-        const int block = local / rt, first = (local - block * rt) * each;
-        Tile r;
-        r.expert = expert;
-        r.m0 = block * 256;
-        r.row0 = c.lo[expert] + first;
-        r.nrows = min(each, rows - first);
-        r.n = round_up(r.nrows, 32);
-        left -= step;
-        local += step;
-        return r;
+        const int4 t = i < kListed ? c.listed[i] : locate_tile(a, c, first + i * step);
+        ++i;
+        return Tile{t.x, t.y, t.z, t.w, round_up(t.w, 32)};
     }
 };
 
@@ -259,15 +255,16 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
     if (warp == 2) tmem_alloc<2>(smem_u32(&c.tmem), kTmemColumns);
     const int total = scan_experts<kScanThreads>(a.offsets, a.num_experts, static_cast<int>(a.rows),
                                                  kRowsMax, c.lo, c.tiles, c.scan);
+    const int steps = divide_up(a.k, kStep);
+    Walk walk(a, c, divide_up(a.n, 256) * total);
+    __syncthreads();
+    if (threadIdx.x < min(walk.count, kListed))
+        c.listed[threadIdx.x] = locate_tile(a, c, walk.first + threadIdx.x * walk.step);
     tcgen05_fence_before();
     __syncthreads();
     cluster_barrier();
     tcgen05_fence_after();
     const uint32_t tmem = c.tmem;
-
-    const int steps = divide_up(a.k, kStep);
-    const int tiles = divide_up(a.n, 256) * total;
-    Walk walk(a, c, tiles);
 
     // Registers: the warps that hold the moved sums take some of the others'
     // (8 * 32 * 144 + 12 * 32 * 64 = the launch's 640 * 96).
@@ -548,7 +545,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             };
             copy_group(0);
             uint32_t done = 0, g_it = 0;  // steps of the tiles before; groups
-            for (; walk.left > 0; walk.left -= walk.step, done += steps) {
+            for (; walk.more(); ++walk.i, done += steps) {
                 for (int g = 0; g < tile_groups; ++g, ++g_it) {
 #pragma unroll 1
                     for (int round = 0; round < Sc::kRounds; ++round) {
