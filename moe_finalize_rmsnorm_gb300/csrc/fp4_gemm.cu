@@ -7,15 +7,16 @@
 // pair of SMs, each holding half of either operand, and its N an expert's rows, any
 // multiple of 32 up to 192.  A persistent pair per two SMs walks the tiles: a warp
 // copies blocks (TMA, 128-byte swizzle, 256 summed values a step), a warp issues the
-// products into one of two accumulators in TMEM, four or eight warps move the other
-// accumulator out, and where rows are gathered, further warps copy them by number.
+// products into one of two accumulators in TMEM, eight warps move the other accumulator
+// out, and where rows are gathered, further warps copy them by number.
 //
 // The scales lie in rows beside the values' rows, and the products read them from TMEM:
-// lane l, column c the four bytes of row 32 c + l.  Four warps bring 64 bytes a row into
-// shared memory (cp.async, one such group ahead), turn them into blocks of 32 lanes by 16
-// bytes that lie beside the stage's operands, and the warp that issues the products copies
-// a step's blocks into TMEM before it (tcgen05.cp, which runs in order with them).  The 128
-// columns behind the accumulators hold them: that is why a tile ends at 192 rows.
+// lane l, column c the four bytes of row 32 c + l.  Four warps read 64 bytes a row (a
+// group: four or eight steps; four lanes to a row, the rows 32 apart in one thread), write
+// them to shared memory as blocks of 32 lanes by 16 bytes, and the warp that issues the
+// products copies a step's blocks into TMEM before it (tcgen05.cp, which runs in order with
+// them).  The 128 columns behind the accumulators hold them: that is why a tile ends at 192
+// rows.
 #include "experts.cuh"
 #include "experts.h"
 #include "fp4.cuh"
@@ -29,15 +30,16 @@ constexpr int kStep = 256;                // summed values per stage: 128 bytes
 constexpr int kStepBytes = kStep / 2;
 constexpr int kABytes = 128 * kStepBytes;  // A of one CTA and stage
 constexpr int kStageBytes = kABytes + kRowsMax / 2 * kStepBytes;
-constexpr int kStages = 5;
+constexpr int kStages = 6;
 constexpr int kBlockBytes = 512;          // of scales: 32 lanes by 16 bytes, four TMEM columns
 constexpr int kTmemColumns = 512;         // two accumulators of 192, and the scales
 constexpr int kScaleColumn = 2 * kRowsMax;
 constexpr int kScanThreads = 256;         // threads that scan the experts
 constexpr int kListed = 128;              // tiles of a pair that are found at the start
-constexpr int kScaleRows = 128 + kRowsMax;      // rows whose scales a CTA holds
-constexpr int kGroupBytes = kScaleRows * 64;    // 64 bytes of scales a row
-constexpr int kScaleThreads = 128;
+// Scales of a group, 64 bytes a row: four pieces of 16 bytes a row (one step's, or two), as
+// blocks for 128 columns and 256 rows.
+constexpr int kPieceBytes = 12 * kBlockBytes;
+constexpr int kGroupBytes = 4 * kPieceBytes;
 
 // FP32 results, and BF16 results of more than kLongSum summed values: the sums leave the
 // tensor cores every this many steps and are added up in registers, as the tensor cores
@@ -50,19 +52,17 @@ struct Scales {
     static constexpr int kBytes = FORMAT == kMx ? 8 : 16;     // of a row and step
     static constexpr int kSteps = 64 / kBytes;                // steps of a group
     static constexpr int kWords = kBytes / 4;
-    static constexpr int kStageBytes = 3 * kWords * kBlockBytes;  // the columns', the rows'
+    static constexpr int kStepBytes = 3 * kWords * kBlockBytes;  // the columns', the rows'
     static constexpr int kColumns = 12 * kWords;              // of TMEM, of a step
     static constexpr int kBuffers = FORMAT == kMx ? 4 : 2;    // steps held in TMEM
     static_assert(kScaleColumn + kBuffers * kColumns <= kTmemColumns, "TMEM");
-    static constexpr int kRounds = kSteps / 4;                // of a group, a warp a step
-    static_assert(4 <= kStages, "what the waits of the scales' warps rest on");
 };
 
 // Warps: 0 block copies, 1 products, from 4 on the epilogue, then four for the scales,
 // then those that gather (with 2 and 3).
 template <bool SUMS, bool GATHER>
 struct Warps {
-    static constexpr int kEpilogue = SUMS ? 8 : 4;
+    static constexpr int kEpilogue = 8;
     static constexpr int kScale = 4 + kEpilogue;
     static constexpr int kFirstGather = kScale + 4;
     static constexpr int kShare = SUMS ? 1 : 2;  // gathering warps of a stage
@@ -72,19 +72,19 @@ struct Warps {
 };
 
 struct Control {
-    int4 list[kStages * 2][24];  // rows by number, four a copy; a part for each gathering warp
-    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    int4 list[kStages * 24];     // rows by number, four a copy; a part for each gathering warp
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], scale_full[2],
+        scale_empty[2];
     int4 listed[kListed];        // this pair's first tiles: expert, column, row, rows
     uint32_t tmem;
     int scan[kScanThreads / 32];
     int tiles[kMaxExperts + 1];  // row tiles of the experts before this one
-    int lo[kMaxExperts + 1];     // first row; the next expert's is the end
 };
 
-template <int FORMAT>
-constexpr int kSmemBytes = 1024 + kStages * (kStageBytes + Scales<FORMAT>::kStageBytes) +
-                           2 * kGroupBytes + static_cast<int>(sizeof(Control));
-static_assert(kSmemBytes<kNv> <= 227 * 1024, "shared memory of one CTA");
+constexpr int kSmemBytes =
+    1024 + kStages * kStageBytes + 2 * kGroupBytes + static_cast<int>(sizeof(Control));
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+static_assert((kMaxExperts + 1) * 4 <= kStageBytes, "the experts' first rows, at the start");
 
 struct Maps {
     CUtensorMap a, b;  // whole blocks
@@ -102,16 +102,23 @@ struct Tile {
 __device__ __forceinline__ int round_up(int v, int to) { return (v + to - 1) / to * to; }
 __device__ __forceinline__ int divide_up(int v, int by) { return (v + by - 1) / by; }
 
+// A value that all lanes hold alike, known to the compiler as such: what the asynchronous
+// instructions take from uniform registers is then computed there, and branches on it do not
+// count as divergent.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Tile number t: an expert's column blocks lie behind each other, the row tiles of a block
 // together.
-__device__ __forceinline__ int4 locate_tile(const Fp4GemmArgs &a, const Control &c, int t) {
+template <typename Lo>
+__device__ __forceinline__ int4 locate_tile(const Fp4GemmArgs &a, const Control &c, int t,
+                                            const Lo &lo) {
     const int mt = divide_up(a.n, 256);
     const int e = expert_of_pass(c.tiles, a.num_experts, 1 << (31 - __clz(a.num_experts)), t / mt);
-    const int rows = c.lo[e + 1] - c.lo[e], rt = c.tiles[e + 1] - c.tiles[e];
+    const int row0 = lo(e), rows = lo(e + 1) - row0, rt = c.tiles[e + 1] - c.tiles[e];
     const int local = t - c.tiles[e] * mt;
     const int each = round_up(divide_up(rows, rt), 32);  // only the last tile is padded
     const int block = local / rt, first = (local - block * rt) * each;
-    return make_int4(e, block * 256, c.lo[e] + first, min(each, rows - first));
+    return make_int4(e, block * 256, row0 + first, min(each, rows - first));
 }
 
 // A pair's tiles in order: every `step`-th one.  The first kListed are found by all threads
@@ -131,9 +138,18 @@ struct Walk {
 
     // This tile, and on to the next (more() holds).
     __device__ Tile take() {
-        const int4 t = i < kListed ? c.listed[i] : locate_tile(a, c, first + i * step);
+        int4 t;
+        if (i < kListed)
+            t = c.listed[i];
+        else
+            t = locate_tile(a, c, first + i * step, [&](int e) {  // as scan_experts does
+                const int rows = static_cast<int>(a.rows);
+                if (!a.offsets) return e == 0 ? 0 : rows;
+                return min(max(__ldg(a.offsets + e), 0), rows);
+            });
         ++i;
-        return Tile{t.x, t.y, t.z, t.w, round_up(t.w, 32)};
+        const int rows = uniform(t.w);
+        return Tile{uniform(t.x), uniform(t.y), uniform(t.z), rows, round_up(rows, 32)};
     }
 };
 
@@ -209,19 +225,10 @@ __device__ __forceinline__ void store_rows(const Fp4GemmArgs &a, int64_t out, bo
         }
 }
 
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *p, int valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(valid)
-                 : "memory");
-}
-
 __device__ __forceinline__ void sts_16(uint32_t addr, const uint4 &v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
                  "r"(v.z), "r"(v.w)
                  : "memory");
-}
-
-__device__ __forceinline__ void scale_warps_meet() {
-    asm volatile("bar.sync 1, %0;" ::"n"(kScaleThreads) : "memory");
 }
 
 template <int FORMAT, bool GATHER, bool SUMS>
@@ -231,40 +238,46 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
     using Sc = Scales<FORMAT>;
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-    const uint32_t scale_blocks = base + kStages * kStageBytes;
-    const uint32_t groups = scale_blocks + kStages * Sc::kStageBytes;
+    const uint32_t groups = base + kStages * kStageBytes;
     Control &c = *reinterpret_cast<Control *>(raw + (groups + 2 * kGroupBytes - smem_u32(raw)));
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
     const uint32_t full = smem_u32(c.full), empty = smem_u32(c.empty);
     const uint32_t acc_full = smem_u32(c.acc_full), acc_empty = smem_u32(c.acc_empty);
+    const uint32_t scale_full = smem_u32(c.scale_full), scale_empty = smem_u32(c.scale_empty);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + 8 * i, 1 + 2);  // the copies, and either CTA's scales
+            mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
             mbar_init(acc_empty + 8 * i, W::kEpilogue * 2);
+            mbar_init(scale_full + 8 * i, 4 * 2);
+            mbar_init(scale_empty + 8 * i, 1);
         }
         fence_mbar_init();
     }
     // After the wait, not before: a kernel that this one waits for may want TMEM.
     pdl_wait();
     if (warp == 2) tmem_alloc<2>(smem_u32(&c.tmem), kTmemColumns);
+    // the experts' first rows lie where the operands will: only the list is made from them
+    int *lo = reinterpret_cast<int *>(raw + (base - smem_u32(raw)));
     const int total = scan_experts<kScanThreads>(a.offsets, a.num_experts, static_cast<int>(a.rows),
-                                                 kRowsMax, c.lo, c.tiles, c.scan);
+                                                 kRowsMax, lo, c.tiles, c.scan);
     const int steps = divide_up(a.k, kStep);
-    Walk walk(a, c, divide_up(a.n, 256) * total);
+    Walk walk(a, c, uniform(divide_up(a.n, 256) * total));
     __syncthreads();
     if (threadIdx.x < min(walk.count, kListed))
-        c.listed[threadIdx.x] = locate_tile(a, c, walk.first + threadIdx.x * walk.step);
+        c.listed[threadIdx.x] = locate_tile(a, c, walk.first + threadIdx.x * walk.step,
+                                            [&](int e) { return lo[e]; });
+    fence_proxy_async_smem();  // before the copies overwrite them
     tcgen05_fence_before();
     __syncthreads();
     cluster_barrier();
     tcgen05_fence_after();
-    const uint32_t tmem = c.tmem;
+    const uint32_t tmem = uniform(c.tmem);
 
     // Registers: the warps that hold the moved sums take some of the others'
     // (8 * 32 * 144 + 12 * 32 * 64 = the launch's 640 * 96).
@@ -274,8 +287,8 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
     bool ok = true;
     if (warp >= 4 && warp < W::kScale) {
         if constexpr (kMoveRegisters) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
-        // Results: lane = output column, TMEM column = output row; four warps (one
-        // per 32 lanes) to all TMEM columns, or eight to every other 32.
+        // Results: lane = output column, TMEM column = output row; eight warps, of which
+        // two take the same 32 lanes and every other 32 rows.
         const int w = warp % 4, group = (warp - 4) / 4;
         constexpr int kGroups = W::kEpilogue / 4;
         const uint32_t done_at = map_to_cta(acc_empty, 0);
@@ -337,7 +350,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             } else {
                 const uint32_t from = take();
                 if (!ok) break;
-                for (int r = 0; r < d.nrows; r += 32) {
+                for (int r = group * 32; r < d.nrows; r += kGroups * 32) {
                     uint32_t v[32];
                     tmem_ld32(from + r, v);
                     store_rows<32>(a, int64_t{d.row0 + r} * a.out_ld + col0, col, d.nrows - r,
@@ -398,17 +411,21 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             // Products.  A step takes the tensor cores some 400 cycles, and this warp has to
             // issue its 10 to 16 instructions in less: one barrier a step, places and parities
             // kept by counting.
-            uint32_t stage = 0, phase = 0, buffer = 0, acc_n = 0;
-            const uint64_t operands = smem_desc(base, 16, 1024);
-            const uint64_t blocks = block_desc(scale_blocks);
+            uint32_t stage = 0, phase = 0, buffer = 0, acc_n = 0, group_n = 0;
+            const uint64_t operands = smem_desc(base, 16, 1024), blocks = block_desc(groups);
             const int last_parts = (a.k - (steps - 1) * kStep + 63) / 64;
             int next_n = walk.more() ? walk.take().n : 0;
             while (ok && next_n > 0) {
                 const int n = next_n;
                 const uint32_t idesc = fp4_desc<FORMAT>(n, 0);
                 const uint32_t second = fp4_desc<FORMAT>(n, 2);  // the word's other two scales
-                int in_segment = 0;
+                int in_segment = 0, in_group = 0;
                 for (int s = 0; s < steps; ++s) {
+                    if (in_group == 0) {
+                        ok = warp_wait(scale_full + 8 * (group_n & 1), group_n >> 1 & 1,
+                                       a.timeout_ns);
+                        if (!ok) break;
+                    }
                     if (in_segment == 0) {
                         ok = warp_wait(acc_empty + 8 * (acc_n & 1), (acc_n >> 1 & 1) ^ 1,
                                        a.timeout_ns);
@@ -419,10 +436,15 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                     tcgen05_fence_after();
                     const bool last = s + 1 == steps;
                     const bool end = last || (SUMS && in_segment == kSegment - 1);
+                    const bool group_end = last || in_group == Sc::kSteps - 1;
                     if (elect_one()) {
                         const uint64_t da = operands + stage * (kStageBytes / 16);
                         const uint64_t db = da + kABytes / 16;
-                        const uint64_t sc = blocks + stage * (Sc::kStageBytes / 16);
+                        const int piece = FORMAT == kMx ? in_group / 2 : in_group;
+                        const uint64_t sc = blocks + (group_n & 1) * (kGroupBytes / 16) +
+                                            piece * (kPieceBytes / 16) +
+                                            (FORMAT == kMx ? in_group % 2 : 0) *
+                                                (Sc::kStepBytes / 16);
                         const uint32_t dst = tmem + (acc_n & 1) * kRowsMax;
                         const uint32_t scales = tmem + kScaleColumn + buffer * Sc::kColumns;
                         const int parts = last ? last_parts : 4;
@@ -442,11 +464,14 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                                                 p > 0 || in_segment > 0);
                         }
                         mma_commit<2>(empty + 8 * stage);
+                        if (group_end) mma_commit<2>(scale_empty + 8 * (group_n & 1));
                         if (end) mma_commit<2>(acc_full + 8 * (acc_n & 1));
                     }
                     __syncwarp();
                     in_segment = end ? 0 : in_segment + 1;
+                    in_group = group_end ? 0 : in_group + 1;
                     acc_n += end;
+                    group_n += group_end;
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1;
@@ -457,132 +482,98 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                 }
             }
         } else if (warp >= W::kScale && warp < W::kFirstGather) {
-            // Scales.  Thread i of 128 copies 16 bytes of every 32nd row, rows 0 .. 127 the
-            // columns', 128 .. 319 the tile's rows; then in rounds of four steps each warp turns
-            // one step's.  A warp that gave up goes on meeting the others.
-            const int member = threadIdx.x - 32 * W::kScale;
+            // Scales.  A thread takes 16 bytes (a piece) of one row in 32 and of those every 32
+            // behind it: four of the tile's columns, and up to six of its rows, of which four
+            // rows' words make a lane of a block.  They are read a group ahead.  Eight lanes
+            // have eight rows' same piece: 128 bytes of a block.
             const int row_bytes = a.k / (FORMAT == kMx ? 32 : 16);
-            const int w = warp % 4;
-            const int tile_groups = divide_up(steps, Sc::kSteps);
-            // rows lie multiples of 16 bytes apart
-            const uint32_t w_ld = static_cast<uint32_t>(a.ws_ld / 16);
-            const uint32_t x_ld = static_cast<uint32_t>(a.xs_ld / 16);
-            Walk ahead = walk;          // the tile to copy next
-            int next_g = 0;             // its group
-            bool left = ahead.more();
+            const uint32_t scale_full_at = map_to_cta(scale_full, 0);
+            const int groups_of_tile = divide_up(steps, Sc::kSteps);
+            const int line = warp % 4 * 8 + lane % 8, piece = lane / 8;
             const uint8_t *w_from = nullptr;  // this thread's first row of the columns
-            int w_rows = 0;                   // rows 32 u of the tile's columns that exist
-            int x_rows[kRowsMax / 32];        // of this thread, -1: none (zeros)
-            const int chunk = member % 4;
-            auto copy_group = [&](uint32_t buffer) {
-                if (left) {
-                    if (next_g == 0) {
-                        const Tile d = ahead.take();
-                        const int n = d.m0 + static_cast<int>(rank) * 128 + member / 4;
-                        w_from = a.w_scales + d.expert * a.ws_expert + n * a.ws_ld;
-                        w_rows = (a.n - n + 31) / 32;
-#pragma unroll
-                        for (int u = 0; u < kRowsMax / 32; ++u) {
-                            const int i = 32 * u + member / 4;
-                            int row = -1;
-                            if (i < d.nrows) {
-                                row = d.row0 + i;
-                                if (GATHER) row = __ldg(a.row_index + row);
-                                if (row >= a.x_rows) row = -1;
-                            }
-                            x_rows[u] = row;
-                        }
-                    }
-                    const int from = next_g * 64 + chunk * 16;
-                    const int valid = min(max(row_bytes - from, 0), 16);
-                    const uint32_t to = groups + buffer * kGroupBytes + member / 4 * 64 +
-                                        ((chunk ^ (member / 8 % 4)) << 4);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const bool read = valid > 0 && u < w_rows;
-                        cp_async_16(to + u * 32 * 64,
-                                    read ? w_from + (static_cast<uint64_t>(w_ld) * (32 * u) << 4) + from
-                                         : a.w_scales,
-                                    read ? valid : 0);
-                    }
+            int w_rows = 0;                   // rows of them that exist
+            int x_rows[kRowsMax / 32];        // -1: none (zeros)
+            uint4 q[12] = {};                 // (the last 64 rows of the blocks do not exist)
+            // 16 bytes, zeros behind the first `valid`
+            auto load = [&](const uint8_t *p, int valid) {
+                if (valid >= 16) return __ldg(reinterpret_cast<const uint4 *>(p));
+                uint64_t lo = 0, hi = 0;
+                for (int i = 0; i < valid; ++i) {
+                    const uint64_t byte = __ldg(p + i);
+                    if (i < 8)
+                        lo |= byte << (8 * i);
+                    else
+                        hi |= byte << (8 * i - 64);
+                }
+                return make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
+                                  static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32));
+            };
+            int next_g = 0;  // the group to read next, of the tile at hand
+            auto read_group = [&]() {
+                if (next_g == 0) {
+                    if (!walk.more()) return;
+                    const Tile d = walk.take();
+                    const int n = d.m0 + static_cast<int>(rank) * 128 + line;
+                    w_from = a.w_scales + d.expert * a.ws_expert + n * a.ws_ld;
+                    w_rows = (a.n - n + 31) / 32;
 #pragma unroll
                     for (int u = 0; u < kRowsMax / 32; ++u) {
-                        const bool read = valid > 0 && x_rows[u] >= 0;
-                        const uint32_t row = read ? x_rows[u] : 0;
-                        cp_async_16(to + (128 + u * 32) * 64,
-                                    a.x_scales + (static_cast<uint64_t>(row) * x_ld << 4) +
-                                        (read ? from : 0),
-                                    read ? valid : 0);
-                    }
-                    if (++next_g == tile_groups) {
-                        next_g = 0;
-                        left = ahead.more();
+                        const int i = 32 * u + line;
+                        int row = -1;
+                        if (i < d.nrows) {
+                            row = d.row0 + i;
+                            if (GATHER) row = __ldg(a.row_index + row);
+                            if (row >= a.x_rows) row = -1;
+                        }
+                        x_rows[u] = row;
                     }
                 }
-                cp_async_commit();
+                const int from = next_g * 64 + piece * 16, valid = row_bytes - from;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    q[u] = make_uint4(0, 0, 0, 0);
+                    if (valid > 0 && u < w_rows) q[u] = load(w_from + 32 * u * a.ws_ld + from, valid);
+                }
+#pragma unroll
+                for (int u = 0; u < kRowsMax / 32; ++u) {
+                    q[4 + u] = make_uint4(0, 0, 0, 0);
+                    if (valid > 0 && x_rows[u] >= 0)
+                        q[4 + u] = load(a.x_scales + x_rows[u] * a.xs_ld + from, valid);
+                }
+                if (++next_g == groups_of_tile) next_g = 0;
             };
-            uint32_t v[12][Sc::kWords] = {};  // of this warp's step (the last 64 rows do not exist)
-            auto read = [&](uint32_t g_it, int in_group) {
-                // row 32 i + lane (rows two apart lie in other banks)
-                const int at = in_group * Sc::kBytes;
-                const uint32_t p = groups + (g_it & 1) * kGroupBytes + lane * 64 +
-                                   (((at / 16) ^ (lane / 2 % 4)) << 4) + at % 16;
+            const int all = walk.count * groups_of_tile;  // (a tile's columns bound both)
+            read_group();
+            int g = 0;
+            for (; g < all; ++g) {
+                ok = warp_wait(scale_empty + 8 * (g & 1), (g >> 1 & 1) ^ 1, a.timeout_ns);
+                if (!ok) break;
+                const uint32_t to = groups + (g & 1) * kGroupBytes + piece * kPieceBytes + line * 16;
 #pragma unroll
-                for (int i = 0; i < 10; ++i) {
-                    if constexpr (FORMAT == kMx) {
-                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                     : "=r"(v[i][0]), "=r"(v[i][1])
-                                     : "r"(p + i * 2048)
-                                     : "memory");
-                    } else {
-                        const uint4 q = lds_16(p + i * 2048);
-                        v[i][0] = q.x;
-                        v[i][1] = q.y;
-                        v[i][Sc::kWords - 2] = q.z;
-                        v[i][Sc::kWords - 1] = q.w;
+                for (int j = 0; j < 4; ++j) {  // words of the 16 bytes
+                    const int step = j / Sc::kWords, word = j % Sc::kWords;
+#pragma unroll
+                    for (int b = 0; b < 3; ++b) {
+                        const int block = step * 3 * Sc::kWords +
+                                          (b == 0 ? word : Sc::kWords + 2 * word + b - 1);
+                        const auto w = [&](const uint4 &v) {
+                            return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+                        };
+                        sts_16(to + block * kBlockBytes, make_uint4(w(q[4 * b]), w(q[4 * b + 1]),
+                                                                    w(q[4 * b + 2]), w(q[4 * b + 3])));
                     }
                 }
-            };
-            copy_group(0);
-            uint32_t done = 0, g_it = 0;  // steps of the tiles before; groups
-            for (; walk.more(); ++walk.i, done += steps) {
-                for (int g = 0; g < tile_groups; ++g, ++g_it) {
-#pragma unroll 1
-                    for (int round = 0; round < Sc::kRounds; ++round) {
-                        if (round == 0) cp_async_wait<0>();
-                        // The steps before are written, and a group is there, the one before
-                        // read; its place is filled anew once this round's bytes are on the way.
-                        scale_warps_meet();
-                        const int in_group = 4 * round + w, s = g * Sc::kSteps + in_group;
-                        read(g_it, in_group);
-                        if (round == 0) copy_group((g_it + 1) & 1);
-                        if (s >= steps || !ok) continue;
-                        // The stage's last use is done.  Every step before this round is written,
-                        // so the products are done kStages before those, of this step's stage the
-                        // use before the last too; a parity would not tell it from the last.
-                        const uint32_t it = done + s, stage = it % kStages;
-                        ok = warp_wait(empty + 8 * stage, (it / kStages & 1) ^ 1, a.timeout_ns);
-                        if (!ok) continue;
-                        const uint32_t to = scale_blocks + stage * Sc::kStageBytes + lane * 16;
-#pragma unroll
-                        for (int j = 0; j < Sc::kWords; ++j)
-#pragma unroll
-                            for (int b = 0; b < 3; ++b) {
-                                const int block = b == 0 ? j : Sc::kWords + 2 * j + b - 1;
-                                sts_16(to + block * kBlockBytes,
-                                       make_uint4(v[4 * b][j], v[4 * b + 1][j], v[4 * b + 2][j],
-                                                  v[4 * b + 3][j]));
-                            }
-                        // The copies to TMEM read this SM's shared memory through the
-                        // asynchronous proxy, issued behind the arrival; so the arrival may
-                        // be relaxed (a release at cluster scope takes 0.9 us).
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(full_at + 8 * stage);
-                    }
-                }
+                // The copies to TMEM read this SM's shared memory through the asynchronous
+                // proxy, issued behind the arrival; so the arrival may be relaxed (a release at
+                // cluster scope takes 0.9 us).
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(scale_full_at + 8 * (g & 1));
+                read_group();
             }
-            cp_async_wait<0>();
+            // the last groups' products are done, before this CTA may leave
+            for (int i = max(g - 2, 0); ok && i < g; ++i)
+                ok = warp_wait(scale_empty + 8 * (i & 1), i >> 1 & 1, a.timeout_ns);
         } else if (GATHER && (warp == 2 || warp == 3 || warp >= W::kFirstGather)) {
             // Rows by number, four a copy (-1, no such row, arrives as zeros), by one or two
             // warps for every stage.  The numbers go through shared memory, so that the elected
@@ -593,7 +584,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             const uint32_t bar = full_at + 8 * stage;
             const uint32_t sb = base + stage * kStageBytes + kABytes;
             uint32_t it = sub < W::kShare ? stage : ~0u;  // this warp's next step, over the tiles
-            int4 *list = c.list[sub < W::kShare ? index : 0];
+            int4 *list = c.list + (sub < W::kShare ? index : 0) * (24 / W::kShare);
             uint32_t done = 0;                            // steps of the tiles before
             while (ok && it != ~0u && walk.more()) {
                 const Tile d = walk.take();
@@ -652,13 +643,13 @@ template <int FORMAT, bool GATHER, bool SUMS>
 cudaError_t launch(const Maps &maps, const Fp4GemmArgs &a, int64_t tiles, cudaStream_t s) {
     const unsigned ctas = static_cast<unsigned>(2 * min(tiles, int64_t{a.num_pairs}));
     return launch_ex(fp4_gemm_kernel<FORMAT, GATHER, SUMS>, dim3(ctas),
-                     dim3(Warps<SUMS, GATHER>::kThreads), kSmemBytes<FORMAT>, s, 2, a.programmatic, maps, a);
+                     dim3(Warps<SUMS, GATHER>::kThreads), kSmemBytes, s, 2, a.programmatic, maps, a);
 }
 
 template <int FORMAT, bool GATHER, bool SUMS>
 cudaError_t prepare() {
     return cudaFuncSetAttribute(fp4_gemm_kernel<FORMAT, GATHER, SUMS>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<FORMAT>);
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
 }
 
 }  // namespace
@@ -683,7 +674,7 @@ cudaError_t prepare_fp4_gemm(int *pairs) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(Warps<true, true>::kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes<kNv>;
+    cfg.dynamicSmemBytes = kSmemBytes;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaOccupancyMaxActiveClusters(pairs, fp4_gemm_kernel<kNv, true, true>, &cfg);
