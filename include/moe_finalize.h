@@ -553,8 +553,9 @@ mf_status moe_grouped_gemv_int4(const void *x, int64_t x_rows, int64_t x_stride,
  *   scales           device, [rows] rows of k / 32 (MX) or k / 16 (NV) bytes,
  *                    scales_stride apart.
  *   k                a multiple of 32, 32 .. 2^20.
- *   Byte strides are multiples of 16, at least the row's bytes; x, quantized and
- *   scales 16-byte aligned.  Bytes behind a row's are neither read nor written.
+ *   Byte strides are multiples of 16, at least the row's bytes, scales' below 2^31;
+ *   x, quantized and scales 16-byte aligned.  Bytes behind a row's are neither read
+ *   nor written.
  *   Buffers may not overlap (MF_ERR_ALIGN).
  *
  * Errors: MF_ERR_INVALID (format), MF_ERR_UNSUPPORTED (k), MF_ERR_SHAPE,
@@ -601,8 +602,10 @@ mf_status moe_dequantize_fp4(const uint8_t *quantized, int64_t quantized_stride,
  *                    multiple of 8 elements, at least n.
  *   n                a multiple of 8, 8 .. 2^20.   num_experts  1 .. 1024.
  *   k                a multiple of 32, 32 .. 2^20.
- *   Byte strides are multiples of 16, at least the row's bytes; x, weight, their
- *   scales and output 16-byte aligned.  Bytes behind a row's are not read.
+ *   Byte strides are multiples of 16, at least the row's bytes, scales' below 2^31;
+ *   x, weight, their scales and output 16-byte aligned.  Scales are read in whole
+ *   16-byte pieces: the bytes behind a row's up to the next multiple of 16 belong to
+ *   the buffer (the last row's, too), and have no effect.
  *
  * Errors: those of moe_grouped_gemm, and MF_ERR_INVALID (format; no expert_offsets
  * with more than one expert).  Zero rows: MF_OK, nothing launched.

@@ -23,6 +23,11 @@ bool byte_stride_ok(int64_t stride, int64_t width) {
     return stride >= width && stride % 16 == 0 && stride < (int64_t{1} << 36);
 }
 
+// Scales' rows, in 32 bits, too.
+bool scale_stride_ok(int64_t stride, int64_t width) {
+    return byte_stride_ok(stride, width) && stride < (int64_t{1} << 31);
+}
+
 bool k_ok(int32_t k) { return k >= 32 && k <= mf::kMaxWidth && k % 32 == 0; }
 
 int64_t extent(int64_t rows, int64_t stride, int64_t width) {
@@ -34,7 +39,7 @@ mf_status check_rows(mf_fp4_format format, int64_t rows, int32_t k, mf_dtype dty
     if (!format_ok(format)) return MF_ERR_INVALID;
     if (!k_ok(k)) return MF_ERR_UNSUPPORTED;
     if (rows < 0 || rows > mf::kMaxRows || !mf::row_stride_ok(row_stride, k) ||
-        !byte_stride_ok(q_stride, k / 2) || !byte_stride_ok(s_stride, k / block_of(format)))
+        !byte_stride_ok(q_stride, k / 2) || !scale_stride_ok(s_stride, k / block_of(format)))
         return MF_ERR_SHAPE;
     // a thread for every 32 values, 128 to a block
     if ((rows * (k / 8) + 511) / 512 > 0x7fffffffLL) return MF_ERR_SHAPE;
@@ -163,9 +168,9 @@ mf_status moe_grouped_gemm_fp4(const uint8_t *x, int64_t x_rows, int64_t x_strid
         x_rows < (row_index ? (rows > 0) : rows))
         return MF_ERR_SHAPE;
     const int32_t groups = k / block_of(format);
-    if (!byte_stride_ok(x_stride, k / 2) || !byte_stride_ok(x_scales_stride, groups) ||
+    if (!byte_stride_ok(x_stride, k / 2) || !scale_stride_ok(x_scales_stride, groups) ||
         !byte_stride_ok(weight_row_stride, k / 2) ||
-        !byte_stride_ok(weight_scales_row_stride, groups) ||
+        !scale_stride_ok(weight_scales_row_stride, groups) ||
         !mf::row_stride_ok(output_stride, n))
         return MF_ERR_SHAPE;
     if (num_experts > 1 &&

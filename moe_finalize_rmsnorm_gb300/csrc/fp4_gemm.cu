@@ -54,25 +54,29 @@ struct Scales {
     static constexpr int kWords = kBytes / 4;
     static constexpr int kStepBytes = 3 * kWords * kBlockBytes;  // the columns', the rows'
     static constexpr int kColumns = 12 * kWords;              // of TMEM, of a step
-    static constexpr int kBuffers = FORMAT == kMx ? 4 : 2;    // steps held in TMEM
-    static_assert(kScaleColumn + kBuffers * kColumns <= kTmemColumns, "TMEM");
+    static_assert(kScaleColumn + 2 * kColumns <= kTmemColumns, "scales of two steps in TMEM");
 };
 
-// Warps: 0 block copies, 1 products, from 4 on the epilogue, then four for the scales,
-// then those that gather (with 2 and 3).
+// Warps: 0 block copies, 1 products, from 4 on eight for the epilogue, then eight for the
+// scales, then those that gather (with 2 and 3, one to a stage).
+constexpr int kEpilogueWarps = 8;
+constexpr int kFirstScale = 4 + kEpilogueWarps;
+constexpr int kFirstGather = kFirstScale + 8;
+
 template <bool SUMS, bool GATHER>
 struct Warps {
-    static constexpr int kEpilogue = 8;
-    static constexpr int kScale = 4 + kEpilogue;
-    static constexpr int kFirstGather = kScale + 4;
-    static constexpr int kShare = SUMS ? 1 : 2;  // gathering warps of a stage
-    static constexpr int kAll =
-        GATHER ? (SUMS ? 20 : kFirstGather + kShare * kStages - 2) : kFirstGather;
-    static constexpr int kThreads = 32 * kAll;
+    static constexpr int kThreads = 32 * (GATHER ? kFirstGather + kStages - 2 : kFirstGather);
+    // With moved sums the epilogue's warps take some of the others' registers
+    // (256 * 144 + 384 * 64 = the launch's 640 * 96; 256 * 128 + 512 * 56 = 768 * 80).
+    static constexpr int kMany = GATHER ? 128 : 144, kFew = GATHER ? 56 : 64;
+    static constexpr int kLaunched = GATHER ? 80 : 96;
+    static_assert(kThreads == (GATHER ? 768 : 640) &&
+                      256 * kMany + (kThreads - 256) * kFew <= kThreads * kLaunched,
+                  "register split");
 };
 
 struct Control {
-    int4 list[kStages * 24];     // rows by number, four a copy; a part for each gathering warp
+    int4 list[kStages * (kRowsMax / 8)];  // rows by number, four a copy, for each stage
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], scale_full[2],
         scale_empty[2];
     int4 listed[kListed];        // this pair's first tiles: expert, column, row, rows
@@ -153,30 +157,37 @@ struct Walk {
     }
 };
 
-// Instruction descriptor: E2M1 operands along K, FP32 accumulators, M 256; `id`: the first
-// byte of a scale's word.
+// Instruction descriptor: E2M1 operands along K, FP32 accumulators, M 256; the first two (or
+// four) bytes of a scale's word, with kSecond the other two.
 template <int FORMAT>
-__device__ __forceinline__ uint32_t fp4_desc(int n, uint32_t id) {
-    return (id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
-           (uint32_t{FORMAT == kMx} << 23) | (16u << 24) | (id << 29);
+__device__ __forceinline__ uint32_t fp4_desc(int n) {
+    return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (uint32_t{FORMAT == kMx} << 23) | (16u << 24);
 }
+constexpr uint32_t kSecond = (2u << 4) | (2u << 29);
 
+// (a, b: the lower halves of the operands' descriptors, `upper` what they share.)
 template <int FORMAT>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t scale_a, uint32_t scale_b, bool accumulate) {
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint32_t a, uint32_t b, uint32_t upper,
+                                        uint32_t idesc, uint32_t scale_a, uint32_t scale_b,
+                                        bool accumulate) {
     if constexpr (FORMAT == kMx)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-            "[%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"(uint32_t{accumulate})
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %7, 0;\n\t"
+            "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, [%5], "
+            "[%6], p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(upper), "r"(idesc), "r"(scale_a), "r"(scale_b),
+            "r"(uint32_t{accumulate})
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
-            "[%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"(uint32_t{accumulate})
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %7, 0;\n\t"
+            "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %4, "
+            "[%5], [%6], p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(upper), "r"(idesc), "r"(scale_a), "r"(scale_b),
+            "r"(uint32_t{accumulate})
             : "memory");
 }
 
@@ -189,9 +200,12 @@ __device__ __forceinline__ uint64_t block_desc(uint32_t block) {
 
 // Such a block to four TMEM columns, the same in each quarter of the lanes, in both CTAs;
 // in order with the products.
-__device__ __forceinline__ void scales_to_tmem(uint32_t addr, uint64_t block) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(addr), "l"(block)
-                 : "memory");
+__device__ __forceinline__ void scales_to_tmem(uint32_t addr, uint32_t block, uint32_t upper) {
+    asm volatile(
+        "{\n\t.reg .b64 b;\n\tmov.b64 b, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], b;\n\t}" ::"r"(addr),
+        "r"(block), "r"(upper)
+        : "memory");
 }
 
 // A whole warp's wait on a barrier that either CTA of the pair arrives on: all lanes go on,
@@ -205,7 +219,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
         : "=r"(there)
         : "r"(bar), "r"(parity)
         : "memory");
-    if (__all_sync(0xffffffffu, there)) return true;
+    if (__builtin_expect(__all_sync(0xffffffffu, there), 1)) return true;
     return __all_sync(0xffffffffu, mbar_wait_long<true>(bar, parity, limit_ns));
 }
 
@@ -253,7 +267,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, W::kEpilogue * 2);
+            mbar_init(acc_empty + 8 * i, kEpilogueWarps * 2);
             mbar_init(scale_full + 8 * i, 4 * 2);
             mbar_init(scale_empty + 8 * i, 1);
         }
@@ -279,18 +293,13 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
     tcgen05_fence_after();
     const uint32_t tmem = uniform(c.tmem);
 
-    // Registers: the warps that hold the moved sums take some of the others'
-    // (8 * 32 * 144 + 12 * 32 * 64 = the launch's 640 * 96).
-    constexpr bool kMoveRegisters = SUMS && GATHER;
-    static_assert(!kMoveRegisters || W::kThreads == 640, "register split");
-
     bool ok = true;
-    if (warp >= 4 && warp < W::kScale) {
-        if constexpr (kMoveRegisters) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    if (warp >= 4 && warp < kFirstScale) {
+        if constexpr (SUMS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::kMany));
         // Results: lane = output column, TMEM column = output row; eight warps, of which
         // two take the same 32 lanes and every other 32 rows.
         const int w = warp % 4, group = (warp - 4) / 4;
-        constexpr int kGroups = W::kEpilogue / 4;
+        constexpr int kGroups = kEpilogueWarps / 4;
         const uint32_t done_at = map_to_cta(acc_empty, 0);
         const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
         uint32_t acc_n = 0;  // accumulators taken so far
@@ -360,7 +369,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             }
         }
     } else {
-        if constexpr (kMoveRegisters) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if constexpr (SUMS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kFew));
         const uint32_t full_at = map_to_cta(full, 0);
         if (warp == 0) {
             // Copies of whole blocks, and each stage's byte count.
@@ -409,113 +418,112 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                 }
         } else if (warp == 1 && rank == 0) {
             // Products.  A step takes the tensor cores some 400 cycles, and this warp has to
-            // issue its 10 to 16 instructions in less: one barrier a step, places and parities
-            // kept by counting.
-            uint32_t stage = 0, phase = 0, buffer = 0, acc_n = 0, group_n = 0;
+            // issue its 10 to 16 instructions in less, so the loop is kept short: places are kept
+            // by counting, and the last step multiplies its zeros too.
             const uint64_t operands = smem_desc(base, 16, 1024), blocks = block_desc(groups);
-            const int last_parts = (a.k - (steps - 1) * kStep + 63) / 64;
-            int next_n = walk.more() ? walk.take().n : 0;
-            while (ok && next_n > 0) {
-                const int n = next_n;
-                const uint32_t idesc = fp4_desc<FORMAT>(n, 0);
-                const uint32_t second = fp4_desc<FORMAT>(n, 2);  // the word's other two scales
+            const uint32_t operands_upper = static_cast<uint32_t>(operands >> 32);
+            const uint32_t blocks_upper = static_cast<uint32_t>(blocks >> 32);
+            constexpr int kRowsFrom = Sc::kWords;  // the rows' first block
+            uint32_t stage = 0, phase = 0, acc_n = 0, group_n = 0, scales = tmem + kScaleColumn;
+            const uint32_t turn = scales ^ (scales + Sc::kColumns);
+            const auto products = [&](const int n) {
+                const uint32_t idesc = fp4_desc<FORMAT>(n);
                 int in_segment = 0, in_group = 0;
-                for (int s = 0; s < steps; ++s) {
+                uint32_t from = 0;
+#pragma unroll 1
+                for (int left = steps; left > 0; --left) {
                     if (in_group == 0) {
-                        ok = warp_wait(scale_full + 8 * (group_n & 1), group_n >> 1 & 1,
-                                       a.timeout_ns);
-                        if (!ok) break;
+                        if (!warp_wait(scale_full + 8 * (group_n & 1), group_n >> 1 & 1,
+                                       a.timeout_ns))
+                            return false;
+                        from = static_cast<uint32_t>(blocks) + (group_n & 1) * (kGroupBytes / 16);
                     }
-                    if (in_segment == 0) {
-                        ok = warp_wait(acc_empty + 8 * (acc_n & 1), (acc_n >> 1 & 1) ^ 1,
-                                       a.timeout_ns);
-                        if (!ok) break;
-                    }
-                    ok = warp_wait(full + 8 * stage, phase, a.timeout_ns);
-                    if (!ok) break;
+                    if (in_segment == 0 && !warp_wait(acc_empty + 8 * (acc_n & 1),
+                                                      (acc_n >> 1 & 1) ^ 1, a.timeout_ns))
+                        return false;
+                    if (!warp_wait(full + 8 * stage, phase, a.timeout_ns)) return false;
                     tcgen05_fence_after();
-                    const bool last = s + 1 == steps;
-                    const bool end = last || (SUMS && in_segment == kSegment - 1);
-                    const bool group_end = last || in_group == Sc::kSteps - 1;
+                    const uint32_t bar = empty + 8 * stage;
+                    const uint32_t da = static_cast<uint32_t>(operands) + stage * (kStageBytes / 16);
+                    const uint32_t db = da + kABytes / 16;
+                    const uint32_t dst = tmem + (acc_n & 1) * kRowsMax;
+                    ++in_group;
+                    ++in_segment;
+                    const bool group_end = left == 1 || in_group == Sc::kSteps;
+                    const bool end = left == 1 || (SUMS && in_segment == kSegment);
                     if (elect_one()) {
-                        const uint64_t da = operands + stage * (kStageBytes / 16);
-                        const uint64_t db = da + kABytes / 16;
-                        const int piece = FORMAT == kMx ? in_group / 2 : in_group;
-                        const uint64_t sc = blocks + (group_n & 1) * (kGroupBytes / 16) +
-                                            piece * (kPieceBytes / 16) +
-                                            (FORMAT == kMx ? in_group % 2 : 0) *
-                                                (Sc::kStepBytes / 16);
-                        const uint32_t dst = tmem + (acc_n & 1) * kRowsMax;
-                        const uint32_t scales = tmem + kScaleColumn + buffer * Sc::kColumns;
-                        const int parts = last ? last_parts : 4;
 #pragma unroll
                         for (int i = 0; i < 3 * Sc::kWords; ++i)
-                            if (i < Sc::kWords || (i - Sc::kWords) % 2 == 0 || n > 128)
-                                scales_to_tmem(scales + 4 * i, sc + i * (kBlockBytes / 16));
+                            scales_to_tmem(scales + 4 * i, from + i * (kBlockBytes / 16),
+                                           blocks_upper);
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
                             // 64 summed values: 32 bytes of a row, a word of its scales or half
-                            const int word = FORMAT == kMx ? p / 2 : p;
-                            if (p < parts)
-                                mma_fp4<FORMAT>(dst, da + p * 2, db + p * 2,
-                                                FORMAT == kMx && p % 2 ? second : idesc,
-                                                scales + 4 * word,
-                                                scales + 4 * Sc::kWords + 8 * word,
-                                                p > 0 || in_segment > 0);
+                            const int w = FORMAT == kMx ? p / 2 : p;
+                            mma_fp4<FORMAT>(dst, da + p * 2, db + p * 2, operands_upper,
+                                            FORMAT == kMx && p % 2 ? idesc | kSecond : idesc,
+                                            scales + 4 * w, scales + 4 * (kRowsFrom + 2 * w),
+                                            p > 0 || in_segment > 1);
                         }
-                        mma_commit<2>(empty + 8 * stage);
+                        mma_commit<2>(bar);
                         if (group_end) mma_commit<2>(scale_empty + 8 * (group_n & 1));
                         if (end) mma_commit<2>(acc_full + 8 * (acc_n & 1));
                     }
-                    __syncwarp();
-                    in_segment = end ? 0 : in_segment + 1;
-                    in_group = group_end ? 0 : in_group + 1;
-                    acc_n += end;
-                    group_n += group_end;
+                    from += Sc::kStepBytes / 16;
+                    scales ^= turn;
+                    if (group_end) {
+                        in_group = 0;
+                        ++group_n;
+                    }
+                    if (end) {
+                        in_segment = 0;
+                        ++acc_n;
+                    }
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1;
                     }
-                    buffer = (buffer + 1) % Sc::kBuffers;
-                    // the next tile is found while this one's products run
-                    if (s == 0) next_n = walk.more() ? walk.take().n : 0;
                 }
-            }
-        } else if (warp >= W::kScale && warp < W::kFirstGather) {
-            // Scales.  A thread takes 16 bytes (a piece) of one row in 32 and of those every 32
-            // behind it: four of the tile's columns, and up to six of its rows, of which four
-            // rows' words make a lane of a block.  They are read a group ahead.  Eight lanes
-            // have eight rows' same piece: 128 bytes of a block.
+                return true;
+            };
+            while (ok && walk.more()) ok = products(walk.take().n);
+            __syncwarp();
+        } else if (warp >= kFirstScale && warp < kFirstGather) {
+            // Scales.  Two teams of four warps take every other group (a read takes a group's time
+            // and more).  A thread takes 16 bytes (a piece) of one row in 32 and of those every
+            // 32 behind it: four of the tile's columns, and up to six of its rows, of which four
+            // rows' words make a lane of a block.  Eight lanes have eight rows' same piece: 128
+            // bytes of a block.
+            const int team = (warp - kFirstScale) / 4;
             const int row_bytes = a.k / (FORMAT == kMx ? 32 : 16);
             const uint32_t scale_full_at = map_to_cta(scale_full, 0);
             const int groups_of_tile = divide_up(steps, Sc::kSteps);
             const int line = warp % 4 * 8 + lane % 8, piece = lane / 8;
-            const uint8_t *w_from = nullptr;  // this thread's first row of the columns
-            int w_rows = 0;                   // rows of them that exist
-            int x_rows[kRowsMax / 32];        // -1: none (zeros)
+            const uint32_t w_ld = static_cast<uint32_t>(a.ws_ld);  // (below 2^31)
+            const uint32_t x_ld = static_cast<uint32_t>(a.xs_ld);
+            const int all = walk.count * groups_of_tile;  // (a tile's columns bound both)
+            const uint8_t *w_from = nullptr;  // the expert's scales
+            int w_row = 0;                    // this thread's first column
+            int x_rows[kRowsMax / 32];        // its rows of x, -1: none (zeros)
             uint4 q[12] = {};                 // (the last 64 rows of the blocks do not exist)
-            // 16 bytes, zeros behind the first `valid`
-            auto load = [&](const uint8_t *p, int valid) {
-                if (valid >= 16) return __ldg(reinterpret_cast<const uint4 *>(p));
-                uint64_t lo = 0, hi = 0;
-                for (int i = 0; i < valid; ++i) {
-                    const uint64_t byte = __ldg(p + i);
-                    if (i < 8)
-                        lo |= byte << (8 * i);
-                    else
-                        hi |= byte << (8 * i - 64);
-                }
-                return make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
-                                  static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32));
+            const auto read_16 = [](const uint8_t *base, uint32_t row, uint32_t ld, bool read) {
+                const uint8_t *p = base + uint64_t{row} * ld;
+                uint4 v;
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                    "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+                    "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                    : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+                    : "l"(p), "r"(uint32_t{read}));
+                return v;
             };
-            int next_g = 0;  // the group to read next, of the tile at hand
-            auto read_group = [&]() {
-                if (next_g == 0) {
-                    if (!walk.more()) return;
+            auto read_group = [&](int g) {
+                const int tile = g / groups_of_tile;
+                if (tile >= walk.i) {  // the tile was not taken yet
+                    walk.i = tile;
                     const Tile d = walk.take();
-                    const int n = d.m0 + static_cast<int>(rank) * 128 + line;
-                    w_from = a.w_scales + d.expert * a.ws_expert + n * a.ws_ld;
-                    w_rows = (a.n - n + 31) / 32;
+                    w_row = d.m0 + static_cast<int>(rank) * 128 + line;
+                    w_from = a.w_scales + d.expert * a.ws_expert;
 #pragma unroll
                     for (int u = 0; u < kRowsMax / 32; ++u) {
                         const int i = 32 * u + line;
@@ -528,27 +536,38 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                         x_rows[u] = row;
                     }
                 }
-                const int from = next_g * 64 + piece * 16, valid = row_bytes - from;
+                const int from = (g - tile * groups_of_tile) * 64 + piece * 16;
+                const int valid = row_bytes - from;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    q[u] = make_uint4(0, 0, 0, 0);
-                    if (valid > 0 && u < w_rows) q[u] = load(w_from + 32 * u * a.ws_ld + from, valid);
-                }
+                for (int u = 0; u < 4; ++u)
+                    q[u] = read_16(w_from + from, w_row + 32 * u, w_ld,
+                                   valid > 0 && w_row + 32 * u < a.n);
 #pragma unroll
-                for (int u = 0; u < kRowsMax / 32; ++u) {
-                    q[4 + u] = make_uint4(0, 0, 0, 0);
-                    if (valid > 0 && x_rows[u] >= 0)
-                        q[4 + u] = load(a.x_scales + x_rows[u] * a.xs_ld + from, valid);
+                for (int u = 0; u < kRowsMax / 32; ++u)
+                    q[4 + u] = read_16(a.x_scales + from, x_rows[u], x_ld,
+                                       valid > 0 && x_rows[u] >= 0);
+                if (valid > 0 && valid < 16) {  // what lies behind a row's bytes counts as zeros
+                    uint32_t keep[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int bytes = min(max(valid - 4 * j, 0), 4);
+                        keep[j] = bytes == 4 ? ~0u : (1u << (8 * bytes)) - 1;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4 + kRowsMax / 32; ++u) {
+                        q[u].x &= keep[0];
+                        q[u].y &= keep[1];
+                        q[u].z &= keep[2];
+                        q[u].w &= keep[3];
+                    }
                 }
-                if (++next_g == groups_of_tile) next_g = 0;
             };
-            const int all = walk.count * groups_of_tile;  // (a tile's columns bound both)
-            read_group();
-            int g = 0;
-            for (; g < all; ++g) {
-                ok = warp_wait(scale_empty + 8 * (g & 1), (g >> 1 & 1) ^ 1, a.timeout_ns);
+            if (team < all) read_group(team);
+            const uint32_t to = groups + team * kGroupBytes + piece * kPieceBytes + line * 16;
+            uint32_t n = 0;  // groups of this team so far
+            for (int g = team; g < all; g += 2, ++n) {
+                ok = warp_wait(scale_empty + 8 * team, (n & 1) ^ 1, a.timeout_ns);
                 if (!ok) break;
-                const uint32_t to = groups + (g & 1) * kGroupBytes + piece * kPieceBytes + line * 16;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {  // words of the 16 bytes
                     const int step = j / Sc::kWords, word = j % Sc::kWords;
@@ -568,38 +587,33 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                 // cluster scope takes 0.9 us).
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(scale_full_at + 8 * (g & 1));
-                read_group();
+                if (lane == 0) mbar_arrive_cluster(scale_full_at + 8 * team);
+                if (g + 2 < all) read_group(g + 2);
             }
-            // the last groups' products are done, before this CTA may leave
-            for (int i = max(g - 2, 0); ok && i < g; ++i)
-                ok = warp_wait(scale_empty + 8 * (i & 1), i >> 1 & 1, a.timeout_ns);
-        } else if (GATHER && (warp == 2 || warp == 3 || warp >= W::kFirstGather)) {
-            // Rows by number, four a copy (-1, no such row, arrives as zeros), by one or two
-            // warps for every stage.  The numbers go through shared memory, so that the elected
-            // lane reads them with uniform addresses.
-            const int index = warp < 4 ? warp - 2 : warp - W::kFirstGather + 2;
-            const uint32_t stage = index % kStages;
-            const int sub = index / kStages;
+            // the last group's copies are done, before this CTA may leave
+            if (ok && n > 0) ok = warp_wait(scale_empty + 8 * team, (n & 1) ^ 1, a.timeout_ns);
+        } else if (GATHER && (warp == 2 || warp == 3 || warp >= kFirstGather)) {
+            // Rows by number, four a copy (-1, no such row, arrives as zeros), a warp to a stage.
+            // The numbers go through shared memory, so that the elected lane reads them with
+            // uniform addresses.
+            const uint32_t stage = warp < 4 ? warp - 2 : warp - kFirstGather + 2;
             const uint32_t bar = full_at + 8 * stage;
             const uint32_t sb = base + stage * kStageBytes + kABytes;
-            uint32_t it = sub < W::kShare ? stage : ~0u;  // this warp's next step, over the tiles
-            int4 *list = c.list + (sub < W::kShare ? index : 0) * (24 / W::kShare);
-            uint32_t done = 0;                            // steps of the tiles before
-            while (ok && it != ~0u && walk.more()) {
+            int4 *list = c.list + stage * (kRowsMax / 8);
+            uint32_t it = stage;  // this warp's next step, over the tiles
+            uint32_t done = 0;    // steps of the tiles before
+            while (ok && walk.more()) {
                 const Tile d = walk.take();
                 const int half = d.n / 2, b0 = d.row0 + rank * half;
-                const int row_end = d.row0 + d.nrows;
-                const int quads = (half / 4 - sub + W::kShare - 1) / W::kShare;
+                const int row_end = d.row0 + d.nrows, quads = half / 4;
                 auto x_row = [&](int i) {
                     const int v = i < row_end ? __ldg(a.row_index + i) : -1;
                     return v >= 0 && v < a.x_rows ? v : -1;
                 };
                 if (it < done + steps) {
-                    // every kShare-th four rows of the CTA's half (24 fours at most)
-                    for (int q = lane; q < quads; q += 32) {
-                        const int i = b0 + 4 * (W::kShare * q + sub);
-                        list[q] = make_int4(x_row(i), x_row(i + 1), x_row(i + 2), x_row(i + 3));
+                    if (lane < quads) {  // of the CTA's half: 24 fours at most
+                        const int i = b0 + 4 * lane;
+                        list[lane] = make_int4(x_row(i), x_row(i + 1), x_row(i + 2), x_row(i + 3));
                     }
                     __syncwarp();
                 }
@@ -618,8 +632,8 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
 #pragma unroll
                             for (int q = 0; q < kBatch; ++q)
                                 if (q0 + q < quads)
-                                    tma_gather4<true>(sb + (W::kShare * (q0 + q) + sub) * 512,
-                                                      &maps.b4, x, rows[q], bar);
+                                    tma_gather4<true>(sb + (q0 + q) * 512, &maps.b4, x, rows[q],
+                                                      bar);
                         }
                     }
                     __syncwarp();

@@ -57,6 +57,17 @@ def _packed(q: torch.Tensor, scales: torch.Tensor, name: str, dims: int) -> tupl
     return f[0], k
 
 
+def _whole_pieces(scales: torch.Tensor, name: str) -> None:
+    """The product reads scales in 16-byte pieces: the last row's has to lie in its memory."""
+    if scales.numel():
+        end = scales.storage_offset() + sum((n - 1) * st for n, st in
+                                            zip(scales.shape, scales.stride()))
+        end += 1 + -scales.shape[-1] % 16
+        if end > scales.untyped_storage().nbytes():
+            raise ValueError(f"{name}'s last row must be followed by bytes up to a multiple of 16 "
+                             "(as moe_fp4_empty allocates)")
+
+
 def _row_bytes(t: torch.Tensor) -> int:
     """Bytes between the rows of packed values or scales; one row has none to keep."""
     if t.shape[-2] > 1:
@@ -147,6 +158,8 @@ def moe_grouped_gemm_fp4(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.
     else:
         _index(expert_offsets, "expert_offsets", (E + 1,))
     _row_index(row_index, rows, x.shape[0])
+    _whole_pieces(x_scales, "x")
+    _whole_pieces(weight_scales, "weight")
     _req(factor is None or (factor.dtype == torch.float32 and factor.shape == (E,) and
                             factor.is_contiguous()), "factor must be contiguous FP32 [experts]")
     dev = output.device

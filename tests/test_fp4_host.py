@@ -54,7 +54,7 @@ def test_strides(lib):
     for bad in (0, 16, 40, -32, 2 ** 36):
         assert quantize(lib, qs=bad) == SHAPE and dequantize(lib, qs=bad) == SHAPE, bad
         assert gemm(lib, xs=bad) == SHAPE and gemm(lib, ws=bad) == SHAPE, bad
-    for bad in (0, 8, 24, -16, 2 ** 36):
+    for bad in (0, 8, 24, -16, 2 ** 31, 2 ** 36):
         assert quantize(lib, ss=bad) == SHAPE and dequantize(lib, ss=bad) == SHAPE, bad
         assert gemm(lib, scs=bad) == SHAPE and gemm(lib, wscs=bad) == SHAPE, bad
     for bad in (56, 68, 0):
@@ -137,6 +137,11 @@ def off(E):
                                     row_index=meta(5, dtype=I32)),
     lambda: mf.moe_grouped_gemm_fp4(*pair(0), *pair(2, 32), off(2), meta(6, 32),
                                     row_index=meta(6, dtype=I32)),
+    # a last row of scales at the end of its memory
+    lambda: mf.moe_grouped_gemm_fp4(*pair(6), pair(1, 1)[0], meta(1, 1, 2, dtype=U8).view(MX),
+                                    off(1), meta(6, 1)),
+    lambda: mf.moe_grouped_gemm_fp4(pair(1)[0], meta(1, 2, dtype=U8).view(MX), *pair(1, 32), off(1),
+                                    meta(1, 32)),
     # right but for the device
     lambda: mf.moe_quantize_fp4(meta(4, 64), *pair(4)),
     lambda: mf.moe_dequantize_fp4(*pair(4), meta(4, 64)),
