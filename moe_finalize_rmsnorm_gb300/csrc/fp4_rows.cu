@@ -1,7 +1,7 @@
 // The 4-bit floating point product for few rows per expert (decode): bound by the
 // weights' bytes.
 //
-// A warp takes 32 output columns and up to 8 NT rows, streams 256 summed values of its
+// A warp takes 32 output columns and up to 8 rows, streams 256 summed values of its
 // columns a stage (128 bytes a column, one tensor-map copy) with their scales and the
 // rows' through its own ring in shared memory, and multiplies in mma.m16n8k16, columns
 // along M, on FP16: E2M1 values are exact there.  A lane takes the eight values of a
@@ -26,12 +26,12 @@ namespace {
 constexpr int kCols = 32;   // columns of a warp
 constexpr int kSpan = 256;  // summed values of a stage
 
-template <int FORMAT, int NT>
+template <int FORMAT>
 struct Fp4Shape {
-    static constexpr int kWarps = NT == 1 ? 10 : 8;
+    static constexpr int kWarps = 10;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kStages = 3;
-    static constexpr int kRows = 8 * NT;                        // of one pass over the weights
+    static constexpr int kRows = 8;                             // of one pass over the weights
     static constexpr int kScales = FORMAT == kMx ? 8 : 16;      // of a column and stage
     static constexpr int kColBytes = kCols * kSpan / 2;         // a stage's columns
     static constexpr int kWsAt = kRows * kSpan / 2;             // behind the rows: scales
@@ -97,9 +97,9 @@ __device__ __forceinline__ uint32_t two_e4m3(uint32_t bytes) {
     return r;
 }
 
-template <int FORMAT, int NT>
+template <int FORMAT>
 struct Fp4Rows {
-    using S = Fp4Shape<FORMAT, NT>;
+    using S = Fp4Shape<FORMAT>;
     const Fp4GemmArgs &a;
     const CUtensorMap &map;
     typename S::Control &c;
@@ -148,7 +148,7 @@ struct Fp4Rows {
             __syncwarp();
             const int byte0 = p.stage * (kSpan / 2), left = a.k / 2 - byte0;
 #pragma unroll
-            for (int i = 0; i < 2 * NT; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 const int r = 4 * i + lane / 8, chunk = lane % 8;
                 const int from = __shfl_sync(0xffffffffu, row, r);
                 const int valid = from < 0 ? 0 : min(max(left - 16 * chunk, 0), 16);
@@ -224,13 +224,13 @@ struct Fp4Rows {
                                                 4 * (((line >> 2) & 1) ^ half));
     }
 
-    // One column block with up to 8 NT rows.  A copy that does not arrive within `limit`
+    // One column block with up to 8 rows.  A copy that does not arrive within `limit`
     // sets the status and the limit to zero: the warp goes on (the others wait for it at
     // the block's barrier), with results of no meaning.
     __device__ void item(Cursor &now, Cursor &ahead, int &row, uint32_t &it,
                          uint64_t &limit) const {
         const Cursor d = now;
-        float acc[2][NT][4] = {};
+        float acc[2][4] = {};
         while (now.item == d.item) {
             const uint32_t slot = it % S::kStages;
             cp_async_wait<S::kStages - 2>();
@@ -247,30 +247,28 @@ struct Fp4Rows {
             for (int half = 0; half < 2; ++half) {
                 // MX: columns g + 8 i, and the rows 2 t and 2 t + 1 of the results; NV: the
                 // columns and the row g that this lane feeds
-                uint4 sw[4], sx[NT][2];
+                uint4 sw[4], sx[2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sw[i] = scales(g + 8 * i, half);
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        sx[i][j] = scales(kCols + 8 * i + (FORMAT == kMx ? 2 * t + j : g), half);
+                for (int j = 0; j < 2; ++j)
+                    sx[j] = scales(kCols + (FORMAT == kMx ? 2 * t + j : g), half);
                 const auto word = [](const uint4 &v, int i) {
                     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
                 };
-                float sum[2][NT][4];
+                float sum[2][4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     const uint32_t at = g * 128 + (((4 * half + b) ^ g) << 4) + 4 * t;
-                    uint32_t wv[4][4], xv[NT][4];
+                    uint32_t wv[4][4], xv[4];
                     const uint32_t pick = t < 2 ? 0x1010u : 0x3232u;  // NV: this lane's block
 #pragma unroll
-                    for (int i = 0; i < 4 + NT; ++i) {
-                        uint32_t(&v)[4] = i < 4 ? wv[i < 4 ? i : 0] : xv[i < 4 ? 0 : i - 4];
-                        from_e2m1(lds<uint32_t>(at + (i < 4 ? w + 1024 * i : x + 1024 * (i - 4))), v);
+                    for (int i = 0; i < 5; ++i) {
+                        uint32_t(&v)[4] = i < 4 ? wv[i < 4 ? i : 0] : xv;
+                        from_e2m1(lds<uint32_t>(at + (i < 4 ? w + 1024 * i : x)), v);
                         if (FORMAT == kNv) {
                             const uint32_t s = __byte_perm(
-                                word(i < 4 ? sw[i < 4 ? i : 0] : sx[i < 4 ? 0 : i - 4][0], b), 0, pick);
+                                word(i < 4 ? sw[i < 4 ? i : 0] : sx[0], b), 0, pick);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) v[j] = hmul2(v[j], s);
                         }
@@ -281,22 +279,19 @@ struct Fp4Rows {
                                                 wv[2 * m + 1][1]};
                         const uint32_t a1[4] = {wv[2 * m][2], wv[2 * m + 1][2], wv[2 * m][3],
                                                 wv[2 * m + 1][3]};
+                        if (FORMAT == kMx || b % 2 == 0)
+                            mma_f16_first(sum[m], a0, xv[0], xv[1]);
+                        else
+                            mma_f16(sum[m], a0, xv[0], xv[1]);
+                        mma_f16(sum[m], a1, xv[2], xv[3]);
 #pragma unroll
-                        for (int i = 0; i < NT; ++i) {
-                            if (FORMAT == kMx || b % 2 == 0)
-                                mma_f16_first(sum[m][i], a0, xv[i][0], xv[i][1]);
-                            else
-                                mma_f16(sum[m][i], a0, xv[i][0], xv[i][1]);
-                            mma_f16(sum[m][i], a1, xv[i][2], xv[i][3]);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                if (FORMAT == kMx)
-                                    acc[m][i][j] = fmaf(
-                                        sum[m][i][j] * __uint_as_float(word(sw[2 * m + j / 2], b)),
-                                        __uint_as_float(word(sx[i][j % 2], b)), acc[m][i][j]);
-                                else if (b % 2 == 1)
-                                    acc[m][i][j] += sum[m][i][j];
-                            }
+                        for (int j = 0; j < 4; ++j) {
+                            if (FORMAT == kMx)
+                                acc[m][j] =
+                                    fmaf(sum[m][j] * __uint_as_float(word(sw[2 * m + j / 2], b)),
+                                         __uint_as_float(word(sx[j % 2], b)), acc[m][j]);
+                            else if (b % 2 == 1)
+                                acc[m][j] += sum[m][j];
                         }
                     }
                 }
@@ -305,21 +300,18 @@ struct Fp4Rows {
             __syncwarp();
             ++it;
         }
-        // acc[m][i][j]: n = 16 m + g + 8 (j / 2), row = 8 i + 2 t + j % 2
+        // acc[m][j]: n = 16 m + g + 8 (j / 2), row = 2 t + j % 2
         float *mine = c.sums[warp];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int n = 16 * m + g + 8 * (j / 2);
-                    const int r = 8 * i + 2 * t + j % 2;
-                    if (share > 1)
-                        mine[r * kCols + n] = acc[m][i][j];
-                    else if (r < d.rows && d.n0 + n < a.n)
-                        store(d, r, n, acc[m][i][j]);
-                }
+            for (int j = 0; j < 4; ++j) {
+                const int n = 16 * m + g + 8 * (j / 2), r = 2 * t + j % 2;
+                if (share > 1)
+                    mine[r * kCols + n] = acc[m][j];
+                else if (r < d.rows && d.n0 + n < a.n)
+                    store(d, r, n, acc[m][j]);
+            }
         if (share == 1) return;
         meet();
         if (d.n0 + lane < a.n)
@@ -337,10 +329,10 @@ struct Fp4Rows {
     }
 };
 
-template <int FORMAT, int NT>
-__global__ void __launch_bounds__(Fp4Shape<FORMAT, NT>::kThreads, 1)
+template <int FORMAT>
+__global__ void __launch_bounds__(Fp4Shape<FORMAT>::kThreads, 1)
     fp4_rows_kernel(const __grid_constant__ CUtensorMap map, const Fp4GemmArgs a, const int share) {
-    using S = Fp4Shape<FORMAT, NT>;
+    using S = Fp4Shape<FORMAT>;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + (((smem_u32(raw) + 1023u) & ~1023u) - smem_u32(raw));
     auto &c = *reinterpret_cast<typename S::Control *>(smem + S::kWarps * S::kStages * S::kColBytes);
@@ -355,7 +347,7 @@ __global__ void __launch_bounds__(Fp4Shape<FORMAT, NT>::kThreads, 1)
     const int block = warp / share;
     const unsigned col_blocks = (a.n + kCols - 1) / kCols;
     const int at_once = S::kWarps / share, items = total * static_cast<int>(col_blocks);
-    const Fp4Rows<FORMAT, NT> k{a,
+    const Fp4Rows<FORMAT> k{a,
                                 map,
                                 c,
                                 warp,
@@ -388,9 +380,9 @@ __global__ void __launch_bounds__(Fp4Shape<FORMAT, NT>::kThreads, 1)
                                  a.timeout_ns);
 }
 
-template <int FORMAT, int NT>
+template <int FORMAT>
 cudaError_t launch(const Fp4GemmArgs &a, cudaStream_t s) {
-    using S = Fp4Shape<FORMAT, NT>;
+    using S = Fp4Shape<FORMAT>;
     using u64 = cuuint64_t;
     CUtensorMap map;
     if (!encode_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, 3,
@@ -403,33 +395,29 @@ cudaError_t launch(const Fp4GemmArgs &a, cudaStream_t s) {
                            (a.rows / S::kRows + min(int64_t{a.num_experts}, a.rows));
     if (blocks > INT32_MAX / 2) return cudaErrorInvalidValue;  // they are counted in 32 bits
     const int share = warps_of_block(blocks, (a.k + kSpan - 1) / kSpan, S::kWarps, a.num_sms);
-    return launch_ex(fp4_rows_kernel<FORMAT, NT>,
+    return launch_ex(fp4_rows_kernel<FORMAT>,
                      dim3(static_cast<unsigned>(min(blocks, int64_t{a.num_sms}))),
                      dim3(S::kThreads), S::kSmem, s, 1, a.programmatic, map, a, share);
 }
 
-template <int FORMAT, int NT>
+template <int FORMAT>
 cudaError_t prepare() {
-    return cudaFuncSetAttribute(fp4_rows_kernel<FORMAT, NT>,
+    return cudaFuncSetAttribute(fp4_rows_kernel<FORMAT>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Fp4Shape<FORMAT, NT>::kSmem);
+                                Fp4Shape<FORMAT>::kSmem);
 }
 
 }  // namespace
 
 cudaError_t prepare_fp4_rows() {
     cudaError_t e = find_encoder();
-    if (e == cudaSuccess) e = prepare<kMx, 1>();
-    if (e == cudaSuccess) e = prepare<kMx, 2>();
-    if (e == cudaSuccess) e = prepare<kNv, 1>();
-    if (e == cudaSuccess) e = prepare<kNv, 2>();
+    if (e == cudaSuccess) e = prepare<kMx>();
+    if (e == cudaSuccess) e = prepare<kNv>();
     return e;
 }
 
 cudaError_t launch_fp4_rows(const Fp4GemmArgs &a, cudaStream_t s) {
-    const bool few = a.rows <= 8 || a.rows <= 2 * int64_t{a.num_experts};
-    if (a.format == kMx) return few ? launch<kMx, 1>(a, s) : launch<kMx, 2>(a, s);
-    return few ? launch<kNv, 1>(a, s) : launch<kNv, 2>(a, s);
+    return a.format == kMx ? launch<kMx>(a, s) : launch<kNv>(a, s);
 }
 
 }  // namespace mf

@@ -250,7 +250,8 @@ def check(s, out):
 SIZES = [([1], 8, 32), ([1, 0, 2], 16, 96), ([5, 1, 0, 9], 264, 512), ([3] * 8, 520, 2880),
          ([1] * 8, 4096, 4096), ([17, 40, 0, 3], 136, 1056), ([70, 1, 129], 1032, 288),
          ([256, 255, 257, 0, 1], 256, 544), ([193, 64, 32], 2056, 1024), ([600], 392, 768),
-         ([0, 0], 64, 64), ([33] * 5, 128, 8192), ([300, 20], 120, 320), ([1000, 24], 48, 1248)]
+         ([0, 0], 64, 64), ([33] * 5, 128, 8192), ([300, 20], 120, 320), ([1000, 24], 48, 1248),
+         ([12, 0, 1] + [0] * 13, 72, 352), ([1] * 40, 64, 128), ([513, 225], 264, 1120)]
 
 
 @pytest.mark.parametrize("sizes,n,k", SIZES)
