@@ -5,18 +5,21 @@
 //
 // computed transposed, as the BF16 products are: a tile's M is 256 output columns over a
 // pair of SMs, each holding half of either operand, and its N an expert's rows, any
-// multiple of 32 up to 192.  A persistent pair per two SMs walks the tiles: a warp
-// copies blocks (TMA, 128-byte swizzle, 256 summed values a step), a warp issues the
-// products into one of two accumulators in TMEM, eight warps move the other accumulator
-// out, and where rows are gathered, further warps copy them by number.
+// multiple of 32 up to 256 (FP32 results 192).  A persistent pair per two SMs walks the
+// tiles: a warp copies blocks (TMA, 128-byte swizzle, 256 summed values a step), a warp
+// issues the products into one of two accumulators in TMEM, eight warps move the other
+// accumulator out, and where rows are gathered, further warps copy them by number.
 //
 // The scales lie in rows beside the values' rows, and the products read them from TMEM:
-// lane l, column c the four bytes of row 32 c + l.  Four warps read 64 bytes a row (a
-// group: four or eight steps; four lanes to a row, the rows 32 apart in one thread), write
-// them to shared memory as blocks of 32 lanes by 16 bytes, and the warp that issues the
-// products copies a step's blocks into TMEM before it (tcgen05.cp, which runs in order with
-// them).  The 128 columns behind the accumulators hold them: that is why a tile ends at 192
-// rows.
+// lane l, column c the four bytes of row 32 c + l.  Two teams of four warps read 64 bytes a
+// row (a group: four or eight steps; four lanes to a row, the rows 32 apart in one thread),
+// write them to shared memory as blocks of 32 lanes by 16 bytes, and the warp that issues
+// the products copies a step's blocks into TMEM before it (tcgen05.cp, which runs in order
+// with them).
+//
+// TMEM has 512 columns, and two steps' scales take 96 (E4M3) or 48 of them.  So with 256
+// rows the two accumulators overlap: by 96 or 48 columns, which the epilogue moves out
+// first, and says so, before the rest.
 #include "experts.cuh"
 #include "experts.h"
 #include "fp4.cuh"
@@ -25,15 +28,11 @@
 namespace mf {
 namespace {
 
-constexpr int kRowsMax = 192;             // N of a tile
 constexpr int kStep = 256;                // summed values per stage: 128 bytes
 constexpr int kStepBytes = kStep / 2;
 constexpr int kABytes = 128 * kStepBytes;  // A of one CTA and stage
-constexpr int kStageBytes = kABytes + kRowsMax / 2 * kStepBytes;
-constexpr int kStages = 6;
 constexpr int kBlockBytes = 512;          // of scales: 32 lanes by 16 bytes, four TMEM columns
-constexpr int kTmemColumns = 512;         // two accumulators of 192, and the scales
-constexpr int kScaleColumn = 2 * kRowsMax;
+constexpr int kTmemColumns = 512;
 constexpr int kScanThreads = 256;         // threads that scan the experts
 constexpr int kListed = 128;              // tiles of a pair that are found at the start
 // Scales of a group, 64 bytes a row: four pieces of 16 bytes a row (one step's, or two), as
@@ -54,7 +53,24 @@ struct Scales {
     static constexpr int kWords = kBytes / 4;
     static constexpr int kStepBytes = 3 * kWords * kBlockBytes;  // the columns', the rows'
     static constexpr int kColumns = 12 * kWords;              // of TMEM, of a step
-    static_assert(kScaleColumn + 2 * kColumns <= kTmemColumns, "scales of two steps in TMEM");
+    static constexpr int kColumn = kTmemColumns - 2 * kColumns;  // two steps' in TMEM
+};
+
+// What follows from a tile's rows.  SUMS: the sums are moved (kSegment), which takes a
+// register for each of a thread's results.
+template <bool SUMS>
+struct Shape {
+    static constexpr int kRows = SUMS ? 192 : 256;  // N of a tile
+    static constexpr int kStageBytes = kABytes + kRows / 2 * kStepBytes;
+    static constexpr int kStages = SUMS ? 6 : 5;
+};
+
+// The second accumulator's first column, and how many it shares with the first.
+template <int FORMAT, bool SUMS>
+struct Accumulators {
+    static constexpr int kSecond = Scales<FORMAT>::kColumn - Shape<SUMS>::kRows;
+    static constexpr int kShared = Shape<SUMS>::kRows > kSecond ? Shape<SUMS>::kRows - kSecond : 0;
+    static_assert(!SUMS || kShared == 0, "moved sums give whole accumulators back");
 };
 
 // Warps: 0 block copies, 1 products, from 4 on eight for the epilogue, then eight for the
@@ -65,30 +81,35 @@ constexpr int kFirstGather = kFirstScale + 8;
 
 template <bool SUMS, bool GATHER>
 struct Warps {
-    static constexpr int kThreads = 32 * (GATHER ? kFirstGather + kStages - 2 : kFirstGather);
+    static constexpr int kThreads =
+        32 * (GATHER ? kFirstGather + Shape<SUMS>::kStages - 2 : kFirstGather);
     // With moved sums the epilogue's warps take some of the others' registers
     // (256 * 144 + 384 * 64 = the launch's 640 * 96; 256 * 128 + 512 * 56 = 768 * 80).
     static constexpr int kMany = GATHER ? 128 : 144, kFew = GATHER ? 56 : 64;
     static constexpr int kLaunched = GATHER ? 80 : 96;
-    static_assert(kThreads == (GATHER ? 768 : 640) &&
-                      256 * kMany + (kThreads - 256) * kFew <= kThreads * kLaunched,
+    static_assert(!SUMS || (kThreads == (GATHER ? 768 : 640) &&
+                            256 * kMany + (kThreads - 256) * kFew <= kThreads * kLaunched),
                   "register split");
 };
 
+template <bool SUMS>
 struct Control {
-    int4 list[kStages * (kRowsMax / 8)];  // rows by number, four a copy, for each stage
+    static constexpr int kStages = Shape<SUMS>::kStages;
+    int4 list[kStages * (Shape<SUMS>::kRows / 8)];  // rows by number, four a copy, for each stage
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], scale_full[2],
-        scale_empty[2];
+        scale_empty[2], shared_empty;
     int4 listed[kListed];        // this pair's first tiles: expert, column, row, rows
     uint32_t tmem;
     int scan[kScanThreads / 32];
     int tiles[kMaxExperts + 1];  // row tiles of the experts before this one
 };
 
-constexpr int kSmemBytes =
-    1024 + kStages * kStageBytes + 2 * kGroupBytes + static_cast<int>(sizeof(Control));
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
-static_assert((kMaxExperts + 1) * 4 <= kStageBytes, "the experts' first rows, at the start");
+template <bool SUMS>
+constexpr int kSmemBytes = 1024 + Shape<SUMS>::kStages * Shape<SUMS>::kStageBytes +
+                           2 * kGroupBytes + static_cast<int>(sizeof(Control<SUMS>));
+static_assert(kSmemBytes<false> <= 227 * 1024 && kSmemBytes<true> <= 227 * 1024,
+              "shared memory of one CTA");
+static_assert((kMaxExperts + 1) * 4 <= kABytes, "the experts' first rows, at the start");
 
 struct Maps {
     CUtensorMap a, b;  // whole blocks
@@ -113,8 +134,8 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 
 // Tile number t: an expert's column blocks lie behind each other, the row tiles of a block
 // together.
-template <typename Lo>
-__device__ __forceinline__ int4 locate_tile(const Fp4GemmArgs &a, const Control &c, int t,
+template <typename C, typename Lo>
+__device__ __forceinline__ int4 locate_tile(const Fp4GemmArgs &a, const C &c, int t,
                                             const Lo &lo) {
     const int mt = divide_up(a.n, 256);
     const int e = expert_of_pass(c.tiles, a.num_experts, 1 << (31 - __clz(a.num_experts)), t / mt);
@@ -128,13 +149,14 @@ __device__ __forceinline__ int4 locate_tile(const Fp4GemmArgs &a, const Control 
 // A pair's tiles in order: every `step`-th one.  The first kListed are found by all threads
 // together at the start (a warp that finds one alone takes 0.3 - 0.5 us, once a tile for
 // either of the copies and the products: 12 of 75 us at 12 tiles a pair).
+template <typename C>
 struct Walk {
     const Fp4GemmArgs &a;
-    const Control &c;
+    const C &c;
     const int first, step, count;
     int i;
 
-    __device__ Walk(const Fp4GemmArgs &args, const Control &control, int tiles)
+    __device__ Walk(const Fp4GemmArgs &args, const C &control, int tiles)
         : a(args), c(control), first(blockIdx.x / 2), step(gridDim.x / 2),
           count((tiles - first + step - 1) / step), i(0) {}
 
@@ -223,20 +245,29 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
     return __all_sync(0xffffffffu, mbar_wait_long<true>(bar, parity, limit_ns));
 }
 
-// 32 output columns (one per lane) by `N` output rows: a row's 64 or 128 bytes are one
-// store of the warp.
-template <int N, typename V>
+// 32 output columns (one per lane) by 16 output rows: a row's 64 or 128 bytes are one store
+// of the warp.
+template <typename V>
 __device__ __forceinline__ void store_rows(const Fp4GemmArgs &a, int64_t out, bool col, int rows,
                                            const V &value) {
     out += threadIdx.x % 32;
 #pragma unroll
-    for (int j = 0; j < N; ++j, out += a.out_ld)
+    for (int j = 0; j < 16; ++j, out += a.out_ld)
         if (col && j < rows) {
             if (a.out_fp32)
                 static_cast<float *>(a.out)[out] = value(j);
             else
                 static_cast<__nv_bfloat16 *>(a.out)[out] = __float2bfloat16_rn(value(j));
         }
+}
+
+// The same of 32 rows in BF16, two to a word.
+__device__ __forceinline__ void store_pairs(const Fp4GemmArgs &a, int64_t out, bool col, int rows,
+                                            const uint32_t (&v)[16]) {
+    uint16_t *o = static_cast<uint16_t *>(a.out) + out + threadIdx.x % 32;
+#pragma unroll
+    for (int j = 0; j < 32; ++j, o += a.out_ld)
+        if (col && j < rows) *o = static_cast<uint16_t>(v[j / 2] >> (j % 2 * 16));
 }
 
 __device__ __forceinline__ void sts_16(uint32_t addr, const uint4 &v) {
@@ -250,15 +281,19 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
     fp4_gemm_kernel(const __grid_constant__ Maps maps, const Fp4GemmArgs a) {
     using W = Warps<SUMS, GATHER>;
     using Sc = Scales<FORMAT>;
+    using Acc = Accumulators<FORMAT, SUMS>;
+    constexpr int kRowsMax = Shape<SUMS>::kRows, kStages = Shape<SUMS>::kStages;
+    constexpr int kStageBytes = Shape<SUMS>::kStageBytes;
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t groups = base + kStages * kStageBytes;
-    Control &c = *reinterpret_cast<Control *>(raw + (groups + 2 * kGroupBytes - smem_u32(raw)));
+    auto &c = *reinterpret_cast<Control<SUMS> *>(raw + (groups + 2 * kGroupBytes - smem_u32(raw)));
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
     const uint32_t full = smem_u32(c.full), empty = smem_u32(c.empty);
     const uint32_t acc_full = smem_u32(c.acc_full), acc_empty = smem_u32(c.acc_empty);
     const uint32_t scale_full = smem_u32(c.scale_full), scale_empty = smem_u32(c.scale_empty);
+    const uint32_t shared_empty = smem_u32(&c.shared_empty);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -271,6 +306,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             mbar_init(scale_full + 8 * i, 4 * 2);
             mbar_init(scale_empty + 8 * i, 1);
         }
+        mbar_init(shared_empty, kEpilogueWarps * 2);
         fence_mbar_init();
     }
     // After the wait, not before: a kernel that this one waits for may want TMEM.
@@ -301,6 +337,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
         const int w = warp % 4, group = (warp - 4) / 4;
         constexpr int kGroups = kEpilogueWarps / 4;
         const uint32_t done_at = map_to_cta(acc_empty, 0);
+        [[maybe_unused]] const uint32_t shared_at = map_to_cta(shared_empty, 0);
         const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
         uint32_t acc_n = 0;  // accumulators taken so far
         while (ok && walk.more()) {
@@ -311,7 +348,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             auto take = [&]() {  // wait for the next accumulator
                 ok = warp_wait(acc_full + 8 * (acc_n & 1), acc_n >> 1 & 1, a.timeout_ns);
                 tcgen05_fence_after();
-                return lanes + (acc_n & 1) * kRowsMax;
+                return lanes + (acc_n & 1) * Acc::kSecond;
             };
             auto give_back = [&]() {
                 tcgen05_fence_before();
@@ -352,20 +389,46 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
                         if (r + 16 * part < d.nrows)
-                            store_rows<16>(a, int64_t{d.row0 + r + 16 * part} * a.out_ld + col0, col,
+                            store_rows(a, int64_t{d.row0 + r + 16 * part} * a.out_ld + col0, col,
                                            d.nrows - r - 16 * part,
                                            [&](int j) { return sums[i][16 * part + j] * factor; });
                 }
             } else {
+                // The columns that the accumulators share are moved first: the first one's
+                // last, the second one's first.  32 rows at a time, two of them in BF16 pairs
+                // before either is stored, as both may lie there.
+                constexpr int kAll = kRowsMax / 32;
+                static_assert(Acc::kShared <= 3 * 32, "within the first two of either group's");
+                const bool second = acc_n & 1;
                 const uint32_t from = take();
                 if (!ok) break;
-                for (int r = group * 32; r < d.nrows; r += kGroups * 32) {
-                    uint32_t v[32];
-                    tmem_ld32(from + r, v);
-                    store_rows<32>(a, int64_t{d.row0 + r} * a.out_ld + col0, col, d.nrows - r,
-                                   [&](int j) { return __uint_as_float(v[j]) * factor; });
+                for (int p = group; p < kAll; p += 2 * kGroups) {
+                    uint32_t pairs[2][16];
+                    int r[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int at = p + i * kGroups;
+                        r[i] = 32 * (second ? at : kAll - 1 - at);
+                        if (r[i] >= d.nrows) continue;
+                        uint32_t v[32];
+                        tmem_ld32(from + r[i], v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            pairs[i][j] = pack2_rn(__uint_as_float(v[2 * j]) * factor,
+                                                   __uint_as_float(v[2 * j + 1]) * factor);
+                    }
+                    if (p == group) {
+                        tcgen05_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(shared_at);
+                    }
+                    if (p + 2 * kGroups >= kAll) give_back();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (r[i] < d.nrows)
+                            store_pairs(a, int64_t{d.row0 + r[i]} * a.out_ld + col0, col,
+                                        d.nrows - r[i], pairs[i]);
                 }
-                give_back();
             }
         }
     } else {
@@ -424,8 +487,9 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             const uint32_t operands_upper = static_cast<uint32_t>(operands >> 32);
             const uint32_t blocks_upper = static_cast<uint32_t>(blocks >> 32);
             constexpr int kRowsFrom = Sc::kWords;  // the rows' first block
-            uint32_t stage = 0, phase = 0, acc_n = 0, group_n = 0, scales = tmem + kScaleColumn;
+            uint32_t stage = 0, phase = 0, acc_n = 0, group_n = 0, scales = tmem + Sc::kColumn;
             const uint32_t turn = scales ^ (scales + Sc::kColumns);
+            int before = 0;  // rows of the tile before
             const auto products = [&](const int n) {
                 const uint32_t idesc = fp4_desc<FORMAT>(n);
                 int in_segment = 0, in_group = 0;
@@ -438,15 +502,24 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                             return false;
                         from = static_cast<uint32_t>(blocks) + (group_n & 1) * (kGroupBytes / 16);
                     }
-                    if (in_segment == 0 && !warp_wait(acc_empty + 8 * (acc_n & 1),
-                                                      (acc_n >> 1 & 1) ^ 1, a.timeout_ns))
-                        return false;
+                    if (in_segment == 0) {
+                        if (!warp_wait(acc_empty + 8 * (acc_n & 1), (acc_n >> 1 & 1) ^ 1,
+                                       a.timeout_ns))
+                            return false;
+                        // The columns shared with the tile before, where either reaches them
+                        // (the tile before that has left all its columns, so that the parity
+                        // tells).
+                        if (Acc::kShared > 0 && (acc_n & 1 ? before : n) > Acc::kSecond &&
+                            acc_n > 0 && !warp_wait(shared_empty, (acc_n & 1) ^ 1, a.timeout_ns))
+                            return false;
+                        before = n;
+                    }
                     if (!warp_wait(full + 8 * stage, phase, a.timeout_ns)) return false;
                     tcgen05_fence_after();
                     const uint32_t bar = empty + 8 * stage;
                     const uint32_t da = static_cast<uint32_t>(operands) + stage * (kStageBytes / 16);
                     const uint32_t db = da + kABytes / 16;
-                    const uint32_t dst = tmem + (acc_n & 1) * kRowsMax;
+                    const uint32_t dst = tmem + (acc_n & 1) * Acc::kSecond;
                     ++in_group;
                     ++in_segment;
                     const bool group_end = left == 1 || in_group == Sc::kSteps;
@@ -657,13 +730,14 @@ template <int FORMAT, bool GATHER, bool SUMS>
 cudaError_t launch(const Maps &maps, const Fp4GemmArgs &a, int64_t tiles, cudaStream_t s) {
     const unsigned ctas = static_cast<unsigned>(2 * min(tiles, int64_t{a.num_pairs}));
     return launch_ex(fp4_gemm_kernel<FORMAT, GATHER, SUMS>, dim3(ctas),
-                     dim3(Warps<SUMS, GATHER>::kThreads), kSmemBytes, s, 2, a.programmatic, maps, a);
+                     dim3(Warps<SUMS, GATHER>::kThreads), kSmemBytes<SUMS>, s, 2, a.programmatic,
+                     maps, a);
 }
 
 template <int FORMAT, bool GATHER, bool SUMS>
 cudaError_t prepare() {
     return cudaFuncSetAttribute(fp4_gemm_kernel<FORMAT, GATHER, SUMS>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<SUMS>);
 }
 
 }  // namespace
@@ -688,7 +762,7 @@ cudaError_t prepare_fp4_gemm(int *pairs) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(Warps<true, true>::kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = kSmemBytes<true>;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaOccupancyMaxActiveClusters(pairs, fp4_gemm_kernel<kNv, true, true>, &cfg);
@@ -710,11 +784,12 @@ cudaError_t launch_fp4_gemm(const Fp4GemmArgs &a, cudaStream_t s) {
         !encode_map(&m.b4, type, a.x, 2, {bytes, xr, 1}, {x_ld, 0}, kStepBytes, 1))
         return cudaErrorInvalidValue;
     // at most this many tiles: the experts' sizes are known on the device only
-    const int64_t tiles = (n + 255) / 256 *
-                          (a.rows / kRowsMax + min(int64_t{a.num_experts}, a.rows));
+    const bool sums = a.out_fp32 || a.k > kLongSum, gather = a.row_index != nullptr;
+    const int64_t tiles =
+        (n + 255) / 256 * (a.rows / (sums ? Shape<true>::kRows : Shape<false>::kRows) +
+                           min(int64_t{a.num_experts}, a.rows));
     // tiles are counted in 32 bits (results of so many do not fit into memory)
     if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-    const bool sums = a.out_fp32 || a.k > kLongSum, gather = a.row_index != nullptr;
     if (a.format == kMx) {
         if (sums)
             return gather ? launch<kMx, true, true>(m, a, tiles, s)
