@@ -34,7 +34,7 @@ constexpr int kABytes = 128 * kStepBytes;  // A of one CTA and stage
 constexpr int kBlockBytes = 512;          // of scales: 32 lanes by 16 bytes, four TMEM columns
 constexpr int kTmemColumns = 512;
 constexpr int kScanThreads = 256;         // threads that scan the experts
-constexpr int kListed = 128;              // tiles of a pair that are found at the start
+constexpr int kListed = 64;               // tiles of a pair that are found at the start
 // Scales of a group, 64 bytes a row: four pieces of 16 bytes a row (one step's, or two), as
 // blocks for 128 columns and 256 rows.
 constexpr int kPieceBytes = 12 * kBlockBytes;
@@ -74,15 +74,15 @@ struct Accumulators {
 };
 
 // Warps: 0 block copies, 1 products, from 4 on eight for the epilogue, then eight for the
-// scales, then those that gather (with 2 and 3, one to a stage).
+// scales, then those that gather (with 2 and 3).
 constexpr int kEpilogueWarps = 8;
 constexpr int kFirstScale = 4 + kEpilogueWarps;
 constexpr int kFirstGather = kFirstScale + 8;
 
 template <bool SUMS, bool GATHER>
 struct Warps {
-    static constexpr int kThreads =
-        32 * (GATHER ? kFirstGather + Shape<SUMS>::kStages - 2 : kFirstGather);
+    static constexpr int kGatherWarps = SUMS ? 6 : 8;
+    static constexpr int kThreads = 32 * (GATHER ? kFirstGather + kGatherWarps - 2 : kFirstGather);
     // With moved sums the epilogue's warps take some of the others' registers
     // (256 * 144 + 384 * 64 = the launch's 640 * 96; 256 * 128 + 512 * 56 = 768 * 80).
     static constexpr int kMany = GATHER ? 128 : 144, kFew = GATHER ? 56 : 64;
@@ -95,9 +95,9 @@ struct Warps {
 template <bool SUMS>
 struct Control {
     static constexpr int kStages = Shape<SUMS>::kStages;
-    int4 list[kStages * (Shape<SUMS>::kRows / 8)];  // rows by number, four a copy, for each stage
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], scale_full[2],
         scale_empty[2], shared_empty;
+    int numbers[8][2 * 64];      // of gathered rows, for the scales' warps
     int4 listed[kListed];        // this pair's first tiles: expert, column, row, rows
     uint32_t tmem;
     int scan[kScanThreads / 32];
@@ -268,6 +268,10 @@ __device__ __forceinline__ void store_pairs(const Fp4GemmArgs &a, int64_t out, b
 #pragma unroll
     for (int j = 0; j < 32; ++j, o += a.out_ld)
         if (col && j < rows) *o = static_cast<uint16_t>(v[j / 2] >> (j % 2 * 16));
+}
+
+__device__ __forceinline__ void cp_async_4(int *dst, const int32_t *p) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(p) : "memory");
 }
 
 __device__ __forceinline__ void sts_16(uint32_t addr, const uint4 &v) {
@@ -590,9 +594,37 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                     : "l"(p), "r"(uint32_t{read}));
                 return v;
             };
+            // What a tile's first reads would wait for, a tile ahead: the numbers of its rows (to
+            // shared memory; a warp needs those of eight lines), and the columns' scales in L2.
+            int *numbers = c.numbers[warp - kFirstScale];  // of this tile, or the next
+            int turn = 0;
+            const int stride = groups_of_tile == 1 ? 2 : 1;  // from one of this team's tiles on
+            auto prepare_tile = [&](const Tile &e, int buffer) {
+                if (GATHER) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int u = lane / 8 + 4 * half, i = 32 * u + warp % 4 * 8 + lane % 8;
+                        if (u < kRowsMax / 32 && i < e.nrows)
+                            cp_async_4(numbers + buffer * 64 + 8 * u + lane % 8,
+                                       a.row_index + e.row0 + i);
+                    }
+                    cp_async_commit();
+                }
+                const int n0 = e.m0 + static_cast<int>(rank) * 128, n = min(128, a.n - n0);
+                if (threadIdx.x == 32 * kFirstScale && n > 0 && w_ld <= 2u * row_bytes + 16) {
+                    const uint8_t *p = a.w_scales + e.expert * a.ws_expert + uint64_t{w_ld} * n0;
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p),
+                                 "r"((n - 1) * w_ld + round_up(row_bytes, 16))
+                                 : "memory");
+                }
+            };
             auto read_group = [&](int g) {
                 const int tile = g / groups_of_tile;
                 if (tile >= walk.i) {  // the tile was not taken yet
+                    if (GATHER) {
+                        cp_async_wait<0>();
+                        __syncwarp();
+                    }
                     walk.i = tile;
                     const Tile d = walk.take();
                     w_row = d.m0 + static_cast<int>(rank) * 128 + line;
@@ -602,12 +634,15 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                         const int i = 32 * u + line;
                         int row = -1;
                         if (i < d.nrows) {
-                            row = d.row0 + i;
-                            if (GATHER) row = __ldg(a.row_index + row);
+                            row = GATHER ? numbers[turn * 64 + 8 * u + lane % 8] : d.row0 + i;
                             if (row >= a.x_rows) row = -1;
                         }
                         x_rows[u] = row;
                     }
+                    turn ^= 1;
+                    auto next = walk;
+                    next.i = tile + stride;
+                    if (next.more()) prepare_tile(next.take(), turn);
                 }
                 const int from = (g - tile * groups_of_tile) * 64 + piece * 16;
                 const int valid = row_bytes - from;
@@ -635,7 +670,12 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                     }
                 }
             };
-            if (team < all) read_group(team);
+            if (team < all) {
+                auto first = walk;
+                first.i = team / groups_of_tile;
+                prepare_tile(first.take(), turn);
+                read_group(team);
+            }
             const uint32_t to = groups + team * kGroupBytes + piece * kPieceBytes + line * 16;
             uint32_t n = 0;  // groups of this team so far
             for (int g = team; g < all; g += 2, ++n) {
@@ -666,52 +706,46 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             // the last group's copies are done, before this CTA may leave
             if (ok && n > 0) ok = warp_wait(scale_empty + 8 * team, (n & 1) ^ 1, a.timeout_ns);
         } else if (GATHER && (warp == 2 || warp == 3 || warp >= kFirstGather)) {
-            // Rows by number, four a copy (-1, no such row, arrives as zeros), a warp to a stage.
-            // The numbers go through shared memory, so that the elected lane reads them with
-            // uniform addresses.
-            const uint32_t stage = warp < 4 ? warp - 2 : warp - kFirstGather + 2;
-            const uint32_t bar = full_at + 8 * stage;
-            const uint32_t sb = base + stage * kStageBytes + kABytes;
-            int4 *list = c.list + stage * (kRowsMax / 8);
-            uint32_t it = stage;  // this warp's next step, over the tiles
-            uint32_t done = 0;    // steps of the tiles before
+            // Rows by number, four a copy (-1, no such row, arrives as zeros).  Every warp issues
+            // up to four of a step's copies, some 80 cycles each: with a warp to a stage, which
+            // takes four times as long, the step waits for it (249 against 205 us of blocks).
+            constexpr int kQuads = kRowsMax / 8 / W::kGatherWarps;
+            static_assert(kQuads * W::kGatherWarps * 8 == kRowsMax, "fours of a CTA's half");
+            const int index = warp < 4 ? warp - 2 : warp - kFirstGather + 2;
+            uint32_t stage = 0, phase = 1;
             while (ok && walk.more()) {
                 const Tile d = walk.take();
                 const int half = d.n / 2, b0 = d.row0 + rank * half;
-                const int row_end = d.row0 + d.nrows, quads = half / 4;
+                const int row_end = d.row0 + d.nrows;
                 auto x_row = [&](int i) {
                     const int v = i < row_end ? __ldg(a.row_index + i) : -1;
                     return v >= 0 && v < a.x_rows ? v : -1;
                 };
-                if (it < done + steps) {
-                    if (lane < quads) {  // of the CTA's half: 24 fours at most
-                        const int i = b0 + 4 * lane;
-                        list[lane] = make_int4(x_row(i), x_row(i + 1), x_row(i + 2), x_row(i + 3));
-                    }
-                    __syncwarp();
+                int4 rows[kQuads];
+#pragma unroll
+                for (int q = 0; q < kQuads; ++q) {
+                    const int i = b0 + 4 * (W::kGatherWarps * q + index);
+                    rows[q] = make_int4(x_row(i), x_row(i + 1), x_row(i + 2), x_row(i + 3));
                 }
-                for (; it < done + steps; it += kStages) {
-                    ok = warp_wait(empty + 8 * stage, (it / kStages & 1) ^ 1, a.timeout_ns);
+                const int quads = (half / 4 - index + W::kGatherWarps - 1) / W::kGatherWarps;
+                for (int s = 0; s < steps; ++s) {
+                    ok = warp_wait(empty + 8 * stage, phase, a.timeout_ns);
                     if (!ok) break;
                     if (elect_one()) {
-                        const int x = static_cast<int>(it - done) * kStepBytes;
-                        // eight at a time: the numbers are read before the first copy
-                        constexpr int kBatch = 8;
-                        for (int q0 = 0; q0 < quads; q0 += kBatch) {
-                            int4 rows[kBatch];
+                        const uint32_t bar = full_at + 8 * stage;
+                        const uint32_t sb = base + stage * kStageBytes + kABytes + index * 512;
 #pragma unroll
-                            for (int q = 0; q < kBatch; ++q)
-                                if (q0 + q < quads) rows[q] = list[q0 + q];
-#pragma unroll
-                            for (int q = 0; q < kBatch; ++q)
-                                if (q0 + q < quads)
-                                    tma_gather4<true>(sb + (q0 + q) * 512, &maps.b4, x, rows[q],
-                                                      bar);
-                        }
+                        for (int q = 0; q < kQuads; ++q)
+                            if (q < quads)
+                                tma_gather4<true>(sb + q * (W::kGatherWarps * 512), &maps.b4,
+                                                  s * kStepBytes, rows[q], bar);
                     }
                     __syncwarp();
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
                 }
-                done += steps;
             }
         }
     }
