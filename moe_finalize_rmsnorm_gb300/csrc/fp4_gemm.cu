@@ -81,14 +81,13 @@ constexpr int kFirstGather = kFirstScale + 8;
 
 template <bool SUMS, bool GATHER>
 struct Warps {
-    static constexpr int kGatherWarps = SUMS ? 6 : 8;
+    static constexpr int kGatherWarps = 6;
     static constexpr int kThreads = 32 * (GATHER ? kFirstGather + kGatherWarps - 2 : kFirstGather);
     // With moved sums the epilogue's warps take some of the others' registers
     // (256 * 144 + 384 * 64 = the launch's 640 * 96; 256 * 128 + 512 * 56 = 768 * 80).
     static constexpr int kMany = GATHER ? 128 : 144, kFew = GATHER ? 56 : 64;
-    static constexpr int kLaunched = GATHER ? 80 : 96;
-    static_assert(!SUMS || (kThreads == (GATHER ? 768 : 640) &&
-                            256 * kMany + (kThreads - 256) * kFew <= kThreads * kLaunched),
+    static_assert(kThreads == (GATHER ? 768 : 640) && 256 * kMany + (kThreads - 256) * kFew <=
+                                                          kThreads * (GATHER ? 80 : 96),
                   "register split");
 };
 
@@ -335,7 +334,8 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
 
     bool ok = true;
     if (warp >= 4 && warp < kFirstScale) {
-        if constexpr (SUMS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::kMany));
+        if constexpr (SUMS)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::kMany));
         // Results: lane = output column, TMEM column = output row; eight warps, of which
         // two take the same 32 lanes and every other 32 rows.
         const int w = warp % 4, group = (warp - 4) / 4;
@@ -707,10 +707,9 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             if (ok && n > 0) ok = warp_wait(scale_empty + 8 * team, (n & 1) ^ 1, a.timeout_ns);
         } else if (GATHER && (warp == 2 || warp == 3 || warp >= kFirstGather)) {
             // Rows by number, four a copy (-1, no such row, arrives as zeros).  Every warp issues
-            // up to four of a step's copies, some 80 cycles each: with a warp to a stage, which
-            // takes four times as long, the step waits for it (249 against 205 us of blocks).
-            constexpr int kQuads = kRowsMax / 8 / W::kGatherWarps;
-            static_assert(kQuads * W::kGatherWarps * 8 == kRowsMax, "fours of a CTA's half");
+            // some of a step's copies, 80 cycles each: with a warp to a stage, which takes six
+            // times as long, the step waits for it.
+            constexpr int kQuads = (kRowsMax / 8 + W::kGatherWarps - 1) / W::kGatherWarps;
             const int index = warp < 4 ? warp - 2 : warp - kFirstGather + 2;
             uint32_t stage = 0, phase = 1;
             while (ok && walk.more()) {
