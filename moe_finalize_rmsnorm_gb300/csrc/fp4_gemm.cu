@@ -20,6 +20,15 @@
 // TMEM has 512 columns, and two steps' scales take 96 (E4M3) or 48 of them.  So with 256
 // rows the two accumulators overlap: by 96 or 48 columns, which the epilogue moves out
 // first, and says so, before the rest.
+//
+// What bounds it (GB300, 4096 x 4096, short runs): up to some 200 rows an expert the
+// weights' bytes (32 experts of 64 rows 52 us, E8M0; 45 at the copy bandwidth).  Beyond,
+// shared memory, which moves 128 bytes a cycle: a step of 256 rows brings 32 KB in and
+// reads it once more (512 cycles, as many as its products take), and its scales, read
+// through L1, written as blocks and read again, take 192 (E4M3) or 96.  512 rows an expert
+// run at 5.7 (E8M0) and 4.8 (E4M3) PFLOP/s, gathered 5.4 and 4.6; without the scales' reads
+// they would at 6.1.  Tiles of 192 rows, which the scales leave whole accumulators for: 5.2
+// and 4.3.
 #include "experts.cuh"
 #include "experts.h"
 #include "fp4.cuh"
@@ -42,7 +51,11 @@ constexpr int kGroupBytes = 4 * kPieceBytes;
 
 // FP32 results, and BF16 results of more than kLongSum summed values: the sums leave the
 // tensor cores every this many steps and are added up in registers, as the tensor cores
-// truncate each partial sum.
+// truncate each partial sum, towards zero: of values of one sign (E4M3 scales) one
+// accumulator loses 6.9e-7 of the sum at 4096 values, 4.4e-6 at 16384, 4.3e-5 at 131072 and
+// 1.8e-4 at 524288.  Moved every 10 steps it is 2.6e-7 to 3.8e-7 at any of these lengths,
+// and 5.8e-8 of 4096 values of either sign.  Up to kLongSum the loss is far below the BF16
+// rounding (1.4e-3).
 constexpr int kSegment = 10;
 constexpr int kLongSum = 131072;
 
@@ -96,7 +109,6 @@ struct Control {
     static constexpr int kStages = Shape<SUMS>::kStages;
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], scale_full[2],
         scale_empty[2], shared_empty;
-    int numbers[8][2 * 64];      // of gathered rows, for the scales' warps
     int4 listed[kListed];        // this pair's first tiles: expert, column, row, rows
     uint32_t tmem;
     int scan[kScanThreads / 32];
@@ -269,10 +281,6 @@ __device__ __forceinline__ void store_pairs(const Fp4GemmArgs &a, int64_t out, b
         if (col && j < rows) *o = static_cast<uint16_t>(v[j / 2] >> (j % 2 * 16));
 }
 
-__device__ __forceinline__ void cp_async_4(int *dst, const int32_t *p) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(p) : "memory");
-}
-
 __device__ __forceinline__ void sts_16(uint32_t addr, const uint4 &v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
                  "r"(v.z), "r"(v.w)
@@ -300,7 +308,9 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + 8 * i, 1);
+            // the byte count, and all gathering warps: one without a row in a small tile would
+            // else fall behind `empty`, whose parity does not tell two phases apart
+            mbar_init(full + 8 * i, 1 + (GATHER ? 2 * W::kGatherWarps : 0));
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -394,8 +404,8 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                     for (int part = 0; part < 2; ++part)
                         if (r + 16 * part < d.nrows)
                             store_rows(a, int64_t{d.row0 + r + 16 * part} * a.out_ld + col0, col,
-                                           d.nrows - r - 16 * part,
-                                           [&](int j) { return sums[i][16 * part + j] * factor; });
+                                       d.nrows - r - 16 * part,
+                                       [&](int j) { return sums[i][16 * part + j] * factor; });
                 }
             } else {
                 // The columns that the accumulators share are moved first: the first one's
@@ -568,7 +578,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
         } else if (warp >= kFirstScale && warp < kFirstGather) {
             // Scales.  Two teams of four warps take every other group (a read takes a group's time
             // and more).  A thread takes 16 bytes (a piece) of one row in 32 and of those every
-            // 32 behind it: four of the tile's columns, and up to six of its rows, of which four
+            // 32 behind it: four of the tile's columns, and up to eight of its rows, of which four
             // rows' words make a lane of a block.  Eight lanes have eight rows' same piece: 128
             // bytes of a block.
             const int team = (warp - kFirstScale) / 4;
@@ -582,7 +592,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
             const uint8_t *w_from = nullptr;  // the expert's scales
             int w_row = 0;                    // this thread's first column
             int x_rows[kRowsMax / 32];        // its rows of x, -1: none (zeros)
-            uint4 q[12] = {};                 // (the last 64 rows of the blocks do not exist)
+            uint4 q[12] = {};                 // (blocks are for 256 rows)
             const auto read_16 = [](const uint8_t *base, uint32_t row, uint32_t ld, bool read) {
                 const uint8_t *p = base + uint64_t{row} * ld;
                 uint4 v;
@@ -594,37 +604,9 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                     : "l"(p), "r"(uint32_t{read}));
                 return v;
             };
-            // What a tile's first reads would wait for, a tile ahead: the numbers of its rows (to
-            // shared memory; a warp needs those of eight lines), and the columns' scales in L2.
-            int *numbers = c.numbers[warp - kFirstScale];  // of this tile, or the next
-            int turn = 0;
-            const int stride = groups_of_tile == 1 ? 2 : 1;  // from one of this team's tiles on
-            auto prepare_tile = [&](const Tile &e, int buffer) {
-                if (GATHER) {
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int u = lane / 8 + 4 * half, i = 32 * u + warp % 4 * 8 + lane % 8;
-                        if (u < kRowsMax / 32 && i < e.nrows)
-                            cp_async_4(numbers + buffer * 64 + 8 * u + lane % 8,
-                                       a.row_index + e.row0 + i);
-                    }
-                    cp_async_commit();
-                }
-                const int n0 = e.m0 + static_cast<int>(rank) * 128, n = min(128, a.n - n0);
-                if (threadIdx.x == 32 * kFirstScale && n > 0 && w_ld <= 2u * row_bytes + 16) {
-                    const uint8_t *p = a.w_scales + e.expert * a.ws_expert + uint64_t{w_ld} * n0;
-                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p),
-                                 "r"((n - 1) * w_ld + round_up(row_bytes, 16))
-                                 : "memory");
-                }
-            };
             auto read_group = [&](int g) {
                 const int tile = g / groups_of_tile;
                 if (tile >= walk.i) {  // the tile was not taken yet
-                    if (GATHER) {
-                        cp_async_wait<0>();
-                        __syncwarp();
-                    }
                     walk.i = tile;
                     const Tile d = walk.take();
                     w_row = d.m0 + static_cast<int>(rank) * 128 + line;
@@ -634,15 +616,12 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                         const int i = 32 * u + line;
                         int row = -1;
                         if (i < d.nrows) {
-                            row = GATHER ? numbers[turn * 64 + 8 * u + lane % 8] : d.row0 + i;
+                            row = d.row0 + i;
+                            if (GATHER) row = __ldg(a.row_index + row);
                             if (row >= a.x_rows) row = -1;
                         }
                         x_rows[u] = row;
                     }
-                    turn ^= 1;
-                    auto next = walk;
-                    next.i = tile + stride;
-                    if (next.more()) prepare_tile(next.take(), turn);
                 }
                 const int from = (g - tile * groups_of_tile) * 64 + piece * 16;
                 const int valid = row_bytes - from;
@@ -670,12 +649,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                     }
                 }
             };
-            if (team < all) {
-                auto first = walk;
-                first.i = team / groups_of_tile;
-                prepare_tile(first.take(), turn);
-                read_group(team);
-            }
+            if (team < all) read_group(team);
             const uint32_t to = groups + team * kGroupBytes + piece * kPieceBytes + line * 16;
             uint32_t n = 0;  // groups of this team so far
             for (int g = team; g < all; g += 2, ++n) {
@@ -738,6 +712,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                             if (q < quads)
                                 tma_gather4<true>(sb + q * (W::kGatherWarps * 512), &maps.b4,
                                                   s * kStepBytes, rows[q], bar);
+                        mbar_arrive_cluster(bar);
                     }
                     __syncwarp();
                     if (++stage == kStages) {

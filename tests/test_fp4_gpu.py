@@ -232,10 +232,10 @@ def check(s, out):
     want, size = exact(s)
     want, size, got = want[:live], size[:live], out[:live, :n].double()
     # one accumulator in the tensor cores, which truncate a partial sum every 64 values (by 2^-22
-    # of the terms at most); FP32 results leave them every 40 truncations, and the pieces are
-    # added in FP32, by up to 16 warps; the factor's product
+    # of the terms at most); FP32 results, and longer sums than 131072, leave them every 40
+    # truncations, and the pieces are added in FP32, by up to 16 warps; the factor's product
     cuts, adds = -(-s["k"] // 64), -(-s["k"] // 32) + 16
-    if out.dtype == FP32:
+    if out.dtype == FP32 or s["k"] > 131072:
         cuts = min(cuts, 40)
     bound = (cuts * 2.0 ** -22 + (adds + 1) * U) * size
     bound = bound + (want.abs() + bound) * (torch.finfo(out.dtype).eps / 2)
@@ -272,6 +272,35 @@ def test_dense(cuda_lib, fmt, rows):
     s["off"] = None
     for dtype in (BF16, FP32):
         check(s, product(cuda_lib, s, dtype))
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_many_tiles(cuda_lib, fmt):
+    """More tiles for a pair of SMs than it lists at its start (64), gathered or not."""
+    for gather, dtype in ((False, BF16), (True, BF16), (True, FP32)):
+        s = layer([3, 1] * 32, 21 * 1024 + 8, 64, fmt, gather=gather, seed=4, extra=2, factor=True)
+        check(s, product(cuda_lib, s, dtype))
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_long_sums(cuda_lib, fmt):
+    """BF16 results of sums that leave the tensor cores on their way, and just not."""
+    for k in (131072, 131104, 200032):
+        for gather in (False, True):
+            s = layer([40, 3], 72, k, fmt, gather=gather, seed=k)
+            for dtype in (BF16, FP32):
+                check(s, product(cuda_lib, s, dtype))
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_small_tiles_between_large_ones(cuda_lib, fmt):
+    """Tiles that reach the columns both accumulators have, and tiles that do not, in any order;
+    gathering warps without a row in between."""
+    sizes = [256, 3, 200, 1, 256, 256, 40, 130, 5, 250, 0, 90, 255, 161, 209, 160, 208]
+    for k in (64, 544, 2080):
+        for gather in (False, True):
+            s = layer(sizes * 3, 264, k, fmt, gather=gather, seed=k)
+            check(s, product(cuda_lib, s, BF16))
 
 
 @pytest.mark.parametrize("fmt", [MX, NV])
