@@ -23,8 +23,8 @@ mf_status check_sizes(int64_t num_tokens, int64_t rows, int32_t hidden, int32_t 
         return MF_ERR_UNSUPPORTED;
     if (rows < 0 || rows > mf::kMaxRows || num_tokens < 0 || num_tokens > mf::kMaxRows / top_k)
         return MF_ERR_SHAPE;
-    // a thread for every eight columns, 128 to a block
-    if ((num_tokens * (hidden / 8) + 127) / 128 > 0x7fffffffLL) return MF_ERR_SHAPE;
+    // a thread for every four columns, 128 to a block
+    if ((num_tokens * (hidden / 4) + 127) / 128 > 0x7fffffffLL) return MF_ERR_SHAPE;
     return MF_OK;
 }
 

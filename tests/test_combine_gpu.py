@@ -80,9 +80,10 @@ def check_combine(s, out):
 def check_grad_weights(s, gw):
     terms = gathered(s) * s["x"].double().unsqueeze(1)
     want = terms.sum(-1)
-    # additions on the longest way: a chunk's 4, the two chains' one, a thread's chunks (a team
-    # has 32 threads at least), 5 between lanes, up to 16 warps; a product's own half step
-    depth = 1 + 4 + 1 + -(-s["H"] // 256) + 5 + 16
+    # additions on the longest way: a chunk's 4, the two chains' one, a thread's chunks (of four
+    # columns or more; a team has 32 threads at least), 5 between lanes, up to 16 warps; a
+    # product's own half step
+    depth = 1 + 4 + 1 + -(-s["H"] // 128) + 5 + 16
     bound = depth * U * terms.abs().sum(-1) * (1 + 2 ** -10)
     bound = bound + (want.abs() + bound) * (torch.finfo(gw.dtype).eps / 2)
     assert ((gw.double() - want).abs() <= bound).all()
@@ -130,12 +131,13 @@ def test_parity(cuda_lib, T, K, H, rows_dtype, token_dtype):
                 assert whole[:, H:].isnan().all()
 
 
-@pytest.mark.parametrize("T", [1, 2, 607, 608, 609, 4000])
-@pytest.mark.parametrize("H", [512, 520, 2048, 2056])
-def test_team_edges(cuda_lib, T, H):
-    """Around the choices of how many threads take a token's gradients."""
-    s = make(T, 3, H, seed=T)
-    gw = torch.full((T, 3), float("nan"), device="cuda")
+@pytest.mark.parametrize("T", [1, 2, 152, 153, 608, 4001])
+@pytest.mark.parametrize("H", [1528, 1536, 1544, 2048, 2056])
+@pytest.mark.parametrize("K", [3, 4, 5, 9])
+def test_team_edges(cuda_lib, T, H, K):
+    """Around the choices of how many threads take a token's gradients, and how many slots."""
+    s = make(T, K, H, seed=T)
+    gw = torch.full((T, K), float("nan"), device="cuda")
     cuda_lib.moe_combine_backward(s["x"], s["p"], s["w"], s["idx"], s["out_rows"], gw)
     check_dispatch(s, s["out_rows"])
     check_grad_weights(s, gw)
