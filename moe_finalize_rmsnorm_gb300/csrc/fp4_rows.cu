@@ -7,8 +7,8 @@
 // along M, on FP16: E2M1 values are exact there.  A lane takes the eight values of a
 // 32-bit word, the four lanes of a quad the 32 of a block:
 //
-//   E8M0   a block's sum is exact (multiples of 1/4 up to 1152); it is scaled in FP32,
-//          acc += (sum * scale of the column) * scale of the row
+//   E8M0   a block's sum is exact (multiples of 1/4 up to 1152), and so is the product of
+//          the two scales within FP32's range: acc += sum * (column's scale * row's scale)
 //   E4M3   q * scale is exact in FP16 (6 bits, 2^-10 .. 2688) and is what is multiplied;
 //          the tensor cores truncate their partial sums, so every 64 values' sum is begun
 //          anew and added up in FP32
@@ -288,8 +288,10 @@ struct Fp4Rows {
                         for (int j = 0; j < 4; ++j) {
                             if (FORMAT == kMx)
                                 acc[m][j] =
-                                    fmaf(sum[m][j] * __uint_as_float(word(sw[2 * m + j / 2], b)),
-                                         __uint_as_float(word(sx[j % 2], b)), acc[m][j]);
+                                    fmaf(sum[m][j],
+                                         __uint_as_float(word(sw[2 * m + j / 2], b)) *
+                                             __uint_as_float(word(sx[j % 2], b)),
+                                         acc[m][j]);
                             else if (b % 2 == 1)
                                 acc[m][j] += sum[m][j];
                         }

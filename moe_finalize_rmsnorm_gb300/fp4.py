@@ -42,42 +42,37 @@ def moe_fp4_empty(shape: tuple, k: int, scale_dtype: torch.dtype, *, device="cud
     return q, s[..., :groups].view(scale_dtype)
 
 
-def _packed(q: torch.Tensor, scales: torch.Tensor, name: str, dims: int) -> tuple[int, int]:
-    """Check packed values and their scales; returns (format, k)."""
-    if q.dim() != dims or q.dtype != torch.uint8 or (q.stride(-1) != 1 and q.shape[-1] > 1):
+def _packed(q: torch.Tensor, scales: torch.Tensor, name: str, dims: int
+            ) -> tuple[int, int, int, int]:
+    """Check packed values and their scales; returns (format, k, bytes between the rows of
+    the values and of the scales)."""
+    qn, qst = q.shape, q.stride()
+    if len(qn) != dims or q.dtype != torch.uint8 or (qst[-1] != 1 and qn[-1] > 1):
         raise ValueError(f"{name} must be a {dims}-D uint8 tensor with unit last-dim stride")
     f = _FORMATS.get(scales.dtype)
-    if f is None or scales.dim() != dims or (scales.stride(-1) != 1 and scales.shape[-1] > 1):
+    sn, sst = scales.shape, scales.stride()
+    if f is None or len(sn) != dims or (sst[-1] != 1 and sn[-1] > 1):
         raise ValueError(f"{name}'s scales must be a {dims}-D tensor of float8_e8m0fnu or "
                          "float8_e4m3fn with unit last-dim stride")
-    k = 2 * q.shape[-1]
-    if k % 32 != 0 or scales.shape[:-1] != q.shape[:-1] or scales.shape[-1] * f[1] != k:
+    width, groups = qn[-1], sn[-1]
+    if width % 16 != 0 or sn[:-1] != qn[:-1] or groups * f[1] != 2 * width:
         raise ValueError(f"{name}'s scales must cover blocks of {f[1]} columns of its rows, "
                          "and its columns must be a multiple of 32")
-    return f[0], k
+    if qn[-2] > 1:
+        return f[0], 2 * width, qst[-2], sst[-2]
+    return f[0], 2 * width, width, (groups + 15) // 16 * 16  # one row: no stride to keep
 
 
 def _whole_pieces(scales: torch.Tensor, name: str) -> None:
     """The product reads scales in 16-byte pieces: the last row's has to lie in its memory."""
-    if scales.numel():
-        end = scales.storage_offset() + sum((n - 1) * st for n, st in
-                                            zip(scales.shape, scales.stride()))
-        end += 1 + -scales.shape[-1] % 16
+    shape = scales.shape
+    if shape[-1] % 16 != 0 and scales.numel():
+        end = scales.storage_offset() + 1 + -shape[-1] % 16
+        for n, st in zip(shape, scales.stride()):
+            end += (n - 1) * st
         if end > scales.untyped_storage().nbytes():
             raise ValueError(f"{name}'s last row must be followed by bytes up to a multiple of 16 "
                              "(as moe_fp4_empty allocates)")
-
-
-def _row_bytes(t: torch.Tensor) -> int:
-    """Bytes between the rows of packed values or scales; one row has none to keep."""
-    if t.shape[-2] > 1:
-        return t.stride(-2)
-    return (t.shape[-1] + 15) // 16 * 16
-
-
-def _written(t: torch.Tensor, name: str) -> None:
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}'s rows must not overlap")
 
 
 def moe_quantize_fp4(x: torch.Tensor, quantized: torch.Tensor, scales: torch.Tensor, *,
@@ -94,9 +89,8 @@ def moe_quantize_fp4(x: torch.Tensor, quantized: torch.Tensor, scales: torch.Ten
     multiple of 32; factor: FP32 tensor of one element.  Returns ``(quantized, scales)``.
     """
     x_ld = _rows(x, "x", _VALUE_DTYPES)
-    fmt, k = _packed(quantized, scales, "quantized", 2)
-    _written(quantized, "quantized")
-    _written(scales, "scales")
+    fmt, k, q_ld, s_ld = _packed(quantized, scales, "quantized", 2)
+    _req(2 * q_ld >= k and s_ld * 32 >= k, "the rows of quantized and scales must not overlap")
     rows = quantized.shape[0]
     _req(x.shape == (rows, k), "x and quantized disagree on the rows or on k")
     _req(factor is None or (factor.dtype == torch.float32 and factor.numel() == 1),
@@ -105,8 +99,8 @@ def moe_quantize_fp4(x: torch.Tensor, quantized: torch.Tensor, scales: torch.Ten
     dev = quantized.device
     _same_device(dev, x, scales, factor)
     st = _on_device(dev, lib().moe_quantize_fp4, x.data_ptr(), _VALUE_DTYPES[x.dtype], x_ld,
-                    _ptr(factor), quantized.data_ptr(), _row_bytes(quantized), scales.data_ptr(),
-                    _row_bytes(scales), fmt, rows, k, _stream_ptr(stream, dev))
+                    _ptr(factor), quantized.data_ptr(), q_ld, scales.data_ptr(), s_ld, fmt, rows,
+                    k, _stream_ptr(stream, dev))
     check(st, "moe_quantize_fp4")
     return quantized, scales
 
@@ -116,15 +110,15 @@ def moe_dequantize_fp4(quantized: torch.Tensor, scales: torch.Tensor, output: to
     """What 4-bit values stand for: ``output = value * scale`` (exact in FP32; in BF16 too,
     but for values beyond its range).  output: BF16 or FP32 [rows, k], unit last-dim
     stride, row stride a multiple of 8.  Returns ``output``."""
-    fmt, k = _packed(quantized, scales, "quantized", 2)
+    fmt, k, q_ld, s_ld = _packed(quantized, scales, "quantized", 2)
     out_ld = _output_rows(output, "output")
     rows = quantized.shape[0]
     _req(output.shape == (rows, k), "output and quantized disagree on the rows or on k")
     _int32(k)
     dev = output.device
     _same_device(dev, quantized, scales)
-    st = _on_device(dev, lib().moe_dequantize_fp4, quantized.data_ptr(), _row_bytes(quantized),
-                    scales.data_ptr(), _row_bytes(scales), fmt, output.data_ptr(),
+    st = _on_device(dev, lib().moe_dequantize_fp4, quantized.data_ptr(), q_ld,
+                    scales.data_ptr(), s_ld, fmt, output.data_ptr(),
                     _VALUE_DTYPES[output.dtype], out_ld, rows, k, _stream_ptr(stream, dev))
     check(st, "moe_dequantize_fp4")
     return output
@@ -145,8 +139,8 @@ def moe_grouped_gemm_fp4(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.
     expert only): every row belongs to the one matrix.  row_index: int32 [rows]; an entry
     outside x selects a row of zeros.  Returns ``output``.
     """
-    fmt, k = _packed(weight, weight_scales, "weight", 3)
-    x_fmt, x_k = _packed(x, x_scales, "x", 2)
+    fmt, k, w_ld, ws_ld = _packed(weight, weight_scales, "weight", 3)
+    x_fmt, x_k, x_ld, xs_ld = _packed(x, x_scales, "x", 2)
     _req(x_fmt == fmt, "x and weight must have one format")
     E, n = weight.shape[:2]
     out_ld = _output_rows(output, "output")
@@ -164,11 +158,10 @@ def moe_grouped_gemm_fp4(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.
                             factor.is_contiguous()), "factor must be contiguous FP32 [experts]")
     dev = output.device
     _same_device(dev, x, x_scales, weight, weight_scales, expert_offsets, row_index, factor)
-    st = _on_device(dev, lib().moe_grouped_gemm_fp4, x.data_ptr(), x.shape[0], _row_bytes(x),
-                    x_scales.data_ptr(), _row_bytes(x_scales), _ptr(row_index), weight.data_ptr(),
-                    _row_bytes(weight), weight.stride(0), weight_scales.data_ptr(),
-                    _row_bytes(weight_scales), weight_scales.stride(0), fmt, _ptr(factor),
-                    _ptr(expert_offsets), output.data_ptr(), _VALUE_DTYPES[output.dtype], out_ld,
-                    rows, E, n, k, _stream_ptr(stream, dev))
+    st = _on_device(dev, lib().moe_grouped_gemm_fp4, x.data_ptr(), x.shape[0], x_ld,
+                    x_scales.data_ptr(), xs_ld, _ptr(row_index), weight.data_ptr(), w_ld,
+                    weight.stride(0), weight_scales.data_ptr(), ws_ld, weight_scales.stride(0),
+                    fmt, _ptr(factor), _ptr(expert_offsets), output.data_ptr(),
+                    _VALUE_DTYPES[output.dtype], out_ld, rows, E, n, k, _stream_ptr(stream, dev))
     check(st, "moe_grouped_gemm_fp4")
     return output

@@ -312,6 +312,21 @@ def test_scales_far_apart(cuda_lib, fmt, rows):
     check(s, product(cuda_lib, s, FP32))
 
 
+@pytest.mark.parametrize("rows", [3, 400])
+@pytest.mark.parametrize("fmt,of_weight,of_x", [
+    (MX, 0, 254), (MX, 254, 0), (MX, 0, 127), (MX, 1, 126), (MX, 64, 64), (MX, 250, 20),
+    (MX, 127, 127), (NV, 0x01, 0x7E), (NV, 0x7E, 0x7E), (NV, 0x01, 0x01), (NV, 0, 0x38),
+    (NV, 0xB8, 0x38), (NV, 0xB8, 0x81)])
+def test_ends_of_the_scales(cuda_lib, rows, fmt, of_weight, of_x):
+    """The smallest and largest scales, and E4M3 with the bit that is not used: sums of 256
+    products of one pair of scales are exact."""
+    s = layer([rows], 64, 256, fmt, seed=1)
+    s["ws"].view(U8).fill_(of_weight)
+    s["xs"].view(U8).fill_(of_x)
+    out = product(cuda_lib, s, FP32)
+    assert torch.equal(out.double(), exact(s)[0])
+
+
 @pytest.mark.parametrize("fmt", [MX, NV])
 @pytest.mark.parametrize("rows", [3, 40, 400])
 def test_one_nan_block(cuda_lib, fmt, rows):
