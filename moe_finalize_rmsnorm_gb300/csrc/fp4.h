@@ -27,6 +27,7 @@ struct Fp4RowsArgs {
     int64_t rows;
     int k;
     uint32_t magic;        // 2^32 / (chunks of a row), for few chunks (set by the launch)
+    bool wide;             // x, or the output, in accesses of 32 bytes (set by the launch)
     bool programmatic;
 };
 

@@ -63,16 +63,16 @@ def _packed(q: torch.Tensor, scales: torch.Tensor, name: str, dims: int
     return f[0], 2 * width, width, (groups + 15) // 16 * 16  # one row: no stride to keep
 
 
-def _whole_pieces(scales: torch.Tensor, name: str) -> None:
+def _whole_pieces(scales: torch.Tensor, name: str, behind: int) -> None:
     """The product reads scales in 16-byte pieces: the last row's has to lie in its memory."""
-    shape = scales.shape
-    if shape[-1] % 16 != 0 and scales.numel():
-        end = scales.storage_offset() + 1 + -shape[-1] % 16
-        for n, st in zip(shape, scales.stride()):
-            end += (n - 1) * st
-        if end > scales.untyped_storage().nbytes():
-            raise ValueError(f"{name}'s last row must be followed by bytes up to a multiple of 16 "
-                             "(as moe_fp4_empty allocates)")
+    if scales.numel() == 0:
+        return
+    end = scales.storage_offset() + 1 + behind
+    for n, st in zip(scales.shape, scales.stride()):
+        end += (n - 1) * st
+    if end > scales.untyped_storage().nbytes():
+        raise ValueError(f"{name}'s last row must be followed by bytes up to a multiple of 16 "
+                         "(as moe_fp4_empty allocates)")
 
 
 def moe_quantize_fp4(x: torch.Tensor, quantized: torch.Tensor, scales: torch.Tensor, *,
@@ -142,23 +142,26 @@ def moe_grouped_gemm_fp4(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.
     fmt, k, w_ld, ws_ld = _packed(weight, weight_scales, "weight", 3)
     x_fmt, x_k, x_ld, xs_ld = _packed(x, x_scales, "x", 2)
     _req(x_fmt == fmt, "x and weight must have one format")
-    E, n = weight.shape[:2]
+    E, n, _ = weight.shape
     out_ld = _output_rows(output, "output")
-    rows = output.shape[0]
-    _req(x_k == k and output.shape[1] == n, "shapes disagree on n or k")
+    rows, out_n = output.shape
+    x_rows = x.shape[0]
+    _req(x_k == k and out_n == n, "shapes disagree on n or k")
     _int32(E | n | k)
     if expert_offsets is None:
         _req(E == 1, "expert_offsets may be None with one expert only")
     else:
         _index(expert_offsets, "expert_offsets", (E + 1,))
-    _row_index(row_index, rows, x.shape[0])
-    _whole_pieces(x_scales, "x")
-    _whole_pieces(weight_scales, "weight")
+    _row_index(row_index, rows, x_rows)
+    behind = -(k // (32 if fmt == MF_FP4_MX else 16)) % 16  # bytes up to a whole piece
+    if behind:
+        _whole_pieces(x_scales, "x", behind)
+        _whole_pieces(weight_scales, "weight", behind)
     _req(factor is None or (factor.dtype == torch.float32 and factor.shape == (E,) and
                             factor.is_contiguous()), "factor must be contiguous FP32 [experts]")
     dev = output.device
     _same_device(dev, x, x_scales, weight, weight_scales, expert_offsets, row_index, factor)
-    st = _on_device(dev, lib().moe_grouped_gemm_fp4, x.data_ptr(), x.shape[0], x_ld,
+    st = _on_device(dev, lib().moe_grouped_gemm_fp4, x.data_ptr(), x_rows, x_ld,
                     x_scales.data_ptr(), xs_ld, _ptr(row_index), weight.data_ptr(), w_ld,
                     weight.stride(0), weight_scales.data_ptr(), ws_ld, weight_scales.stride(0),
                     fmt, _ptr(factor), _ptr(expert_offsets), output.data_ptr(),
