@@ -252,7 +252,7 @@ cudaError_t launch_backward(const CombineArgs &a, cudaStream_t s) {
 }
 
 // How many threads take a token: a warp where rows are short (8000 x 8 rows of 512: 25 us,
-// 40 with 128 threads; 20000 x 4 of 1024 70 and 90), 512 threads where there is a token to
+// 40 with 128 threads; 20000 x 4 of 1024 58 and, with eight slots, 70 and 90), 512 threads where there is a token to
 // an SM at most (64 x 8 rows of 7168: 5.1 us, 6.1 with 128; 600 x 8 of 4096 19.6 and 15.4).
 template <bool DY_FP32, bool ROWS_FP32, int SLOTS>
 cudaError_t launch_team(const CombineArgs &a, cudaStream_t s) {

@@ -22,13 +22,12 @@
 // first, and says so, before the rest.
 //
 // What bounds it (GB300, 4096 x 4096, short runs): up to some 200 rows an expert the
-// weights' bytes (32 experts of 64 rows 52 us, E8M0; 45 at the copy bandwidth).  Beyond,
+// weights' bytes (32 experts of 64 rows 53 us, E8M0; 45 at the copy bandwidth).  Beyond,
 // shared memory, which moves 128 bytes a cycle: a step of 256 rows brings 32 KB in and
 // reads it once more (512 cycles, as many as its products take), and its scales, read
 // through L1, written as blocks and read again, take 192 (E4M3) or 96.  512 rows an expert
-// run at 5.7 (E8M0) and 4.8 (E4M3) PFLOP/s, gathered 5.4 and 4.6; without the scales' reads
-// they would at 6.1.  Tiles of 192 rows, which the scales leave whole accumulators for: 5.2
-// and 4.3.
+// run at 5.6 (E8M0) and 5.4 (E4M3) PFLOP/s, gathered 5.4 and 4.9.  Tiles of 192 rows, for
+// which the scales leave whole accumulators, ran at 5.2 and 4.3 when 256 did at 5.7 and 4.8.
 #include "experts.cuh"
 #include "experts.h"
 #include "fp4.cuh"

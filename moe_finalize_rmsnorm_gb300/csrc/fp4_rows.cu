@@ -1,5 +1,4 @@
-// The 4-bit floating point product for few rows per expert (decode): bound by the
-// weights' bytes.
+// The 4-bit floating point product for few rows of small weights (decode): latency.
 //
 // A warp takes 32 output columns and up to 8 rows, streams 256 summed values of its
 // columns a stage (128 bytes a column, one tensor-map copy) with their scales and the
@@ -15,6 +14,11 @@
 //
 // Where there are few column blocks, several warps split one block's summed values and
 // add up through shared memory, in warp order.
+//
+// Measured (GB300, device time): one row through 4096 x 4096 6.1 us (E8M0) and 5.4 (E4M3),
+// 8.8 by the tensor-core kernel; through four matrices of 512 x 2048 4.4 and 4.0 (6.7).  With
+// more weights the instructions count, 25 for a lane's eight weights in ten warps an SM:
+// eight of 4096 x 4096 31 us, 16 by the tensor-core kernel.
 #include "few_rows.cuh"
 #include "fp4.cuh"
 #include "tensor_map.h"
