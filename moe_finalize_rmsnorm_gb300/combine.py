@@ -29,23 +29,42 @@ import torch
 
 from ._abi import MF_DTYPE_BF16, MF_DTYPE_FP32, MF_DTYPE_PACKED_TOPK, check, lib
 from ._binding import _on_device, _req, _stream_ptr
-from .experts import _VALUE_DTYPES, _index, _int32, _output_rows, _ptr, _rows, _same_device
+from .experts import _VALUE_DTYPES, _int32, _ptr, _same_device
 
 _WEIGHT_DTYPES = {torch.bfloat16: MF_DTYPE_BF16, torch.float32: MF_DTYPE_FP32,
                   torch.int32: MF_DTYPE_PACKED_TOPK}
 
 
+def _matrix(t: torch.Tensor, name: str, written: bool = False) -> tuple[int, int, int, int]:
+    """Check a 2-D row-major BF16 or FP32 operand; returns (rows, columns, row stride in
+    elements, dtype code)."""
+    shape, code = t.shape, _VALUE_DTYPES.get(t.dtype)
+    if len(shape) == 2 and code is not None:
+        rows, width = shape
+        ld, unit = t.stride()
+        if unit == 1 or width <= 1:
+            if rows <= 1:
+                return rows, width, width, code  # one row: no stride to keep
+            if written and ld < width:
+                raise ValueError(f"{name}'s rows must not overlap")
+            return rows, width, ld, code
+    raise ValueError(f"{name} must be a 2-D BF16 or FP32 tensor with unit last-dim stride")
+
+
 def _slots(expanded_idx: torch.Tensor, expert_weights) -> tuple[int, int, int]:
     """(tokens, top_k, the weights' dtype code) of a map and its weights."""
-    _req(expanded_idx.dim() == 2, "expanded_idx must be 2-D")
-    T, K = expanded_idx.shape
-    _index(expanded_idx, "expanded_idx", (T, K))
+    shape = expanded_idx.shape
+    if len(shape) != 2 or expanded_idx.dtype != torch.int32 or not expanded_idx.is_contiguous():
+        raise ValueError("expanded_idx must be a contiguous 2-D int32 tensor")
+    T, K = shape
     if expert_weights is None:
         return T, K, MF_DTYPE_FP32
     w = expert_weights
-    _req(w.dtype in _WEIGHT_DTYPES and w.shape == (T, K) and w.is_contiguous(),
-         "expert_weights must be contiguous BF16, FP32 or packed int32 with the index map's shape")
-    return T, K, _WEIGHT_DTYPES[w.dtype]
+    code = _WEIGHT_DTYPES.get(w.dtype)
+    if code is None or w.shape != shape or not w.is_contiguous():
+        raise ValueError("expert_weights must be contiguous BF16, FP32 or packed int32 with the "
+                         "index map's shape")
+    return T, K, code
 
 
 def moe_dispatch(x: torch.Tensor, expanded_idx: torch.Tensor, output: torch.Tensor, *,
@@ -60,18 +79,17 @@ def moe_dispatch(x: torch.Tensor, expanded_idx: torch.Tensor, output: torch.Tens
     named twice.  expert_weights: BF16, FP32 or packed int32 routing words.  Rows that no
     entry names are left as they were.  Returns ``output``.
     """
-    x_ld = _rows(x, "x", _VALUE_DTYPES)
-    out_ld = _output_rows(output, "output")
+    x_rows, x_width, x_ld, x_dtype = _matrix(x, "x")
+    rows, hidden, out_ld, out_dtype = _matrix(output, "output", written=True)
     T, K, wdt = _slots(expanded_idx, expert_weights)
-    rows, hidden = output.shape
-    _req(x.shape == (T, hidden), "x, output and the map disagree on num_tokens or hidden")
+    _req(x_rows == T and x_width == hidden,
+         "x, output and the map disagree on num_tokens or hidden")
     _int32(hidden | K)
     dev = output.device
     _same_device(dev, x, expanded_idx, expert_weights)
-    st = _on_device(dev, lib().moe_dispatch, x.data_ptr(), _VALUE_DTYPES[x.dtype], x_ld,
-                    _ptr(expert_weights), wdt, expanded_idx.data_ptr(), output.data_ptr(),
-                    _VALUE_DTYPES[output.dtype], rows, out_ld, T, hidden, K,
-                    _stream_ptr(stream, dev))
+    st = _on_device(dev, lib().moe_dispatch, x.data_ptr(), x_dtype, x_ld, _ptr(expert_weights),
+                    wdt, expanded_idx.data_ptr(), output.data_ptr(), out_dtype, rows, out_ld, T,
+                    hidden, K, _stream_ptr(stream, dev))
     check(st, "moe_dispatch")
     return output
 
@@ -88,21 +106,18 @@ def moe_combine(permuted: torch.Tensor, expert_weights: torch.Tensor, expanded_i
     expanded_idx: int32 of the same shape; an entry outside the rows contributes zero.
     Returns ``output``.
     """
-    ld = _rows(permuted, "permuted", _VALUE_DTYPES)
-    out_ld = _output_rows(output, "output")
+    rows, width, ld, dtype = _matrix(permuted, "permuted")
+    out_rows, hidden, out_ld, out_dtype = _matrix(output, "output", written=True)
     _req(expert_weights is not None, "expert_weights are required (moe_permuted_row_sum has none)")
     T, K, wdt = _slots(expanded_idx, expert_weights)
-    rows, width = permuted.shape
-    hidden = output.shape[1]
-    _req(output.shape[0] == T, "output and the map disagree on num_tokens")
+    _req(out_rows == T, "output and the map disagree on num_tokens")
     _req(width >= hidden, "permuted has fewer columns than output")
     _int32(hidden | K)
     dev = output.device
     _same_device(dev, permuted, expert_weights, expanded_idx)
-    st = _on_device(dev, lib().moe_combine, permuted.data_ptr(), _VALUE_DTYPES[permuted.dtype],
-                    rows, ld, expert_weights.data_ptr(), wdt, expanded_idx.data_ptr(),
-                    output.data_ptr(), _VALUE_DTYPES[output.dtype], out_ld, T, hidden, K,
-                    _stream_ptr(stream, dev))
+    st = _on_device(dev, lib().moe_combine, permuted.data_ptr(), dtype, rows, ld,
+                    expert_weights.data_ptr(), wdt, expanded_idx.data_ptr(), output.data_ptr(),
+                    out_dtype, out_ld, T, hidden, K, _stream_ptr(stream, dev))
     check(st, "moe_combine")
     return output
 
@@ -124,21 +139,19 @@ def moe_combine_backward(grad_output: torch.Tensor, permuted: torch.Tensor | Non
     rows.  Rows that no entry names are left as they were; where grad_permuted is wanted no
     row may be named twice.  Returns ``(grad_permuted, grad_weights)``.
     """
-    go_ld = _rows(grad_output, "grad_output", _VALUE_DTYPES)
+    go_rows, hidden, go_ld, go_dtype = _matrix(grad_output, "grad_output")
     _req(grad_permuted is not None or grad_weights is not None, "no gradient is wanted")
     _req(grad_weights is None or permuted is not None, "grad_weights needs permuted")
     _req(grad_permuted is None or expert_weights is not None, "grad_permuted needs expert_weights")
     T, K, wdt = _slots(expanded_idx, expert_weights)
-    hidden = grad_output.shape[1]
-    _req(grad_output.shape[0] == T, "grad_output and the map disagree on num_tokens")
+    _req(go_rows == T, "grad_output and the map disagree on num_tokens")
     like = permuted if permuted is not None else grad_permuted
-    ld = _rows(like, "permuted", _VALUE_DTYPES)
-    rows = like.shape[0]
-    _req(like.shape[1] == hidden, "shapes disagree on hidden")
+    rows, width, ld, dtype = _matrix(like, "permuted")
+    _req(width == hidden, "shapes disagree on hidden")
     gp_ld = hidden
     if grad_permuted is not None:
-        gp_ld = _output_rows(grad_permuted, "grad_permuted")
-        _req(grad_permuted.shape == like.shape and grad_permuted.dtype == like.dtype,
+        gp_rows, gp_width, gp_ld, gp_dtype = _matrix(grad_permuted, "grad_permuted", written=True)
+        _req(gp_rows == rows and gp_width == width and gp_dtype == dtype,
              "grad_permuted must have permuted's shape and dtype")
     gw_dtype = MF_DTYPE_FP32
     if grad_weights is not None:
@@ -149,9 +162,8 @@ def moe_combine_backward(grad_output: torch.Tensor, permuted: torch.Tensor | Non
     _int32(hidden | K)
     dev = grad_output.device
     _same_device(dev, permuted, expert_weights, expanded_idx, grad_permuted, grad_weights)
-    st = _on_device(dev, lib().moe_combine_backward, grad_output.data_ptr(),
-                    _VALUE_DTYPES[grad_output.dtype], go_ld, _ptr(permuted),
-                    _VALUE_DTYPES[like.dtype], rows, ld, _ptr(expert_weights), wdt,
+    st = _on_device(dev, lib().moe_combine_backward, grad_output.data_ptr(), go_dtype, go_ld,
+                    _ptr(permuted), dtype, rows, ld, _ptr(expert_weights), wdt,
                     expanded_idx.data_ptr(), _ptr(grad_permuted), gp_ld, _ptr(grad_weights),
                     gw_dtype, T, hidden, K, _stream_ptr(stream, dev))
     check(st, "moe_combine_backward")

@@ -23,7 +23,8 @@ import torch
 
 from ._abi import MF_FP4_MX, MF_FP4_NV, check, lib
 from ._binding import _on_device, _req, _stream_ptr
-from .experts import _VALUE_DTYPES, _index, _int32, _output_rows, _ptr, _row_index, _rows, _same_device
+from .combine import _matrix
+from .experts import _index, _int32, _ptr, _row_index, _same_device
 
 _FORMATS = {torch.float8_e8m0fnu: (MF_FP4_MX, 32), torch.float8_e4m3fn: (MF_FP4_NV, 16)}
 
@@ -88,17 +89,17 @@ def moe_quantize_fp4(x: torch.Tensor, quantized: torch.Tensor, scales: torch.Ten
     x: BF16 or FP32 [rows, k], unit last-dim stride, row stride a multiple of 8, k a
     multiple of 32; factor: FP32 tensor of one element.  Returns ``(quantized, scales)``.
     """
-    x_ld = _rows(x, "x", _VALUE_DTYPES)
+    rows, width, x_ld, x_dtype = _matrix(x, "x")
     fmt, k, q_ld, s_ld = _packed(quantized, scales, "quantized", 2)
     _req(2 * q_ld >= k and s_ld * 32 >= k, "the rows of quantized and scales must not overlap")
-    rows = quantized.shape[0]
-    _req(x.shape == (rows, k), "x and quantized disagree on the rows or on k")
+    _req(quantized.shape[0] == rows and k == width,
+         "x and quantized disagree on the rows or on k")
     _req(factor is None or (factor.dtype == torch.float32 and factor.numel() == 1),
          "factor must be an FP32 tensor of one element")
     _int32(k)
     dev = quantized.device
     _same_device(dev, x, scales, factor)
-    st = _on_device(dev, lib().moe_quantize_fp4, x.data_ptr(), _VALUE_DTYPES[x.dtype], x_ld,
+    st = _on_device(dev, lib().moe_quantize_fp4, x.data_ptr(), x_dtype, x_ld,
                     _ptr(factor), quantized.data_ptr(), q_ld, scales.data_ptr(), s_ld, fmt, rows,
                     k, _stream_ptr(stream, dev))
     check(st, "moe_quantize_fp4")
@@ -111,15 +112,15 @@ def moe_dequantize_fp4(quantized: torch.Tensor, scales: torch.Tensor, output: to
     but for values beyond its range).  output: BF16 or FP32 [rows, k], unit last-dim
     stride, row stride a multiple of 8.  Returns ``output``."""
     fmt, k, q_ld, s_ld = _packed(quantized, scales, "quantized", 2)
-    out_ld = _output_rows(output, "output")
-    rows = quantized.shape[0]
-    _req(output.shape == (rows, k), "output and quantized disagree on the rows or on k")
+    rows, width, out_ld, out_dtype = _matrix(output, "output", written=True)
+    _req(quantized.shape[0] == rows and k == width,
+         "output and quantized disagree on the rows or on k")
     _int32(k)
     dev = output.device
     _same_device(dev, quantized, scales)
     st = _on_device(dev, lib().moe_dequantize_fp4, quantized.data_ptr(), q_ld,
-                    scales.data_ptr(), s_ld, fmt, output.data_ptr(),
-                    _VALUE_DTYPES[output.dtype], out_ld, rows, k, _stream_ptr(stream, dev))
+                    scales.data_ptr(), s_ld, fmt, output.data_ptr(), out_dtype, out_ld, rows, k,
+                    _stream_ptr(stream, dev))
     check(st, "moe_dequantize_fp4")
     return output
 
@@ -143,8 +144,7 @@ def moe_grouped_gemm_fp4(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.
     x_fmt, x_k, x_ld, xs_ld = _packed(x, x_scales, "x", 2)
     _req(x_fmt == fmt, "x and weight must have one format")
     E, n, _ = weight.shape
-    out_ld = _output_rows(output, "output")
-    rows, out_n = output.shape
+    rows, out_n, out_ld, out_dtype = _matrix(output, "output", written=True)
     x_rows = x.shape[0]
     _req(x_k == k and out_n == n, "shapes disagree on n or k")
     _int32(E | n | k)
@@ -165,6 +165,6 @@ def moe_grouped_gemm_fp4(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.
                     x_scales.data_ptr(), xs_ld, _ptr(row_index), weight.data_ptr(), w_ld,
                     weight.stride(0), weight_scales.data_ptr(), ws_ld, weight_scales.stride(0),
                     fmt, _ptr(factor), _ptr(expert_offsets), output.data_ptr(),
-                    _VALUE_DTYPES[output.dtype], out_ld, rows, E, n, k, _stream_ptr(stream, dev))
+                    out_dtype, out_ld, rows, E, n, k, _stream_ptr(stream, dev))
     check(st, "moe_grouped_gemm_fp4")
     return output
