@@ -666,7 +666,8 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                         const int block = step * 3 * Sc::kWords +
                                           (b == 0 ? word : Sc::kWords + 2 * word + b - 1);
                         const auto w = [&](const uint4 &v) {
-                            return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+                            const uint32_t x = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+                            return FORMAT == kNv ? x & 0x7f7f7f7fu : x;  // without the signs
                         };
                         sts_16(to + block * kBlockBytes, make_uint4(w(q[4 * b]), w(q[4 * b + 1]),
                                                                     w(q[4 * b + 2]), w(q[4 * b + 3])));

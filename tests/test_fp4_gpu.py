@@ -327,6 +327,22 @@ def test_ends_of_the_scales(cuda_lib, rows, fmt, of_weight, of_x):
     assert torch.equal(out.double(), exact(s)[0])
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("rows,gather", [(3, False), (400, False), (400, True)])
+def test_the_bit_that_is_not_used(cuda_lib, rows, gather, dtype):
+    """E4M3 scales of any code, NaN among them: with bit 7 set the results are the same."""
+    s = layer([rows, rows], 72, 1184, NV, gather=gather, seed=rows, scale_range=(0, 127))
+    s["xs"].view(U8)[1, 3] = 127
+    s["ws"].view(U8)[1, 5, 2] = 127
+    want = product(cuda_lib, s, dtype)
+    assert want.isnan().any() and not want.isnan().all()
+    for scales in (s["xs"], s["ws"]):
+        scales.view(U8).bitwise_or_(torch.randint(0, 2, scales.shape, device="cuda", dtype=U8) * 128)
+    s["xs"].view(U8)[1, 3] = 255
+    s["ws"].view(U8)[1, 5, 2] = 255
+    assert torch.equal(product(cuda_lib, s, dtype).nan_to_num(123.0), want.nan_to_num(123.0))
+
+
 @pytest.mark.parametrize("fmt", [MX, NV])
 @pytest.mark.parametrize("rows", [3, 40, 400])
 def test_one_nan_block(cuda_lib, fmt, rows):
