@@ -169,6 +169,41 @@ def test_dequantize(cuda_lib, fmt, rows, k):
         assert out[:, k:].isnan().all()
 
 
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_there_and_back_on_streams_and_in_a_graph(cuda_lib, fmt):
+    """Two streams at once with buffers of their own, and a replay with other rows."""
+    rows, k = 133, 1056
+    x = torch.randn((rows, k), device="cuda").bfloat16()
+    factor = torch.full((1,), 0.75, device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for st in streams * 2:
+        q = cuda_lib.moe_fp4_empty((rows,), k, fmt, stream=st)
+        with torch.cuda.stream(st):
+            out = torch.empty((rows, k), device="cuda")
+        cuda_lib.moe_quantize_fp4(x, *q, factor=factor, stream=st)
+        cuda_lib.moe_dequantize_fp4(*q, out, stream=st)
+        got.append((q, out))
+    torch.cuda.synchronize()
+    codes, byte = fp4.quantize(x, fmt, factor)
+    for q, out in got:
+        assert torch.equal(q[0], fp4.pack(codes)) and torch.equal(q[1].view(U8), byte)
+        assert torch.equal(out.double(), fp4.values(*q))
+    q, out = got[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cuda_lib.moe_quantize_fp4(x, *q, factor=factor)
+        cuda_lib.moe_dequantize_fp4(*q, out)
+    x.copy_(torch.randn((rows, k), device="cuda"))
+    factor.fill_(-3.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    codes, byte = fp4.quantize(x, fmt, factor)
+    assert torch.equal(q[0], fp4.pack(codes)) and torch.equal(q[1].view(U8), byte)
+    assert torch.equal(out.double(), fp4.values(*q))
+
+
 # ---------------------------------------------------------------------------
 # the product
 
@@ -375,6 +410,53 @@ def test_offsets_that_do_not_fit(cuda_lib, rows):
     s["sizes"] = [0, 0, 2]
     out = product(cuda_lib, s, FP32)
     check(s, out)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("rows", [7, 40])
+def test_offsets_beyond_32_bits(cuda_lib, rows, fmt):
+    """Rows so far apart that every operand's bytes pass 2^32 (the few rows' kernel and
+    the other)."""
+    E, n, k = 2, 72, 288
+
+    def far(shape, width, dtype, total=2 ** 33):
+        of = 1
+        for d in shape:
+            of *= d
+        whole = torch.empty((*shape, total // of // 16 * 16), dtype=dtype, device="cuda")
+        assert (of - 1) * whole.stride(-2) > 0.8 * total
+        return whole[..., :width]
+
+    s = layer([rows - 2, 2], n, k, fmt, seed=rows)
+    x = far((rows,), k, BF16, 2 ** 32)
+    x.copy_(torch.randn((rows, k), device="cuda"))
+    codes, byte = fp4.quantize(x, fmt, None)
+    for name, width in (("x", k // 2), ("xs", k // fp4.BLOCK[fmt])):
+        s[name] = far((rows,), width, U8)
+    s["xs"] = s["xs"].view(fmt)
+    cuda_lib.moe_quantize_fp4(x, s["x"], s["xs"])
+    assert torch.equal(s["x"], fp4.pack(codes)) and torch.equal(s["xs"].view(U8), byte)
+    del x
+    back = far((rows,), k, FP32, 2 ** 32)
+    cuda_lib.moe_dequantize_fp4(s["x"], s["xs"], back)
+    assert torch.equal(back.double(), fp4.values(s["x"], s["xs"]))
+    del back
+    for name in ("w", "ws"):
+        t = far((E, n), s[name].shape[-1], U8)
+        t.copy_(s[name].view(U8))
+        s[name] = t.view(s[name].dtype)
+    for dtype in (BF16, FP32):
+        out = far((rows,), n + 8, dtype, 2 ** 32).fill_(NAN)
+        cuda_lib.moe_grouped_gemm_fp4(s["x"], s["xs"], s["w"], s["ws"], s["off"], out[:, :n])
+        check(s, out)
+        del out
+    s["index"] = torch.arange(rows - 1, -1, -1, device="cuda").int()
+    out = far((rows,), n, FP32, 2 ** 32)
+    cuda_lib.moe_grouped_gemm_fp4(s["x"], s["xs"], s["w"], s["ws"], s["off"], out,
+                                  row_index=s["index"])
+    check(s, out)
+    del out, t, s
+    torch.cuda.empty_cache()
 
 
 @pytest.mark.parametrize("fmt", [MX, NV])
