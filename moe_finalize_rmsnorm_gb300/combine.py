@@ -44,7 +44,7 @@ def _matrix(t: torch.Tensor, name: str, written: bool = False) -> tuple[int, int
         ld, unit = t.stride()
         if unit == 1 or width <= 1:
             if rows <= 1:
-                return rows, width, width, code  # one row: no stride to keep
+                return rows, width, (width + 7) // 8 * 8, code  # one row: no stride to keep
             if written and ld < width:
                 raise ValueError(f"{name}'s rows must not overlap")
             return rows, width, ld, code

@@ -350,3 +350,13 @@ def test_offsets_beyond_32_bits(cuda_lib):
     gw = torch.empty((16, 4), device="cuda")
     mf.moe_combine_backward(s["x"], big, None, s["idx"], None, gw)
     check_grad_weights(s, gw)
+
+
+def test_one_wide_row(cuda_lib):
+    """A single row of more columns than the tokens', not a multiple of 8."""
+    rows = torch.randn((1, 76), device="cuda").bfloat16()
+    idx = torch.tensor([[0, -1], [1, 0]], dtype=torch.int32, device="cuda")
+    w = torch.rand((2, 2), device="cuda")
+    out = torch.empty((2, 64), device="cuda")
+    cuda_lib.moe_combine(rows, w, idx, out)
+    assert torch.equal(out, torch.stack([w[0, 0], w[1, 1]]).unsqueeze(1) * rows[:, :64].float())

@@ -151,3 +151,13 @@ I32, F32 = torch.int32, torch.float32
 def test_binding_refuses(call):
     with pytest.raises(ValueError):
         call()
+
+
+def test_one_row_keeps_no_stride():
+    """A single row's columns may end anywhere: the stride that the kernels get is a multiple
+    of 8 that covers them."""
+    from moe_finalize_rmsnorm_gb300.combine import _matrix
+    for width, ld in ((64, 64), (60, 64), (1, 8), (68, 72)):
+        whole = torch.empty((1, 100), dtype=torch.bfloat16)
+        assert _matrix(whole[:, :width], "t") == (1, width, ld, 0)
+        assert _matrix(torch.empty((1, width)).expand(1, width), "t", written=True)[2] == ld
