@@ -178,15 +178,25 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
     return remote;
 }
 
-// Arrive on a barrier of either CTA of a pair, for work that tcgen05 fences order: reads
-// of TMEM (waited for, then tcgen05.fence::before_thread_sync) before the products that
-// overwrite it (behind fence::after_thread_sync).  So the arrival itself may be relaxed;
-// its scope has to hold both CTAs.  A release at cluster scope would also wait for the
-// thread's global stores to land (weights' gradient of 128 rows an expert 702 against
-// 586 us, in FP32 870 against 740).
+// Arrive on a barrier of either CTA of a pair without handing on any ordinary store: for
+// work that tcgen05 fences order, reads of TMEM (waited for, then
+// tcgen05.fence::before_thread_sync) before the products that overwrite it (behind
+// fence::after_thread_sync); or where there is nothing to hand on, as for copies whose bytes
+// the barrier counts itself.  Then the arrival may be relaxed; its scope has to hold both
+// CTAs.  A release at cluster scope would also wait for the thread's global stores to land
+// (weights' gradient of 128 rows an expert 702 against 586 us, in FP32 870 against 740).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
                  : "memory");
+}
+
+// The same, handing on what is stored in this CTA's shared memory (by this thread, or known
+// to it through a barrier): whoever waits for the arrival in either CTA sees it.  The release
+// is restricted to shared memory; a whole one waits for global accesses too (see
+// fp4_gemm.cu for what that costs).
+__device__ __forceinline__ void mbar_arrive_cluster_release_smem(uint32_t remote_bar) {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    mbar_arrive_cluster(remote_bar);
 }
 
 __device__ __forceinline__ void cp_async_commit() {

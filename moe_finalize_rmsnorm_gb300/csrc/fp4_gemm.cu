@@ -673,12 +673,16 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                                                                     w(q[4 * b + 2]), w(q[4 * b + 3])));
                     }
                 }
-                // The copies to TMEM read this SM's shared memory through the asynchronous
-                // proxy, issued behind the arrival; so the arrival may be relaxed (a release at
-                // cluster scope takes 0.9 us).
+                // The copies to TMEM read this shared memory through the asynchronous proxy,
+                // issued by a warp that may be in the other CTA.  So every lane's stores are fenced
+                // towards that proxy, gathered by the warp's barrier and released with the
+                // arrival, at the pair's scope but for shared memory alone.  A whole release takes
+                // some 1 us (512 rows by 32 experts in order, E8M0 and E4M3: 98 and 116 us, gathered
+                // 108 and 124; by an idle warp of CTA 1 that passes its teams' arrivals on 98 and
+                // 110, 104 and 116; so 97 and 101, 103 and 113).
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(scale_full_at + 8 * team);
+                if (lane == 0) mbar_arrive_cluster_release_smem(scale_full_at + 8 * team);
                 if (g + 2 < all) read_group(g + 2);
             }
             // the last group's copies are done, before this CTA may leave
