@@ -400,8 +400,9 @@ mf_status moe_combine(const void *permuted, mf_dtype permuted_dtype, int64_t row
  *   grad_weights     device, BF16 or FP32 [num_tokens, top_k] contiguous, aligned to
  *                    its elements, or NULL: not wanted.
  *   The rest, and the errors, as for moe_dispatch, and MF_ERR_INVALID (neither
- *   gradient wanted).  Outputs may not overlap inputs or each other
- *   (MF_ERR_ALIGN).  Zero tokens: MF_OK, nothing launched.
+ *   gradient wanted, of some rows).  Outputs may not overlap inputs or each other
+ *   (MF_ERR_ALIGN).  Zero tokens, or zero rows and no grad_weights: MF_OK, nothing
+ *   launched; without tokens, or without rows, a NULL gradient may be an empty one.
  */
 mf_status moe_combine_backward(const void *grad_output, mf_dtype grad_output_dtype,
                                int64_t grad_output_stride, const void *permuted,

@@ -140,7 +140,6 @@ mf_status moe_combine_backward(const void *grad_output, mf_dtype grad_output_dty
                                int32_t top_k, mf_stream_t stream) {
     mf_status st = check_sizes(num_tokens, rows, hidden, top_k);
     if (st != MF_OK) return st;
-    if (!grad_permuted && !grad_weights) return MF_ERR_INVALID;
     if (!mf::row_stride_ok(grad_output_stride, hidden) ||
         (grad_weights && !mf::row_stride_ok(row_stride, hidden)) ||
         (grad_permuted && !mf::row_stride_ok(grad_permuted_stride, hidden)))
@@ -150,6 +149,8 @@ mf_status moe_combine_backward(const void *grad_output, mf_dtype grad_output_dty
         (grad_weights && !mf::value_dtype(grad_weights_dtype)))
         return MF_ERR_DTYPE;
     if (num_tokens == 0) return MF_OK;
+    // (without rows a gradient of theirs may be a null pointer, as that of an empty tensor)
+    if (!grad_permuted && !grad_weights && rows > 0) return MF_ERR_INVALID;
     if (!grad_output || !expanded_idx_to_permuted_idx || (grad_permuted && !expert_weights) ||
         (grad_weights && rows > 0 && !permuted))
         return MF_ERR_NULL;
