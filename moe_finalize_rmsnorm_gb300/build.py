@@ -23,7 +23,7 @@ LIB = os.path.join(LIB_DIR, "libmoe_finalize.so")
 
 SOURCES = ["api.cu", "experts_api.cu", "tp_finalize.cu", "beam_finalize.cu", "permute.cu",
            "combine.cu", "combine_api.cu", "grouped_gemm.cu", "grouped_gemv.cu", "grouped_rows.cu",
-           "fp4_api.cu", "fp4_quantize.cu", "fp4_rows.cu", "fp4_gemm.cu"]
+           "tensor_map.cu", "fp4_api.cu", "fp4_quantize.cu", "fp4_rows.cu", "fp4_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
               "--expt-relaxed-constexpr", f"-I{INCLUDE}"]

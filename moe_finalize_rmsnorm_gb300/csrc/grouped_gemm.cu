@@ -614,12 +614,6 @@ __global__ void __launch_bounds__(Warps<CTAS, SUMS, GATHER>::kThreads, 1)
     }
 }
 
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeFn g_encode = nullptr;  // the driver's encoder, found once (prepare)
-
 // BF16 values, strides in elements, boxes of one step by `rows`.
 bool encode(CUtensorMap *m, const void *p, int rank, const cuuint64_t (&sizes)[3],
             const int64_t (&strides)[2], int rows) {
@@ -695,29 +689,6 @@ cudaError_t prepare_ctas() {
 }
 
 }  // namespace
-
-bool encode_map(CUtensorMap *m, CUtensorMapDataType type, const void *p, int rank,
-                const cuuint64_t (&sizes)[3], const cuuint64_t (&strides)[2], int columns,
-                int rows) {
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(columns), static_cast<cuuint32_t>(rows), 1};
-    const cuuint32_t ones[3] = {1, 1, 1};
-    return g_encode(m, type, rank, const_cast<void *>(p), sizes, strides, box, ones,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-cudaError_t find_encoder() {
-    if (g_encode) return cudaSuccess;
-    void *fn = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                                           cudaEnableDefault, &found);
-    if (e != cudaSuccess) return e;
-    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-    g_encode = reinterpret_cast<EncodeFn>(fn);
-    return cudaSuccess;
-}
 
 cudaError_t prepare_grouped_gemm(int *pairs) {
     cudaError_t e = find_encoder();

@@ -7,7 +7,8 @@
 
 namespace mf {
 
-// Find the driver's encoder (once, before the first map; not thread-safe by itself).
+// Find the driver's encoder, before the first map (from any thread; another look after one
+// that failed).
 cudaError_t find_encoder();
 
 // Map of a row-major tensor of `rank` 2 or 3: sizes fastest first, byte strides of
