@@ -614,6 +614,8 @@ mf_status moe_dequantize_fp4(const uint8_t *quantized, int64_t quantized_stride,
  *   x, weight, their scales and output 16-byte aligned.  Scales are read in whole
  *   16-byte pieces: the bytes behind a row's up to the next multiple of 16 belong to
  *   the buffer (the last row's, too), and have no effect.
+ *   The output may not overlap an input (MF_ERR_ALIGN; columns beside an input's in
+ *   rows of one stride do not).
  *
  * Errors: those of moe_grouped_gemm, and MF_ERR_INVALID (format; no expert_offsets
  * with more than one expert).  Zero rows: MF_OK, nothing launched.

@@ -27,4 +27,28 @@ inline bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_byt
     return p < q + static_cast<uintptr_t>(b_bytes) && q < p + static_cast<uintptr_t>(a_bytes);
 }
 
+// Rows of `width` bytes, `stride` bytes apart.
+struct ByteRows {
+    const void *p;
+    int64_t rows, stride, width;
+    int64_t extent() const {  // (2^31 rows may lie 2^36 bytes apart)
+        if (rows <= 0) return 0;
+        const __int128 e = static_cast<__int128>(rows - 1) * stride + width;
+        return e < INT64_MAX ? static_cast<int64_t>(e) : INT64_MAX;
+    }
+};
+
+// Whether two sets of rows share a byte.  Columns side by side in rows of one stride do not;
+// rows of different strides count as sharing what lies between their ends.
+inline bool overlap(const ByteRows &a, const ByteRows &b) {
+    if (!overlap(a.p, a.extent(), b.p, b.extent())) return false;
+    if (a.rows == 1 && b.rows == 1) return true;
+    const int64_t stride = a.rows > 1 ? a.stride : b.stride;
+    if (b.rows > 1 && b.stride != stride) return true;
+    const int64_t from = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p) -
+                                              reinterpret_cast<uintptr_t>(a.p));
+    const int64_t at = (from % stride + stride) % stride;  // b's columns, in a's rows
+    return at < a.width || at + b.width > stride;
+}
+
 }  // namespace mf

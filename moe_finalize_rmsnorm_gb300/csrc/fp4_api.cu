@@ -34,6 +34,15 @@ int64_t extent(int64_t rows, int64_t stride, int64_t width) {
     return rows > 0 ? (rows - 1) * stride + width : 0;
 }
 
+// Experts' matrices as rows of one stride, where the experts lie a multiple of it apart.
+mf::ByteRows matrices(const void *p, int64_t experts, int64_t expert_stride, int64_t n,
+                      int64_t row_stride, int64_t width) {
+    if (experts == 1) return {p, n, row_stride, width};
+    if (expert_stride % row_stride == 0)
+        return {p, (experts - 1) * (expert_stride / row_stride) + n, row_stride, width};
+    return {p, 1, 0, (experts - 1) * expert_stride + extent(n, row_stride, width)};
+}
+
 mf_status check_rows(mf_fp4_format format, int64_t rows, int32_t k, mf_dtype dtype,
                      int64_t row_stride, int64_t q_stride, int64_t s_stride) {
     if (!format_ok(format)) return MF_ERR_INVALID;
@@ -185,6 +194,20 @@ mf_status moe_grouped_gemm_fp4(const uint8_t *x, int64_t x_rows, int64_t x_strid
         !aligned(weight_scales, 16) || !aligned(output, 16) || !aligned(expert_offsets, 4) ||
         !aligned(row_index, 4) || !aligned(factor, 4))
         return MF_ERR_ALIGN;
+    const int value = output_dtype == MF_DTYPE_FP32 ? 4 : 2;
+    const mf::ByteRows out = {output, rows, output_stride * value, int64_t{n} * value};
+    const int64_t experts = num_experts;
+    const mf::ByteRows in[7] = {
+        {x, x_rows, x_stride, k / 2},
+        {x_scales, x_rows, x_scales_stride, groups},
+        matrices(weight, experts, weight_expert_stride, n, weight_row_stride, k / 2),
+        matrices(weight_scales, experts, weight_scales_expert_stride, n, weight_scales_row_stride,
+                 groups),
+        {row_index, row_index ? 1 : 0, 0, 4 * rows},
+        {factor, factor ? 1 : 0, 0, 4 * experts},
+        {expert_offsets, expert_offsets ? 1 : 0, 0, 4 * (experts + 1)}};
+    for (const mf::ByteRows &i : in)
+        if (mf::overlap(out, i)) return MF_ERR_ALIGN;
     const mf::DeviceInfo *d = nullptr;
     mf::Fp4GemmArgs a = {};
     const mf_status st = fp4_device(&d, &a.num_pairs);

@@ -135,7 +135,7 @@ def moe_grouped_gemm_fp4(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.
     rows left as they were.
 
     x: uint8 [x_rows, k / 2] and its scales; weight: uint8 [experts, n, k / 2] and its scales;
-    output: BF16 or FP32 [rows, n]; n a multiple of 8, k of 32.  factor: contiguous FP32
+    output: BF16 or FP32 [rows, n], not over an input; n a multiple of 8, k of 32.  factor: contiguous FP32
     [experts], or None.  expert_offsets: int32 [experts + 1], ascending, or None (one
     expert only): every row belongs to the one matrix.  row_index: int32 [rows]; an entry
     outside x selects a row of zeros.  Returns ``output``.

@@ -42,7 +42,7 @@ def permutation(out):
 calls = [bf16, fp4, permutation, bf16]
 outs = [torch.empty((rows, n), device="cuda") for _ in calls]
 streams = [torch.cuda.Stream() for _ in calls]
-meet = threading.Barrier(len(calls))
+meet = threading.Barrier(len(calls), timeout=60)
 got = [None] * len(calls)
 
 
