@@ -22,10 +22,19 @@ bool encode_map(CUtensorMap *m, CUtensorMapDataType type, const void *p, int ran
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(columns), static_cast<cuuint32_t>(rows), 1};
     const cuuint32_t ones[3] = {1, 1, 1};
     const EncodeFn encode = g_encode.load(std::memory_order_acquire);
-    return encode(m, type, rank, const_cast<void *>(p), sizes, strides, box, ones,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const auto encoded = [&] {
+        return encode(m, type, rank, const_cast<void *>(p), sizes, strides, box, ones,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encoded();
+    // The driver wants a context, which a thread has only after some call of the runtime's:
+    // setting the device, the same one, is such a call.
+    int dev = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess &&
+        cudaSetDevice(dev) == cudaSuccess)
+        r = encoded();
+    return r == CUDA_SUCCESS;
 }
 
 cudaError_t find_encoder() {

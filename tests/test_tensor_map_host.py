@@ -1,7 +1,8 @@
 """csrc/tensor_map.cu from several threads (CPU only): each family of products looks the
 driver's encoder up in its first call, under a lock of its own, so that first calls of two
-families may do it at once.  Built as plain C++ against a stand-in for the driver, under
-ThreadSanitizer."""
+families may do it at once; and the encoder wants a context, which a thread that has not
+worked on the device yet has not got.  Built as plain C++ against a stand-in for the driver,
+under ThreadSanitizer."""
 import os
 import subprocess
 
@@ -20,11 +21,17 @@ HARNESS = r"""
 #include "tensor_map.h"
 
 static std::atomic<int> lookups{0}, maps{0};
+static thread_local int device = 0;        // the thread's, as the runtime counts
+static thread_local int context = -1;      // of a device, once it is set
+
+extern "C" cudaError_t cudaGetDevice(int *d) { return *d = device, cudaSuccess; }
+extern "C" cudaError_t cudaSetDevice(int d) { return device = context = d, cudaSuccess; }
 
 static CUresult encode(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                        const cuuint64_t *, const cuuint32_t *box, const cuuint32_t *,
                        CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                        CUtensorMapFloatOOBfill) {
+    if (context != device) return CUDA_ERROR_INVALID_CONTEXT;
     maps.fetch_add(1, std::memory_order_relaxed);
     return box[0] == 64 && box[1] == 32 ? CUDA_SUCCESS : CUDA_ERROR_INVALID_VALUE;
 }
@@ -47,13 +54,17 @@ int main() {
     std::vector<std::thread> threads;
     constexpr int kThreads = 4;
     for (int i = 0; i < kThreads; ++i)
-        threads.emplace_back([&] {
+        threads.emplace_back([&, i] {
+            device = i % 2;  // of a device that another thread works on, or not
             ready.fetch_add(1, std::memory_order_relaxed);
             while (ready.load(std::memory_order_relaxed) < kThreads) std::this_thread::yield();
             CUtensorMap m;
             if (mf::find_encoder() != cudaSuccess ||
                 !mf::encode_map(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, nullptr, 2, {64, 32, 1}, {64, 0},
-                                64, 32))
+                                64, 32) ||
+                device != i % 2 || context != device ||
+                mf::encode_map(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, nullptr, 2, {64, 32, 1}, {64, 0},
+                               65, 32))
                 wrong.fetch_add(1, std::memory_order_relaxed);
         });
     for (auto &t : threads) t.join();
@@ -85,4 +96,4 @@ def test_first_calls_from_several_threads(tmp_path):
     for _ in range(5):
         r = subprocess.run([out], capture_output=True, text=True, timeout=120)
         assert r.returncode == 0, r.stderr[:2000]
-        assert r.stdout == "4\n"
+        assert r.stdout == "8\n"   # four maps, and four that are refused
