@@ -70,8 +70,8 @@ class Model:
         self.full = [Barrier(1 + 2 * gather) for _ in range(stages)]            # CTA 0's
         self.empty = [[Barrier(1) for _ in range(stages)] for _ in pair]
         self.acc_full = [[Barrier(1) for _ in pair] for _ in pair]
-        self.acc_empty = [Barrier(4) for _ in pair]                            # CTA 0's
-        self.shared = Barrier(4)                                               # CTA 0's
+        self.acc_empty = [Barrier(2 if planted == "half of the results" else 4) for _ in pair]
+        self.shared = Barrier(2 if planted == "half of the shared columns" else 4)  # CTA 0's, too
         self.scale_full = [Barrier(2) for _ in pair]                           # CTA 0's
         self.scale_empty = [[Barrier(1) for _ in pair] for _ in pair]
         self.stage_step = [[None] * stages for _ in pair]   # the step whose copies a stage takes
@@ -163,7 +163,7 @@ class Model:
                 if in_segment == 0:
                     if self.planted != "accumulator not waited for":
                         yield self.acc_empty[a], acc // 2 % 2 ^ 1
-                    shared = 256 > self.second and self.segment is None
+                    shared = self.segment is None   # whole accumulators share none
                     if shared and (before if a else n) > self.second and acc > 0:
                         if self.planted != "shared columns not waited for":
                             yield self.shared, a ^ 1
@@ -305,8 +305,65 @@ def test_the_model_finds_stores_that_are_not_ordered(scope):
         schedules(lambda: Model(MIXED, 9, 5, 4, 160, scope=scope))
 
 
+SUMS = [(4, 224), (8, 272)]      # the same of moved sums, whose tiles have 192 rows at most
+
+
+@pytest.mark.parametrize("group,second", SUMS)
+@pytest.mark.parametrize("steps", [1, 9, 10, 11, 20, 23])
+@pytest.mark.parametrize("gather", [0, 6])
+def test_sums_that_leave_the_tensor_cores_on_their_way(group, second, steps, gather):
+    """Several accumulators a tile, and segments of ten steps that end inside groups."""
+    tiles = [192, 32, 160, 192, 64]
+    schedules(lambda: Model(tiles, steps, 6, group, second, gather, segment=10), seeds=4)
+
+
 @pytest.mark.parametrize("planted", ["commits to one CTA", "shared columns not waited for",
-                                     "accumulator not waited for"])
+                                     "accumulator not waited for", "half of the results",
+                                     "half of the shared columns"])
 def test_the_model_finds_broken_rules(planted):
     with pytest.raises(AssertionError):
         schedules(lambda: Model(MIXED * 2, 9, 5, 4, 160, planted=planted), seeds=40)
+
+
+@pytest.mark.parametrize("planted", ["commits to one CTA", "accumulator not waited for",
+                                     "half of the results"])
+def test_the_model_finds_broken_rules_of_moved_sums(planted):
+    with pytest.raises(AssertionError):
+        schedules(lambda: Model([192] * 4, 23, 6, 4, 224, segment=10, planted=planted), seeds=40)
+
+
+def test_the_kernel_has_these_rules():
+    """What the model takes from the source: who arrives on each barrier and how often, the
+    sizes, and the waits before an accumulator is written."""
+    text = " ".join(source().split())
+    for barrier, count in (("empty + 8 * i", "1"), ("acc_full + 8 * i", "1"),
+                           ("acc_empty + 8 * i", "kEpilogueWarps * 2"),
+                           ("scale_full + 8 * i", "4 * 2"), ("scale_empty + 8 * i", "1"),
+                           ("shared_empty", "kEpilogueWarps * 2")):
+        assert f" mbar_init({barrier}, {count});" in text, barrier
+    for rule in (
+            "kRows = SUMS ? 192 : 256;", "kStages = SUMS ? 6 : 5;", "constexpr int kSegment = 10;",
+            "kBytes = FORMAT == kMx ? 8 : 16;", "kSteps = 64 / kBytes;", "kColumns = 12 * kWords;",
+            "kColumn = kTmemColumns - 2 * kColumns;",
+            "kSecond = Scales<FORMAT>::kColumn - Shape<SUMS>::kRows;",
+            # the products' waits
+            "warp_wait(scale_full + 8 * (group_n & 1), group_n >> 1 & 1, a.timeout_ns)",
+            "warp_wait(acc_empty + 8 * (acc_n & 1), (acc_n >> 1 & 1) ^ 1, a.timeout_ns)",
+            "if (Acc::kShared > 0 && (acc_n & 1 ? before : n) > Acc::kSecond && acc_n > 0 && "
+            "!warp_wait(shared_empty, (acc_n & 1) ^ 1, a.timeout_ns)) return false; before = n;",
+            "if (!warp_wait(full + 8 * stage, phase, a.timeout_ns)) return false;",
+            # and their completions, to both CTAs
+            "const bool group_end = left == 1 || in_group == Sc::kSteps;",
+            "const bool end = left == 1 || (SUMS && in_segment == kSegment);",
+            "mma_commit<2>(bar); if (group_end) mma_commit<2>(scale_empty + 8 * (group_n & 1)); "
+            "if (end) mma_commit<2>(acc_full + 8 * (acc_n & 1));",
+            # the results' arrivals, on CTA 0's barriers
+            "done_at = map_to_cta(acc_empty, 0);", "shared_at = map_to_cta(shared_empty, 0);",
+            "r[i] = 32 * (second ? at : kAll - 1 - at);",
+            "if (p == group) { tcgen05_fence_before(); __syncwarp(); "
+            "if (lane == 0) mbar_arrive_cluster(shared_at); } "
+            "if (p + 2 * kGroups >= kAll) give_back();",
+            # the scales' wait, and the copies'
+            "ok = warp_wait(scale_empty + 8 * team, (n & 1) ^ 1, a.timeout_ns);",
+            "ok = warp_wait(empty + 8 * stage, phase, a.timeout_ns);"):
+        assert rule in text, rule
