@@ -6,8 +6,9 @@
 //   backward   d_rows[m(t, j)] = w(t, j) dy[t],   d_w(t, j) = <rows[m(t, j)], dy[t]>
 //
 // All are bound by the rows' bytes: every row is read or written once, and the token's
-// row once for all its slots (GB300: 8000 x 8 rows of 7168 154 us into order, 151 back, 290
-// for both gradients, 6.7 - 6.8 TB/s, the copy's rate).  A slot without a row (m outside the
+// row once for all its slots, by the gradients once for every eight slots (GB300: 8000 x 8
+// rows of 7168 154 us into order, 151 back, 290 for both gradients, 6.7 - 6.8 TB/s, the
+// copy's rate; both gradients of 2000 x 8, 16 and 32 rows of 4096 46, 88 and 174 us).  A slot without a row (m outside the
 // rows) moves nothing, and its weight is not used.
 #include "experts.h"
 #include "rows.cuh"
@@ -251,9 +252,13 @@ cudaError_t launch_backward(const CombineArgs &a, cudaStream_t s) {
                      dim3(kCta), 0, s, 1, a.programmatic, a);
 }
 
-// How many threads take a token: a warp where rows are short (8000 x 8 rows of 512: 25 us,
-// 40 with 128 threads; 20000 x 4 of 1024 58 and, with eight slots, 70 and 90), 512 threads where there is a token to
-// an SM at most (64 x 8 rows of 7168: 5.1 us, 6.1 with 128; 600 x 8 of 4096 19.6 and 15.4).
+// How many threads take a token.  A warp where rows are short and tokens many, up to 192
+// chunks (8000 x 8 rows, a warp against 128 threads: 64 chunks 25.4 and 40.5 us, 128 47.3 and
+// 50.4, 192 68.6 and 72.7, 256 89.7 and 87.2; 8000 x 4 rows 14.0 and 18.2, 25.0 and 24.9, 36.3
+// and 36.1, 47.2 and 45.6).  Of fewer tokens a warp each does not fill the SMs (1000 x 8 rows,
+// 192 chunks: 13.2 and 12.1; 153 x 8: 8.6 and 4.6): the rule has them wrong by that.  512
+// threads where there is a token to an SM at most (152 x 8 rows, 264 chunks 4.5 us and 6.0 with
+// 128 threads, 896 chunks 8.8 and 11.9; 153 x 8 rows 6.8 and 6.0, 11.9 and 12.0).
 template <bool DY_FP32, bool ROWS_FP32, int SLOTS>
 cudaError_t launch_team(const CombineArgs &a, cudaStream_t s) {
     const int chunks = a.hidden / kColumns<DY_FP32, ROWS_FP32>;

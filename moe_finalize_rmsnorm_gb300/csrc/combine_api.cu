@@ -37,11 +37,12 @@ mf_status start(mf::CombineArgs &a, const int32_t *idx, const void *weights, mf_
     const mf::DeviceInfo *d = nullptr;
     const mf_status st = mf::device_info(&d);
     if (st != MF_OK) return st;
-    static_assert(MF_DTYPE_BF16 == 0 && MF_DTYPE_FP32 == 1 && MF_DTYPE_PACKED_TOPK == 2,
+    static_assert(int{MF_DTYPE_BF16} == mf::kRoutingBf16 && int{MF_DTYPE_FP32} == mf::kRoutingFp32 &&
+                      int{MF_DTYPE_PACKED_TOPK} == mf::kRoutingPacked,
                   "the kernels' weight kinds");
     a.idx = idx;
     a.weights = weights;
-    a.weight_kind = weights ? static_cast<int>(weights_dtype) : 3;
+    a.weight_kind = weights ? static_cast<int>(weights_dtype) : mf::kRoutingNone;
     a.num_rows = rows;
     a.num_tokens = num_tokens;
     a.hidden = hidden;

@@ -36,6 +36,9 @@ struct RowSumArgs {
     bool programmatic;
 };
 
+// Routing weights: FP32, BF16, the low half of a packed routing word, or none (1).
+enum RoutingKind { kRoutingBf16 = 0, kRoutingFp32 = 1, kRoutingPacked = 2, kRoutingNone = 3 };
+
 // The way into expert order and back.  `token_rows` has a row for each token, `rows` and
 // `out_rows` (of dispatch and of the gradient) a row for each slot; combine's `out_rows`
 // are the tokens'.
@@ -49,7 +52,7 @@ struct CombineArgs {
     int rows_fp32;           // type of the slots' rows, in or out
     void *out_rows;          // nullptr: no gradient of the rows
     int64_t out_ld;
-    const void *weights;     // [T, K], by `weight_kind` (rows.cuh)
+    const void *weights;     // [T, K], by `weight_kind`
     int weight_kind;
     const int32_t *idx;      // [T, K]
     void *grad_weights;      // [T, K], or nullptr

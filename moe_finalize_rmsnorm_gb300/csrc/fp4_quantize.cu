@@ -12,10 +12,11 @@
 // or 16 that are one block (58 us with 8), so that a warp's loads and stores are one run
 // each, and the 2 or 4 threads of a longer block exchange their largest magnitudes.  The
 // quotients decide between neighbours as the exact ones do: with an E8M0 scale they are
-// exact, and with E4M3 they are rounded as a division's (a reciprocal's product, put right
-// by its remainder): a quotient next to a border between two codes differs from it by
-// more than half a step of FP32, as border times scale has at most 7 bits, and a product
-// with the reciprocal alone would miss some of the ties themselves.
+// exact, and with E4M3 they are rounded as a division's (a reciprocal by one step of
+// Newton's iteration, and its product put right by its remainder: Markstein's correction of
+// a quotient).  A quotient next to a border between two codes differs from it by more than
+// half a step of FP32, as border times scale has at most 7 bits, and a product with the
+// reciprocal alone would miss some of the ties themselves.
 #include "fp4.cuh"
 #include "rows.cuh"
 
@@ -60,8 +61,8 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return r;
 }
 
-// 1 / s, rounded, of the values of E4M3: the hardware's estimate and one step that takes its
-// error out.
+// 1 / s, rounded, of the values of E4M3: the hardware's estimate and one step of Newton's
+// iteration.
 __device__ __forceinline__ float reciprocal(float s) {
     float r;
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) quantize_fp4_kernel(Fp4RowsArgs a) {
             const float r = __uint_as_float((254u - byte) << 23);
             r2 = make_float2(r, r);
         } else {
-            // top / 6, rounded as a division's
+            // top / 6, rounded as a division's: Markstein's correction
             const float m = __uint_as_float(top);
             constexpr float kSixth = 1.f / 6.f;
             const float c = m * kSixth;

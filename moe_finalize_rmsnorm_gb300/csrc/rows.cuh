@@ -1,8 +1,10 @@
-// Rows moved in chunks of eight values (16 bytes of BF16, 32 of FP32): what the
-// permutation's row sum and the kernels of the way into expert order and back share.
+// Rows in chunks of eight values (16 bytes of BF16, 32 of FP32): chunks and their store for
+// the permutation's row sum, the store for 4-bit values on their way back; and the load
+// that reads or not, and routing weights, for the way into expert order and back, too.
 #pragma once
 
 #include "common.cuh"
+#include "experts.h"
 
 namespace mf {
 
@@ -54,16 +56,14 @@ __device__ __forceinline__ void store8(void *rows, int64_t at, const float (&f)[
     }
 }
 
-// Routing weight of a slot: FP32, BF16, or the low half of a packed routing word.
-enum WeightKind { kWeightBf16 = 0, kWeightFp32 = 1, kWeightPacked = 2, kWeightNone = 3 };
-
+// Routing weight of a slot.
 __device__ __forceinline__ float routing_weight(const void *weights, int kind, int64_t slot) {
     switch (kind) {
-        case kWeightFp32: return __ldg(static_cast<const float *>(weights) + slot);
-        case kWeightBf16:
+        case kRoutingFp32: return __ldg(static_cast<const float *>(weights) + slot);
+        case kRoutingBf16:
             return __uint_as_float(
                 uint32_t{__ldg(static_cast<const unsigned short *>(weights) + slot)} << 16);
-        case kWeightPacked:
+        case kRoutingPacked:
             return bf16_lo(__ldg(static_cast<const uint32_t *>(weights) + slot));
         default: return 1.f;
     }
