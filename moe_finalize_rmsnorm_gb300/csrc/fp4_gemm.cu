@@ -22,11 +22,11 @@
 // first, and says so, before the rest.
 //
 // What bounds it (GB300, 4096 x 4096, short runs): up to some 200 rows an expert the
-// weights' bytes (32 experts of 64 rows 53 us, E8M0; 45 at the copy bandwidth).  Beyond, a
-// step of 256 rows takes some 925 cycles (E8M0), 965 (E4M3) or 1060 (E4M3, gathered), and
-// the products keep the tensor cores active for some 640 of them in each.  Shared
-// memory, at 128 bytes a cycle, brings 32 KB in and reads it once more (512 cycles), and
-// writes and reads the scales' blocks (192 cycles, E4M3, or 96), beside the products; which
+// weights' bytes (32 experts of 64 rows 51 us, E8M0; 45 at the copy bandwidth).  Beyond, a
+// step of 256 rows takes 820 - 830 cycles (E4M3 gathered 940; a launch of 16 experts of 512
+// rows, its start and end included), of which the products keep the tensor cores active for
+// 512.  Shared memory, at 128 bytes a cycle, is as busy: it brings 32 KB in and reads it once
+// more (512 cycles), and writes and reads the scales' blocks (192 cycles, E4M3, or 96).  Which
 // waits make up the rest is not measured.  512 rows an expert run at 5.6 (E8M0) and 5.4
 // (E4M3) PFLOP/s, gathered 5.2 and 4.8.  Tiles of 192 rows, for which the scales leave whole
 // accumulators, ran at 5.2 and 4.3 when 256 did at 5.7 and 4.8.
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(Warps<SUMS, GATHER>::kThreads, 1)
                                                a.timeout_ns);
                 }
         } else if (warp == 1 && rank == 0) {
-            // Products.  A step takes the tensor cores some 640 cycles, and this warp has to
+            // Products.  A step takes the tensor cores 512 cycles, and this warp has to
             // issue its 10 to 16 instructions in less, so the loop is kept short: places are kept
             // by counting, and the last step multiplies its zeros too.
             const uint64_t operands = smem_desc(base, 16, 1024), blocks = block_desc(groups);
